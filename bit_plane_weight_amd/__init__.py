@@ -26,6 +26,9 @@ __all__ = [
     "TritFile", "TritFormatError", "TritTensor", "bpw_fnv1a64", "trit_write", "TRIT_F32", "TRIT_TERNARY", "TRIT_BF16",
     "BitcosHost", "bpw_bitcos_pack_i8", "bpw_bitcos_from_planes", "DevBitcos", "bpw_bitcos_upload", "bitcos_job",
     "bpw_bitcos_workspace_bytes", "BitcosPlan",
+    "PagedKv", "QkNormRopePlan", "bpw_qk_norm_rope", "KvAppendPlan", "bpw_kv_append",
+    "bpw_attn_shared_prefix_workspace_bytes", "SharedPrefixAttnPlan", "bpw_attn_shared_prefix",
+    "bpw_verify_draft_workspace_bytes", "DraftVerifyPlan", "bpw_verify_draft",
 ]
 
 
@@ -590,6 +593,272 @@ def bpw_dense_head_gemv(w_bf16, x_bf16, y, stream=None) -> None:
         raise ValueError(f"x_bf16 holds {x_bf16.numel()} elements, needs at least {cols}")
     _lib.check(_lib.lib().bpw_dense_head_gemv(_dptr(w_bf16), rows, cols, _dptr(x_bf16),
                                               _checked(y, "float32", rows, "y"), _stream(stream)))
+
+
+# ------------------------------------------------------------------------------ decode step: heads, cache, attention, drafts
+
+
+def _dtype_code(t, what: str, cache: bool = False) -> int:
+    import torch
+    code = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}.get(t.dtype)
+    if code is None or (cache and code == _lib.F32):
+        raise TypeError(f"{what} must be {'' if cache else 'float32, '}bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _gpu(t, what: str) -> int:
+    """Device address of a strided GPU tensor."""
+    if not getattr(t, "is_cuda", False):
+        raise TypeError(f"{what}: expected a GPU tensor")
+    return t.data_ptr()
+
+
+def _heads(t, tokens: int, head_dim: int, what: str) -> "_lib.BpwHeads":
+    """A [tokens, heads, head_dim] GPU tensor, any strides with contiguous elements (None: no heads)."""
+    h = _lib.BpwHeads()
+    if t is None:
+        return h
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != head_dim:
+        raise ValueError(f"{what} must be [{tokens}, heads, {head_dim}], got {list(t.shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{what}: a head's elements must be contiguous")
+    h.dtype = _dtype_code(t, what)
+    h.d, h.heads = _gpu(t, what), t.shape[1]
+    # the stride of a dimension of one is free: 0, as nothing is reached by it
+    h.token_stride = t.stride(0) if t.shape[0] > 1 else 0
+    h.head_stride = t.stride(1) if t.shape[1] > 1 else 0
+    return h
+
+
+def _written(h, t, what: str) -> None:
+    """Refuses an output whose rows repeat (an expanded view)."""
+    if t is not None and (t.shape[0] > 1 and t.stride(0) == 0 or t.shape[1] > 1 and t.stride(1) == 0):
+        raise ValueError(f"{what} is an expanded view: its rows share memory")
+
+
+def _rotation(positions, inv_freq, tokens: int, interleaved: bool) -> "_lib.BpwRotation":
+    r = _lib.BpwRotation()
+    if inv_freq is None:
+        return r
+    r.rot_dim = 2 * inv_freq.numel()
+    r.d_inv_freq = _checked(inv_freq, "float64", 1, "inv_freq") if r.rot_dim else None
+    if r.rot_dim and positions is None:
+        raise ValueError("positions are required with inv_freq")
+    r.d_positions = _checked(positions, "int32", tokens, "positions")
+    r.interleaved = int(bool(interleaved))
+    return r
+
+
+class PagedKv:
+    """A paged key/value cache (bpw_paged_kv): k_pages and v_pages are GPU tensors [pages, kv_heads, page_size,
+    head_dim] of bfloat16 or float16, any strides with contiguous elements (``x.transpose(1, 2)`` of a
+    [pages, page_size, kv_heads, head_dim] cache too)."""
+
+    def __init__(self, k_pages, v_pages):
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
+            raise ValueError("k_pages and v_pages must both be [pages, kv_heads, page_size, head_dim]")
+        if k_pages.dtype != v_pages.dtype:
+            raise TypeError("k_pages and v_pages have different types")
+        for t, what in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+            if t.shape[3] > 1 and t.stride(3) != 1:
+                raise ValueError(f"{what}: a head's elements must be contiguous")
+            if any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride())):
+                raise ValueError(f"{what} is an expanded view: its rows share memory")
+        c = _lib.BpwPagedKv()
+        c.dtype = _dtype_code(k_pages, "a cache", cache=True)
+        c.n_pages, c.kv_heads, c.page_size, c.head_dim = k_pages.shape
+        c.d_k, c.d_v = _gpu(k_pages, "k_pages"), _gpu(v_pages, "v_pages")
+        # the stride of a dimension of one is free: 0, as nothing is reached by it
+        st = [[x if n > 1 else 0 for n, x in zip(t.shape, t.stride())] for t in (k_pages, v_pages)]
+        c.k_page_stride, c.k_head_stride, c.k_row_stride = st[0][:3]
+        c.v_page_stride, c.v_head_stride, c.v_row_stride = st[1][:3]
+        self.c, self.k_pages, self.v_pages = c, k_pages, v_pages
+
+    @property
+    def page_size(self) -> int:
+        return self.c.page_size
+
+
+class _Bound:
+    """Arguments checked and bound once; run() queues the launches on a stream. The tensors named stay
+    alive with the plan and are read and written as they are when the work runs, so a plan may be run
+    again after their contents change, and its runs captured into a graph."""
+
+    def _bind(self, fn: str, args, keep, d_ws=None):
+        self._fn, self._args, self._ref, self._keep = getattr(_lib.lib(), fn), args, ctypes.byref(args), (keep, d_ws)
+        self._ws = None if d_ws is None else (_dptr(d_ws), d_ws.numel() * d_ws.element_size())
+
+    def run(self, stream=None) -> None:
+        if self._ws is None:
+            status = self._fn(self._ref, _stream(stream))
+        else:
+            status = self._fn(self._ref, self._ws[0], self._ws[1], _stream(stream))
+        if status:
+            _lib.check(status)
+
+
+class QkNormRopePlan(_Bound):
+    """bpw_qk_norm_rope: q [tokens, q_heads, head_dim] and k [tokens, kv_heads, head_dim] normed (where a gain, float32
+    [head_dim], is given) and rotated into q_out and k_out. positions int32 [tokens], inv_freq float64
+    [rot_dim / 2] (None: no rotation). q and q_out, or k and k_out, may be None; an output may be its input."""
+
+    def __init__(self, q, k, q_out, k_out, positions, inv_freq, q_gain=None, k_gain=None, eps: float = 1e-6,
+                 interleaved: bool = False):
+        first = q if q is not None else k
+        if first is None or first.dim() != 3:
+            raise ValueError("q or k must be [tokens, heads, head_dim]")
+        T, D = first.shape[0], first.shape[2]
+        a = _lib.BpwQkNormRopeArgs()
+        a.n_tokens, a.head_dim = T, D
+        a.q, a.k = _heads(q, T, D, "q"), _heads(k, T, D, "k")
+        a.q_out, a.k_out = _heads(q_out, T, D, "q_out"), _heads(k_out, T, D, "k_out")
+        _written(a.q_out, q_out, "q_out")
+        _written(a.k_out, k_out, "k_out")
+        a.d_q_gain, a.d_k_gain = _checked(q_gain, "float32", D, "q_gain"), _checked(k_gain, "float32", D, "k_gain")
+        a.eps = float(eps)
+        a.rot = _rotation(positions, inv_freq, T, interleaved)
+        self._bind("bpw_qk_norm_rope", a, (q, k, q_out, k_out, positions, inv_freq, q_gain, k_gain))
+
+
+def bpw_qk_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_gain=None, k_gain=None, eps: float = 1e-6,
+                     interleaved: bool = False, stream=None) -> None:
+    """One run of a QkNormRopePlan."""
+    QkNormRopePlan(q, k, q_out, k_out, positions, inv_freq, q_gain, k_gain, eps, interleaved).run(stream)
+
+
+class KvAppendPlan(_Bound):
+    """bpw_kv_append: k and v [tokens, kv_heads, head_dim] written to the cache at slots (int64 [tokens]: page * page_size
+    + offset; outside the cache: not written), k normed and rotated on the way; q, if given, normed and rotated
+    into q_out in the same launch."""
+
+    def __init__(self, kv: PagedKv, k, v, slots, positions=None, inv_freq=None, k_gain=None, q=None, q_out=None,
+                 q_gain=None, eps: float = 1e-6, interleaved: bool = False):
+        if k.dim() != 3:
+            raise ValueError("k must be [tokens, kv_heads, head_dim]")
+        T, D = k.shape[0], kv.c.head_dim
+        a = _lib.BpwKvAppendArgs()
+        a.n_tokens, a.kv = T, kv.c
+        a.k, a.v, a.q, a.q_out = (_heads(k, T, D, "k"), _heads(v, T, D, "v"), _heads(q, T, D, "q"),
+                                  _heads(q_out, T, D, "q_out"))
+        _written(a.q_out, q_out, "q_out")
+        if slots is None:
+            raise ValueError("slots are required")
+        a.d_slots = _checked(slots, "int64", T, "slots")
+        a.d_q_gain, a.d_k_gain = _checked(q_gain, "float32", D, "q_gain"), _checked(k_gain, "float32", D, "k_gain")
+        a.eps = float(eps)
+        a.rot = _rotation(positions, inv_freq, T, interleaved)
+        self._bind("bpw_kv_append", a, (kv, k, v, slots, positions, inv_freq, k_gain, q, q_out, q_gain))
+
+
+def bpw_kv_append(kv: PagedKv, k, v, slots, positions=None, inv_freq=None, k_gain=None, q=None, q_out=None, q_gain=None,
+                  eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
+    """One run of a KvAppendPlan."""
+    KvAppendPlan(kv, k, v, slots, positions, inv_freq, k_gain, q, q_out, q_gain, eps, interleaved).run(stream)
+
+
+def _attn_args(kv: PagedKv, q, prefix_len: int, n_seqs: int, max_q: int, max_pages: int):
+    a = _lib.BpwAttnArgs()
+    a.kv = kv.c
+    a.n_tokens, a.n_seqs, a.max_q = q.shape[0], int(n_seqs), int(max_q)
+    a.q = _heads(q, q.shape[0], kv.c.head_dim, "q")
+    a.prefix_len, a.max_pages = int(prefix_len), int(max_pages)
+    return a
+
+
+def bpw_attn_shared_prefix_workspace_bytes(kv: PagedKv, q, prefix_len: int, n_seqs: int, max_q: int,
+                                           max_pages: int | None = None) -> int:
+    """Workspace bytes of a SharedPrefixAttnPlan over this cache and q [tokens, q_heads, head_dim]. max_pages: columns of
+    the page table (None: the cache's pages, which covers every table)."""
+    a = _attn_args(kv, q, prefix_len, n_seqs, max_q, kv.c.n_pages if max_pages is None else max_pages)
+    return _lib.lib().bpw_attn_shared_prefix_workspace_bytes(ctypes.byref(a))
+
+
+class SharedPrefixAttnPlan(_Bound):
+    """bpw_attn_shared_prefix: decode attention of sequences that share a prefix. q and out [tokens, q_heads,
+    head_dim] of the cache's type; prefix_pages int32 holds the prefix_len shared positions (None if 0); table
+    int32 [sequences, max_pages], lens int32 [sequences] each sequence's own positions; q_starts int32 [sequences + 1]
+    the first token of each; max_q the most tokens of one; d_ws a uint8 workspace; lse float32 [tokens, q_heads]
+    or None; scale None: 1 / sqrt(head_dim)."""
+
+    def __init__(self, kv: PagedKv, q, out, prefix_pages, prefix_len: int, table, lens, q_starts, max_q: int, d_ws,
+                 scale: float | None = None, lse=None):
+        if table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("table must be [sequences, max_pages] with contiguous rows")
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens, q_heads, head_dim]")
+        n_seqs = table.shape[0]
+        a = _attn_args(kv, q, prefix_len, n_seqs, max_q, table.shape[1])
+        a.out = _heads(out, q.shape[0], kv.c.head_dim, "out")
+        _written(a.out, out, "out")
+        import torch
+        if table.dtype != torch.int32:
+            raise TypeError(f"table must be torch.int32, got {table.dtype}")
+        a.d_lens = _checked(lens, "int32", n_seqs, "lens")
+        a.d_q_starts = _checked(q_starts, "int32", n_seqs + 1, "q_starts")
+        need = -(-a.prefix_len // kv.c.page_size) if a.prefix_len > 0 else 0
+        a.d_prefix_pages = _checked(prefix_pages, "int32", need, "prefix_pages") if need else None
+        if need and prefix_pages is None:
+            raise ValueError("prefix_pages are required with a prefix")
+        a.d_table = _gpu(table, "table")
+        a.table_stride = max(table.stride(0), table.shape[1]) if n_seqs == 1 else table.stride(0)
+        a.scale = kv.c.head_dim ** -0.5 if scale is None else float(scale)
+        a.d_lse = _checked(lse, "float32", q.shape[0] * q.shape[1], "lse")
+        if d_ws is None:
+            raise ValueError("a workspace is required")
+        self._bind("bpw_attn_shared_prefix", a, (kv, q, out, prefix_pages, table, lens, q_starts, lse), d_ws)
+
+
+def bpw_attn_shared_prefix(kv: PagedKv, q, out, prefix_pages, prefix_len: int, table, lens, q_starts, max_q: int, d_ws,
+                           scale: float | None = None, lse=None, stream=None) -> None:
+    """One run of a SharedPrefixAttnPlan."""
+    SharedPrefixAttnPlan(kv, q, out, prefix_pages, prefix_len, table, lens, q_starts, max_q, d_ws, scale, lse).run(stream)
+
+
+def bpw_verify_draft_workspace_bytes(n_seqs: int, vocab: int) -> int:
+    return _lib.lib().bpw_verify_draft_workspace_bytes(int(n_seqs), int(vocab))
+
+
+class DraftVerifyPlan(_Bound):
+    """bpw_verify_draft: target [sequences, drafts + 1, vocab] and draft [sequences, drafts, vocab] probabilities
+    (draft None: the drafted tokens were certain), tokens int32 [sequences, drafts], accept_u float32
+    [sequences, drafts], sample_u float32 [sequences], n_draft int32 [sequences] or None (all). out_tokens int32 [sequences,
+    drafts + 1] gets the accepted tokens, the drawn one, then -1; accepted int32 [sequences] their count."""
+
+    def __init__(self, target, draft, tokens, accept_u, sample_u, out_tokens, accepted, d_ws, n_draft=None):
+        if target.dim() != 3:
+            raise ValueError("target must be [sequences, drafts + 1, vocab]")
+        B, K, V = target.shape[0], target.shape[1] - 1, target.shape[2]
+        if draft is not None and tuple(draft.shape) != (B, K, V):
+            raise ValueError(f"draft must be [{B}, {K}, {V}], got {list(draft.shape)}")
+        if draft is not None and draft.dtype != target.dtype:
+            raise TypeError("target and draft have different types")
+        for t, what in ((target, "target"), (draft, "draft")):
+            if t is not None and V > 1 and t.stride(2) != 1:
+                raise ValueError(f"{what}: a row must be contiguous")
+        a = _lib.BpwVerifyArgs()
+        a.n_seqs, a.max_drafts, a.vocab, a.dtype = B, K, V, _dtype_code(target, "target")
+        a.d_target, a.target_seq_stride, a.target_step_stride = _gpu(target, "target"), target.stride(0), target.stride(1)
+        if draft is not None:
+            a.d_draft, a.draft_seq_stride, a.draft_step_stride = _gpu(draft, "draft"), draft.stride(0), draft.stride(1)
+        for t, what in ((tokens, "tokens"), (accept_u, "accept_u"), (sample_u, "sample_u"), (out_tokens, "out_tokens"),
+                        (accepted, "accepted")):
+            if t is None:
+                raise ValueError(f"{what} is required")
+        a.d_tokens = _checked(tokens, "int32", B * K, "tokens")
+        a.d_n_draft = _checked(n_draft, "int32", B, "n_draft")
+        a.d_accept_u = _checked(accept_u, "float32", B * K, "accept_u")
+        a.d_sample_u = _checked(sample_u, "float32", B, "sample_u")
+        a.d_out_tokens = _checked(out_tokens, "int32", B * (K + 1), "out_tokens")
+        a.d_accepted = _checked(accepted, "int32", B, "accepted")
+        if d_ws is None:
+            raise ValueError("a workspace is required")
+        self._bind("bpw_verify_draft", a, (target, draft, tokens, accept_u, sample_u, out_tokens, accepted, n_draft), d_ws)
+
+
+def bpw_verify_draft(target, draft, tokens, accept_u, sample_u, out_tokens, accepted, d_ws, n_draft=None,
+                     stream=None) -> None:
+    """One run of a DraftVerifyPlan."""
+    DraftVerifyPlan(target, draft, tokens, accept_u, sample_u, out_tokens, accepted, d_ws, n_draft).run(stream)
 
 
 # ------------------------------------------------------------------------------ measurement

@@ -81,6 +81,59 @@ class BpwQuantJob(ctypes.Structure):
                 ("eps", ctypes.c_float), ("reserved", ctypes.c_uint32)]
 
 
+# bpw_dtype
+F32, BF16, F16 = 0, 1, 2
+
+
+class BpwHeads(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_void_p), ("heads", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class BpwPagedKv(ctypes.Structure):
+    _fields_ = [("d_k", ctypes.c_void_p), ("d_v", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("reserved", ctypes.c_uint32),
+                ("k_page_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64), ("k_row_stride", ctypes.c_int64),
+                ("v_page_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64), ("v_row_stride", ctypes.c_int64)]
+
+
+class BpwRotation(ctypes.Structure):
+    _fields_ = [("d_positions", ctypes.c_void_p), ("d_inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class BpwQkNormRopeArgs(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("q", BpwHeads), ("k", BpwHeads), ("q_out", BpwHeads), ("k_out", BpwHeads),
+                ("d_q_gain", ctypes.c_void_p), ("d_k_gain", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_uint32), ("rot", BpwRotation)]
+
+
+class BpwKvAppendArgs(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int32), ("reserved", ctypes.c_uint32),
+                ("k", BpwHeads), ("v", BpwHeads), ("q", BpwHeads), ("q_out", BpwHeads), ("d_slots", ctypes.c_void_p),
+                ("d_q_gain", ctypes.c_void_p), ("d_k_gain", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("reserved2", ctypes.c_uint32), ("rot", BpwRotation), ("kv", BpwPagedKv)]
+
+
+class BpwAttnArgs(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int32), ("n_seqs", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q", BpwHeads), ("out", BpwHeads), ("d_lse", ctypes.c_void_p),
+                ("d_prefix_pages", ctypes.c_void_p), ("prefix_len", ctypes.c_int64), ("d_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int32), ("reserved", ctypes.c_uint32),
+                ("d_lens", ctypes.c_void_p), ("d_q_starts", ctypes.c_void_p), ("kv", BpwPagedKv)]
+
+
+class BpwVerifyArgs(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("max_drafts", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("d_target", ctypes.c_void_p), ("target_seq_stride", ctypes.c_int64),
+                ("target_step_stride", ctypes.c_int64), ("d_draft", ctypes.c_void_p),
+                ("draft_seq_stride", ctypes.c_int64), ("draft_step_stride", ctypes.c_int64),
+                ("d_tokens", ctypes.c_void_p), ("d_n_draft", ctypes.c_void_p), ("d_accept_u", ctypes.c_void_p),
+                ("d_sample_u", ctypes.c_void_p), ("d_out_tokens", ctypes.c_void_p), ("d_accepted", ctypes.c_void_p)]
+
+
 class BpwError(RuntimeError):
     """A non-OK bpw_status, with the library's reason and (for validation) the offending position."""
 
@@ -171,6 +224,12 @@ def lib():
         "bpw_bitcos_plan_create": (i32, [ctypes.POINTER(BpwBitcosJob), i32, vp, sz, vp, ctypes.POINTER(vp)]),
         "bpw_bitcos_plan_run": (i32, [vp, vp]),
         "bpw_bitcos_plan_free": (None, [vp]),
+        "bpw_qk_norm_rope": (i32, [ctypes.POINTER(BpwQkNormRopeArgs), vp]),
+        "bpw_kv_append": (i32, [ctypes.POINTER(BpwKvAppendArgs), vp]),
+        "bpw_attn_shared_prefix_workspace_bytes": (sz, [ctypes.POINTER(BpwAttnArgs)]),
+        "bpw_attn_shared_prefix": (i32, [ctypes.POINTER(BpwAttnArgs), vp, sz, vp]),
+        "bpw_verify_draft_workspace_bytes": (sz, [i32, i32]),
+        "bpw_verify_draft": (i32, [ctypes.POINTER(BpwVerifyArgs), vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)

@@ -12,7 +12,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 SOURCES = [os.path.join(_HERE, "csrc", f) for f in (
     "bpw_host.cpp", "bpw_gemv.hip", "bpw_gemv_tokens.hip", "bpw_bytelane.hip", "bpw_small_batch.hip", "bpw_dense_head.hip",
     "bpw_quantize.hip", "bpw_measure.hip", "bpw_trit.cpp", "bpw_bitcos.hip", "bpw_bitcos_host.cpp",
-    "bpw_static.hip")]
+    "bpw_static.hip", "bpw_heads.hip", "bpw_attention_d64.hip", "bpw_attention_d128.hip", "bpw_attention_d256.hip",
+    "bpw_verify.hip", "bpw_decode_host.cpp")]
 OUT = os.path.join(_HERE, "libbpw.so")
 
 HIPCC_FLAGS = [

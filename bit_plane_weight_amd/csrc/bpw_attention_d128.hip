@@ -1,0 +1,12 @@
+// bpw_attention_d128.hip - the attention kernels of bpw_attention.h for head sizes padded to 128.
+#include "bpw_attention.h"
+
+namespace bpw {
+
+int launch_attn_d128(const AttnArgs &a, int32_t dtype, int32_t nqp, int32_t nqs, void *stream) {
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (dtype == 1) return run_attn_tiles<__bf16, 128>(a, nqp, nqs, s);
+    return run_attn_tiles<_Float16, 128>(a, nqp, nqs, s);
+}
+
+}  // namespace bpw

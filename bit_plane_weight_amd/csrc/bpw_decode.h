@@ -1,0 +1,97 @@
+// bpw_decode.h - records and launchers shared by the host checks (bpw_decode_host.cpp) and the kernels
+// of the decode-step operators (bpw_heads.hip, bpw_attention*.hip, bpw_verify.hip). Not part of the ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace bpw {
+
+// ---------------------------------------------------------------- heads (norm, rotation, append)
+
+// One set of heads: inputs and outputs by element strides. With slots, out_ts is the stride of a cache
+// row and out_ps of a page.
+struct HeadSet {
+    const void *in;
+    void *out;
+    int64_t in_ts, in_hs;
+    int64_t out_ts, out_hs, out_ps;
+    const float *gain;  // null: no norm
+    int32_t heads;
+    int32_t to_cache;   // 1: the output row is slots[t]
+};
+
+struct HeadsArgs {
+    HeadSet q, k, v;    // v: copied only (append)
+    const int32_t *positions;
+    const double *inv_freq;
+    const int64_t *slots;
+    int64_t n_slots;
+    int32_t n_tokens, head_dim, rot_dim, interleaved;
+    int32_t page_log2;
+    int32_t lanes_log2;      // lanes of one head
+    int32_t tokens_per_wg;
+    float eps;
+};
+
+constexpr int kHeadThreads = 256;
+// vec: every row is read and written 16 bytes at a time (alignment and divisibility checked by the host)
+int launch_heads(const HeadsArgs &a, int32_t dt_in, int32_t dt_out, bool vec, void *stream);
+
+// ---------------------------------------------------------------- attention
+
+constexpr int kAttnWaves = 4;
+constexpr int kAttnThreads = 64 * kAttnWaves;
+constexpr int kAttnStep = 32;                      // positions one wave takes at a time
+constexpr int kAttnUnit = kAttnStep * kAttnWaves;  // positions of one unit of work
+constexpr int kAttnMaxSeqs = 1024;
+constexpr int kAttnMaxWgs = 1024;
+
+struct AttnArgs {
+    const void *q;
+    void *out;
+    float *lse;
+    int64_t q_ts, q_hs, o_ts, o_hs;
+    const void *k, *v;
+    int64_t k_ps, k_hs, v_ps, v_hs;
+    int32_t k_rs, v_rs;      // row strides (elements)
+    const int32_t *prefix_pages;
+    const int32_t *table;
+    int64_t table_stride;
+    const int32_t *lens, *q_starts;
+    int32_t n_tokens, n_seqs, max_q, q_heads, kv_heads, group, head_dim;
+    int32_t page_log2, n_pages, prefix_len, cap;  // cap: positions a table row can hold
+    float scale_log2;
+    int32_t n_wgs;
+    int32_t tiles_p;         // query tiles of the prefix per kv head
+    // workspace
+    int32_t *sched;          // kSchedHead words, then units before each sequence, then items before each
+    float *part_o;           // [pieces][rows of a tile][padded dim]
+    float2 *part_ml;         // [pieces][rows of a tile]: running maximum (log2 units) and sum
+    int64_t part_s;          // offset (floats) of the suffix pieces in part_o
+    int64_t ml_s;            // and in part_ml
+};
+constexpr int kSchedHead = 8;  // units per prefix item, prefix units per workgroup, suffix units per workgroup
+
+int launch_attn_d64(const AttnArgs &a, int32_t dtype, int32_t nqp, int32_t nqs, void *stream);
+int launch_attn_d128(const AttnArgs &a, int32_t dtype, int32_t nqp, int32_t nqs, void *stream);
+int launch_attn_d256(const AttnArgs &a, int32_t dtype, int32_t nqp, int32_t nqs, void *stream);
+
+// ---------------------------------------------------------------- draft verification
+
+constexpr int kVerifyThreads = 256;
+constexpr int kVerifyChunk = 4096;  // vocabulary entries summed by one workgroup
+
+struct VerifyArgs {
+    const void *target, *draft;
+    int64_t t_seq, t_step, d_seq, d_step;
+    const int32_t *tokens, *n_draft;
+    const float *accept_u, *sample_u;
+    int32_t *out_tokens, *accepted;
+    double *sums;           // [n_seqs][chunks]
+    int32_t n_seqs, max_drafts, vocab, chunks;
+};
+int launch_verify(const VerifyArgs &a, int32_t dtype, void *stream);
+
+}  // namespace bpw

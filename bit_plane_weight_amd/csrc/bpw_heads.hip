@@ -1,0 +1,232 @@
+// bpw_heads.hip - RMS norm and position rotation of query and key heads, and the append of keys and
+// values to a paged cache, in one pass over the heads (gfx950, wave64). Launched only by
+// bpw_decode_host.cpp after its checks.
+//
+// Mathematics. n = x * rsqrt(mean(x^2) + eps) * gain in float32; a pair (a, b) of frequency i becomes
+// (a cos - b sin, b cos + a sin). The angle is formed as turns = position * inv_freq / 2 pi in float64
+// and reduced to [-1/2, 1/2] there, because in float32 the angle of position 131072 at frequency 1
+// is already wrong in its third decimal; sine and cosine of the reduced turn are float32.
+//
+// Bound: HBM for prompts (each element read once and written once), the launch for a decode step. A
+// workgroup takes whole tokens, so that the rot_dim / 2 sines and cosines are formed once per token
+// (by as many threads) and shared by its heads through LDS. In the vector path 2^lanes_log2 lanes hold one
+// head, each both partners of its pairs (8 elements of the first half and the 8 opposite ones, or 16
+// neighbours), so the rotation needs no exchange and the norm one sum over the lanes.
+#include "bpw_decode.h"
+#include "bpw_elem.h"
+
+namespace bpw {
+
+// Sum over the 2^n consecutive lanes of a head: every lane gets it. Within 16 lanes by DPP (swap pairs,
+// swap halves of a quad, mirror within 8, mirror within 16).
+__device__ __forceinline__ float lanes_sum(float s, int n) {
+#define BPW_DPP_ADD(ctrl) \
+    s += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, s), ctrl, 0xF, 0xF, false))
+    if (n >= 1) BPW_DPP_ADD(0xB1);
+    if (n >= 2) BPW_DPP_ADD(0x4E);
+    if (n >= 3) BPW_DPP_ADD(0x141);
+    if (n >= 4) BPW_DPP_ADD(0x140);
+#undef BPW_DPP_ADD
+    if (n >= 5) s += __shfl_xor(s, 16);
+    if (n >= 6) s += __shfl_xor(s, 32);
+    return s;
+}
+
+// Cosine and sine of position * inv_freq.
+__device__ __forceinline__ float2 turn(int32_t position, double inv_freq) {
+    double t = (double)position * inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
+    t -= __builtin_rint(t);
+    const float x = (float)(t + t);
+    return make_float2(cospif(x), sinpif(x));
+}
+
+// cs[t][i] for the workgroup's tokens.
+__device__ __forceinline__ void fill_turns(const HeadsArgs &a, int t0, int nt, float2 *cs) {
+    const int nf = a.rot_dim >> 1;
+    for (int i = threadIdx.x; i < nt * nf; i += kHeadThreads) {
+        const int t = i / nf;
+        cs[i] = turn(a.positions[t0 + t], a.inv_freq[i - t * nf]);
+    }
+}
+
+// One head of one token: where it is read and written. set 0: q, 1: k, 2: v.
+template <class TI, class TO>
+struct HeadRow {
+    const TI *in;
+    TO *out;
+    const float *gain;
+    int set;
+    bool store;
+};
+
+template <class TI, class TO>
+__device__ __forceinline__ HeadRow<TI, TO> head_row(const HeadsArgs &a, int64_t t, int h) {
+    HeadRow<TI, TO> r;
+    r.set = h < a.q.heads ? 0 : h < a.q.heads + a.k.heads ? 1 : 2;
+    const HeadSet &s = r.set == 0 ? a.q : r.set == 1 ? a.k : a.v;
+    h -= r.set == 0 ? 0 : r.set == 1 ? a.q.heads : a.q.heads + a.k.heads;
+    r.in = static_cast<const TI *>(s.in) + t * s.in_ts + h * s.in_hs;
+    r.gain = s.gain;
+    r.store = true;
+    int64_t off;
+    if (s.to_cache) {
+        const int64_t slot = a.slots[t];
+        r.store = slot >= 0 && slot < a.n_slots;
+        const int64_t page = slot >> a.page_log2;
+        off = page * s.out_ps + (slot - (page << a.page_log2)) * s.out_ts;
+    } else {
+        off = t * s.out_ts;
+    }
+    r.out = static_cast<TO *>(s.out) + off + h * s.out_hs;
+    return r;
+}
+
+template <class TI, class TO>
+__global__ __launch_bounds__(kHeadThreads) void heads_vec_kernel(HeadsArgs a) {
+    extern __shared__ float2 cs[];
+    const int heads = a.q.heads + a.k.heads + a.v.heads;
+    const int t0 = blockIdx.x * a.tokens_per_wg;
+    const int nt = min(a.tokens_per_wg, a.n_tokens - t0);
+    const int c = threadIdx.x & ((1 << a.lanes_log2) - 1);
+    const int step = kHeadThreads >> a.lanes_log2, total = nt * heads;
+    const bool in = 16 * c < a.head_dim;
+    const bool turned = 16 * c < a.rot_dim;
+    // this lane's two chunks of eight elements
+    const int half = a.rot_dim >> 1;
+    const int i0 = !in ? 0 : turned && !a.interleaved ? 8 * c : 16 * c;
+    const int i1 = !in ? 0 : turned && !a.interleaved ? half + 8 * c : i0 + 8;
+
+    int u = threadIdx.x >> a.lanes_log2;
+    HeadRow<TI, TO> r;
+    f32x8 x0 = {}, x1 = {};
+    int t = 0;
+    if (u < total) {  // the first head's loads leave before the angles are formed
+        t = u / heads;
+        r = head_row<TI, TO>(a, t0 + t, u - t * heads);
+        x0 = load8(r.in + i0);
+        x1 = load8(r.in + i1);
+    }
+    fill_turns(a, t0, nt, cs);
+    __syncthreads();
+    while (u < total) {
+        if (r.gain) {
+            float s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = __builtin_fmaf(x0[e], x0[e], __builtin_fmaf(x1[e], x1[e], s));
+            s = lanes_sum(in ? s : 0.0f, a.lanes_log2);
+            const float f = 1.0f / sqrtf(s / (float)a.head_dim + a.eps);
+            x0 = x0 * f * load8(r.gain + i0);
+            x1 = x1 * f * load8(r.gain + i1);
+        }
+        if (turned && r.set != 2) {
+            const f32x4 *w = reinterpret_cast<const f32x4 *>(cs + t * half + 8 * c);
+            float co[8], si[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const f32x4 p = w[e];
+                co[2 * e] = p.x, si[2 * e] = p.y, co[2 * e + 1] = p.z, si[2 * e + 1] = p.w;
+            }
+            f32x8 y0, y1;
+            if (!a.interleaved) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    y0[e] = x0[e] * co[e] - x1[e] * si[e];
+                    y1[e] = x1[e] * co[e] + x0[e] * si[e];
+                }
+            } else {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    y0[2 * p] = x0[2 * p] * co[p] - x0[2 * p + 1] * si[p];
+                    y0[2 * p + 1] = x0[2 * p + 1] * co[p] + x0[2 * p] * si[p];
+                    y1[2 * p] = x1[2 * p] * co[4 + p] - x1[2 * p + 1] * si[4 + p];
+                    y1[2 * p + 1] = x1[2 * p + 1] * co[4 + p] + x1[2 * p] * si[4 + p];
+                }
+            }
+            x0 = y0;
+            x1 = y1;
+        }
+        if (in && r.store) {
+            store8(r.out + i0, x0);
+            store8(r.out + i1, x1);
+        }
+        u += step;
+        if (u < total) {
+            t = u / heads;
+            r = head_row<TI, TO>(a, t0 + t, u - t * heads);
+            x0 = load8(r.in + i0);
+            x1 = load8(r.in + i1);
+        }
+    }
+}
+
+// Any even head_dim, rot_dim, stride and alignment: a lane takes pairs of elements one at a time.
+template <class TI, class TO>
+__global__ __launch_bounds__(kHeadThreads) void heads_any_kernel(HeadsArgs a) {
+    extern __shared__ float2 cs[];
+    const int heads = a.q.heads + a.k.heads + a.v.heads;
+    const int t0 = blockIdx.x * a.tokens_per_wg;
+    const int nt = min(a.tokens_per_wg, a.n_tokens - t0);
+    const int lanes = 1 << a.lanes_log2, c = threadIdx.x & (lanes - 1);
+    const int step = kHeadThreads >> a.lanes_log2, total = nt * heads, pairs = a.head_dim >> 1, half = a.rot_dim >> 1;
+    fill_turns(a, t0, nt, cs);
+    __syncthreads();
+    for (int u = threadIdx.x >> a.lanes_log2; u < total; u += step) {
+        const int t = u / heads;
+        const HeadRow<TI, TO> r = head_row<TI, TO>(a, t0 + t, u - t * heads);
+        float f = 1.0f;
+        if (r.gain) {
+            float s = 0.0f;
+            for (int p = c; p < pairs; p += lanes) {
+                const float x = (float)r.in[2 * p], y = (float)r.in[2 * p + 1];
+                s = __builtin_fmaf(x, x, __builtin_fmaf(y, y, s));
+            }
+            f = 1.0f / sqrtf(lanes_sum(s, a.lanes_log2) / (float)a.head_dim + a.eps);
+        }
+        for (int p = c; p < pairs; p += lanes) {
+            const bool split = p < half && !a.interleaved;
+            const int i0 = split ? p : 2 * p, i1 = split ? p + half : 2 * p + 1;
+            float x = (float)r.in[i0], y = (float)r.in[i1];
+            if (r.gain) {
+                x = x * f * r.gain[i0];
+                y = y * f * r.gain[i1];
+            }
+            if (p < half && r.set != 2) {
+                const float2 w = cs[t * half + p];
+                const float z = x * w.x - y * w.y;
+                y = y * w.x + x * w.y;
+                x = z;
+            }
+            if (r.store) {
+                r.out[i0] = (TO)x;
+                r.out[i1] = (TO)y;
+            }
+        }
+    }
+}
+
+template <class TI, class TO>
+static int launch_typed(const HeadsArgs &a, bool vec, hipStream_t s) {
+    const unsigned grid = (unsigned)((a.n_tokens + a.tokens_per_wg - 1) / a.tokens_per_wg);
+    const size_t lds = (size_t)a.tokens_per_wg * (size_t)(a.rot_dim / 2) * sizeof(float2);
+    if (vec)
+        heads_vec_kernel<TI, TO><<<grid, kHeadThreads, lds, s>>>(a);
+    else
+        heads_any_kernel<TI, TO><<<grid, kHeadThreads, lds, s>>>(a);
+    return (int)hipGetLastError();
+}
+
+template <class TI>
+static int launch_from(const HeadsArgs &a, int32_t dt_out, bool vec, hipStream_t s) {
+    if (dt_out == 0) return launch_typed<TI, float>(a, vec, s);
+    if (dt_out == 1) return launch_typed<TI, __bf16>(a, vec, s);
+    return launch_typed<TI, _Float16>(a, vec, s);
+}
+
+int launch_heads(const HeadsArgs &a, int32_t dt_in, int32_t dt_out, bool vec, void *stream) {
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (dt_in == 0) return launch_from<float>(a, dt_out, vec, s);
+    if (dt_in == 1) return launch_from<__bf16>(a, dt_out, vec, s);
+    return launch_from<_Float16>(a, dt_out, vec, s);
+}
+
+}  // namespace bpw

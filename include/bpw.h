@@ -479,6 +479,158 @@ void bpw_bitcos_plan_free(bpw_bitcos_plan *plan);
 bpw_status bpw_dense_head_gemv(const uint16_t *d_w_bf16, int64_t rows, int64_t cols, const uint16_t *d_x_bf16,
                                float *d_y, void *stream);
 
+/* ------------------------------------------------------------------------ decode step: heads, cache, attention, drafts */
+
+/* The operators between and after a decode step's ternary products: the norm and rotation of the query
+ * and key heads, the append to a paged key/value cache, attention over that cache, and the verification
+ * of drafted tokens. Each call is checked on the host and queued on `stream` without a copy, an
+ * allocation or a wait, so calls may be captured into a graph. What the arguments point at is read when
+ * the work runs: positions, slots, page tables and lengths may change between runs of the same
+ * arguments. */
+
+typedef enum bpw_dtype { BPW_F32 = 0, BPW_BF16 = 1, BPW_F16 = 2 } bpw_dtype;
+
+/* Head vectors of n tokens: element i of head h of token t is at d[t * token_stride + h * head_stride + i]
+ * (strides in elements, >= 0). A slice of a fused projection's rows is such a view. */
+typedef struct bpw_heads {
+    void *d;               /* device, elements of `dtype` */
+    int32_t heads;
+    int32_t dtype;         /* bpw_dtype */
+    int64_t token_stride;
+    int64_t head_stride;
+} bpw_heads;
+
+/* A paged key/value cache. Position i of a page, head h: K at d_k[page * k_page_stride + h *
+ * k_head_stride + i * k_row_stride], V likewise (strides in elements, head_dim contiguous), so both
+ * [pages][heads][page_size][head_dim] and [pages][page_size][heads][head_dim] are served. */
+typedef struct bpw_paged_kv {
+    void *d_k, *d_v;       /* device, elements of `dtype` */
+    int32_t dtype;         /* BPW_BF16 or BPW_F16 */
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t page_size;     /* positions of a page: a power of two, 16 .. 1024 */
+    int32_t n_pages;
+    uint32_t reserved;     /* 0 */
+    int64_t k_page_stride, k_head_stride, k_row_stride;
+    int64_t v_page_stride, v_head_stride, v_row_stride;
+} bpw_paged_kv;
+
+/* Position rotation. Frequency i turns a pair of elements (a, b) of a head by angle = position *
+ * d_inv_freq[i], reduced in float64: a' = a cos - b sin, b' = b cos + a sin. Pairs are (i, i + rot_dim / 2),
+ * or (2i, 2i + 1) if interleaved. Elements from rot_dim on are not turned; rot_dim 0 turns none. */
+typedef struct bpw_rotation {
+    const int32_t *d_positions; /* device int32 [n_tokens] */
+    const double *d_inv_freq;   /* device double [rot_dim / 2] */
+    int32_t rot_dim;            /* even, 0 .. head_dim */
+    int32_t interleaved;        /* 0 or 1 */
+} bpw_rotation;
+
+/* Norm and rotation of query and key heads in one pass: per token and head
+ *   n = x / sqrt(mean(x^2) + eps) * gain   (n = x where the gain is NULL), then the rotation,
+ * in float32, rounded once to the output's type. q (with q_out) or k (with k_out) may be left out
+ * (heads 0). Inputs and outputs are float32, bfloat16 or float16; q and k share the input type, q_out
+ * and k_out the output type. An output may be its input itself (same pointer, strides and type);
+ * otherwise outputs must not overlap inputs or each other. head_dim is even, 2 .. 1024. */
+typedef struct bpw_qk_norm_rope_args {
+    int32_t n_tokens, head_dim;
+    bpw_heads q, k, q_out, k_out;
+    const float *d_q_gain, *d_k_gain; /* device float [head_dim] or NULL: no norm */
+    float eps;                        /* finite, >= 0 */
+    uint32_t reserved;                /* 0 */
+    bpw_rotation rot;
+} bpw_qk_norm_rope_args;
+
+bpw_status bpw_qk_norm_rope(const bpw_qk_norm_rope_args *a, void *stream);
+
+/* Append n_tokens keys and values to a paged cache: k (norm and rotation as above, on the way) and v (as
+ * it is) rounded to the cache's type and written at slot d_slots[t] = page * page_size + offset. A slot
+ * outside [0, n_pages * page_size) writes nothing (a padding token). Valid slots must differ from one
+ * another. The queries of the same tokens may be normed and rotated in the same launch (q, q_out; heads
+ * 0 leaves them out; every token's query is written, padding tokens' too). k, v and q share their type;
+ * q_out has the cache's type. */
+typedef struct bpw_kv_append_args {
+    int32_t n_tokens;
+    uint32_t reserved;                /* 0 */
+    bpw_heads k, v, q, q_out;
+    const int64_t *d_slots;           /* device int64 [n_tokens] */
+    const float *d_q_gain, *d_k_gain; /* device float [head_dim] or NULL: no norm */
+    float eps;
+    uint32_t reserved2;               /* 0 */
+    bpw_rotation rot;
+    bpw_paged_kv kv;
+} bpw_kv_append_args;
+
+bpw_status bpw_kv_append(const bpw_kv_append_args *a, void *stream);
+
+/* Attention of a decode step whose sequences share a prefix. Sequence b has the query tokens
+ * d_q_starts[b] .. d_q_starts[b + 1] - 1 (n_b of them, at most max_q; none for an idle sequence) and sees
+ * the prefix's prefix_len positions, held by the pages d_prefix_pages[0 ..], then its own
+ * d_lens[b] positions, held by the pages of row b of d_table (the query tokens' own among them, last).
+ * Query token j of n_b sees the prefix and the first d_lens[b] - (n_b - 1 - j) own positions. Query head h
+ * reads key/value head h / (q.heads / kv_heads):
+ *   out = sum_i softmax_i(scale * <q, K_i>) V_i,   lse = log sum_i exp(scale * <q, K_i>)  (natural log).
+ * A token that sees nothing gets out = 0 and lse = -inf. Scores, maxima, sums and outputs are held in
+ * float32; the softmax weights are rounded to the cache's type for the matrix cores.
+ * Device values out of range read no memory: a page outside [0, n_pages) has its positions hidden, lengths
+ * are cut to [0, max_pages * page_size], query tokens past q's n_tokens or past max_q are left out.
+ * Cache contents past a length are not used, whatever they are; a position that some query tokens of its
+ * sequence see must hold finite values for the others too. Tokens of no sequence are not written.
+ * The prefix is read once for all sequences (once per 64 query rows of a key/value head), long prefixes
+ * and sequences are split over the GPU, and the parts joined by a second launch, in a fixed order.
+ * q and out have the cache's type; head_dim is a multiple of 8, 8 .. 256; pointers are 16-byte aligned and
+ * strides multiples of 8 elements; q.heads is a multiple of kv_heads. 1 <= n_seqs <= 1024. */
+typedef struct bpw_attn_shared_prefix_args {
+    int32_t n_tokens, n_seqs, max_q;
+    float scale;                      /* finite, usually 1 / sqrt(head_dim) */
+    bpw_heads q, out;
+    float *d_lse;                     /* device float [n_tokens][q.heads] or NULL */
+    const int32_t *d_prefix_pages;    /* device int32 [ceil(prefix_len / page_size)] (NULL if prefix_len is 0) */
+    int64_t prefix_len;               /* 0 .. 2^30 */
+    const int32_t *d_table;           /* device int32 [n_seqs][table_stride] */
+    int64_t table_stride;             /* >= max_pages */
+    int32_t max_pages;                /* entries of a table row; max_pages * page_size <= 2^30 */
+    uint32_t reserved;                /* 0 */
+    const int32_t *d_lens;            /* device int32 [n_seqs] */
+    const int32_t *d_q_starts;        /* device int32 [n_seqs + 1], rising from 0 */
+    bpw_paged_kv kv;
+} bpw_attn_shared_prefix_args;
+
+/* Device workspace bytes of a call with these arguments (0 if they are refused). */
+size_t bpw_attn_shared_prefix_workspace_bytes(const bpw_attn_shared_prefix_args *a);
+/* d_ws: 256-byte aligned, written by every call: calls that share one must not overlap. */
+bpw_status bpw_attn_shared_prefix(const bpw_attn_shared_prefix_args *a, void *d_ws, size_t ws_len, void *stream);
+
+/* Verification of drafted tokens by the target's probabilities. Sequence b has n_b drafted tokens x_0 ..
+ * (n_b = d_n_draft[b], or max_drafts where d_n_draft is NULL), the target's probabilities p_0 .. p_{n_b} of
+ * its positions, the draft's q_0 .. q_{n_b - 1}, and numbers u_i, r in [0, 1). x_i is accepted while
+ *   u_i * q_i(x_i) < p_i(x_i)      (exact: the product of two float32 in float64);
+ * with n accepted, one more token is drawn: from max(p_n - q_n, 0) if a draft was refused, from p_n if
+ * none was, as the first token whose running sum of masses exceeds r times their total (float64). Where
+ * max(p - q, 0) is zero everywhere, p is used. Entries that are not finite and positive have no mass; the
+ * last token with mass is drawn if none exceeds (r at 1), and -1 where none has mass. A NULL
+ * d_draft stands for drafts of certain tokens: q_i(x_i) = 1, all else 0. A drafted token outside the
+ * vocabulary is refused. out_tokens[b] = the accepted tokens, the drawn one, then -1; accepted[b] = n. */
+typedef struct bpw_verify_draft_args {
+    int32_t n_seqs, max_drafts;       /* n_seqs >= 0, 1 <= max_drafts <= 64 */
+    int32_t vocab;                    /* 1 .. 2^24 */
+    int32_t dtype;                    /* of d_target and d_draft: a bpw_dtype */
+    const void *d_target;             /* device [n_seqs][max_drafts + 1][vocab], strides below (elements) */
+    int64_t target_seq_stride, target_step_stride;
+    const void *d_draft;              /* device [n_seqs][max_drafts][vocab] or NULL */
+    int64_t draft_seq_stride, draft_step_stride;
+    const int32_t *d_tokens;          /* device int32 [n_seqs][max_drafts] */
+    const int32_t *d_n_draft;         /* device int32 [n_seqs] (cut to 0 .. max_drafts) or NULL */
+    const float *d_accept_u;          /* device float [n_seqs][max_drafts] */
+    const float *d_sample_u;          /* device float [n_seqs] */
+    int32_t *d_out_tokens;            /* device int32 [n_seqs][max_drafts + 1] */
+    int32_t *d_accepted;              /* device int32 [n_seqs] */
+} bpw_verify_draft_args;
+
+/* Device workspace bytes for n_seqs sequences and this vocabulary (0 if out of range). */
+size_t bpw_verify_draft_workspace_bytes(int32_t n_seqs, int32_t vocab);
+/* d_ws: 256-byte aligned, written by every call: calls that share one must not overlap. */
+bpw_status bpw_verify_draft(const bpw_verify_draft_args *a, void *d_ws, size_t ws_len, void *stream);
+
 /* ------------------------------------------------------------------------ measurement helpers */
 
 /* Streaming-read probe (Tritium paper, "Method": achieved bandwidth is divided by a streaming-read
