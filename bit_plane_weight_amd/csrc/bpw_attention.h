@@ -38,8 +38,7 @@ __device__ __forceinline__ f32x4 mma<_Float16>(u32v4 a, u32v4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// The work of one workgroup on one item: positions [32 * 4 * u0, 32 * 4 * u1) of a page list for a tile of
-// query rows.
+// The work of one workgroup on one item: units [u0, u1) of a page list for a tile of query rows.
 struct AttnSpan {
     const int32_t *pages;
     int32_t len;       // positions of the segment
@@ -50,8 +49,8 @@ struct AttnSpan {
     int32_t row0;      // first row of the tile
     int32_t n_rows;    // rows of all tiles
     int32_t u0, u1;
-    float *po;         // results of the tile: [16 * NQ][DP]
-    float2 *pml;       // [16 * NQ]
+    float *po;         // results of the tile: [rows][DP]
+    float2 *pml;       // [rows]
 };
 
 constexpr float kNone = -__builtin_inff();
@@ -303,6 +302,261 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s, Att
     }
 }
 
+// ------------------------------------------------------------------------------------------------
+// Many query rows (the prefix of a batch). Here the matrix cores and the exponentials are the bound, not
+// the memory: 64 or 128 rows share each key, so keys and values go once through LDS for the four waves,
+// moved there by the loads themselves (16 bytes a lane, no registers), one tile of kWideTile positions
+// ahead of its use. A wave holds 32 rows: with 32x32x16 products an operand read from LDS serves 32
+// rows, and two waves share a SIMD, so one's products run under the other's exponentials.
+//  - WQ = 4: a wave to each 32 of 128 rows, all positions; WQ = 2: 64 rows, two waves to each 32, half of a
+//    tile's positions each, joined at the end.
+//  - Weights stay in registers as above: a lane's 16 scores of 32 positions are the second operands of
+//    two products once their 16 positions each are numbered (register / 4, lane / 32, register % 4).
+//  - Values are read from LDS transposed (ds_read_b64_tr_b16: 16 lanes read 4 positions x 16 elements, each
+//    gets 4 positions of one element).
+//  - The 16-byte chunks of a row are permuted by an exclusive-or with a key of the row, chosen so that the
+//    rows one instruction reads lie in different banks.
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+constexpr int kWideTile = 64;
+
+template <class T>
+__device__ __forceinline__ f32x16 mma32(u32v4 a, u32v4 b, f32x16 c);
+template <>
+__device__ __forceinline__ f32x16 mma32<__bf16>(u32v4 a, u32v4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x16 mma32<_Float16>(u32v4 a, u32v4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// 16 bytes a lane from memory to LDS at `dst` (the same in all lanes) + 16 * lane. Waited for by vmcnt.
+typedef __attribute__((address_space(1))) const void global_cvoid;
+typedef __attribute__((address_space(3))) void lds_void;
+__device__ __forceinline__ void load_to_lds(void *dst, const void *src) {
+    __builtin_amdgcn_global_load_lds((global_cvoid *)src, (lds_void *)dst, 16, 0, 0);
+}
+__device__ __forceinline__ void wait_loads_to_lds() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Chunk keys. Rows of 128 bytes (DP = 64) come two to the 256 bytes of all banks, longer ones one or less.
+template <int DP>
+__device__ __forceinline__ int key_of_k(int row) {
+    return DP == 64 ? (row >> 1) & 7 : row & 15;
+}
+template <int DP>
+__device__ __forceinline__ int key_of_v(int row) {
+    return DP == 64 ? ((row >> 1) & 1) << 2 : ((row & 3) << 2) | ((row >> 2) & 3);
+}
+
+template <int DP>
+struct WideLds {
+    alignas(16) uint8_t k[2][kWideTile * DP * 2];
+    alignas(16) uint8_t v[2][kWideTile * DP * 2];
+};
+
+template <class T, int DP, int WQ>
+__device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s, WideLds<DP> &lds) {
+    constexpr int ROW = DP * 2, CPR = DP / 8, RPI = 64 / CPR;  // row bytes, chunks of a row, rows of one load
+    constexpr int KC = DP / 16, DB = DP / 32;
+    constexpr int PARTS = kAttnWaves / WQ, NB = kWideTile / 32 / PARTS;  // waves along a tile, blocks of 32 of each
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 31, g = lane >> 5, part = wave / WQ;
+    const int D = a.head_dim, pmask = (1 << a.page_log2) - 1;
+    const int row_first = s.row0 + 32 * (wave % WQ), row = row_first + n;
+
+    u32v4 q[KC];
+    {
+        const int j = row / a.group;
+        const T *p = static_cast<const T *>(a.q) + (int64_t)(s.tok0 + j) * a.q_ts +
+                     (int64_t)(s.head * a.group + row - j * a.group) * a.q_hs;
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+            q[c] = u32v4{0, 0, 0, 0};
+            if (row < s.n_rows && 16 * c + 8 * g < D) q[c] = *reinterpret_cast<const u32v4 *>(p + 16 * c + 8 * g);
+        }
+    }
+    const T *kbase = static_cast<const T *>(a.k) + (int64_t)s.head * a.k_hs;
+    const T *vbase = static_cast<const T *>(a.v) + (int64_t)s.head * a.v_hs;
+
+    auto page_of = [&](int pos) -> int {
+        if (pos >= s.len) return -1;
+        const int id = s.pages[pos >> a.page_log2];
+        return (uint32_t)id < (uint32_t)a.n_pages ? id : -1;
+    };
+    // This wave's 16 positions of the tile at `pos0`; hidden positions and elements past head_dim are zeros
+    // (a zero weight times whatever memory holds there would not be).
+    auto issue = [&](int buf, int pos0, int id) {
+        const int first = pos0 + 16 * wave;
+        const T *kp = kbase + (int64_t)id * a.k_ps + (int64_t)(first & pmask) * a.k_rs;
+        const T *vp = vbase + (int64_t)id * a.v_ps + (int64_t)(first & pmask) * a.v_rs;
+#pragma unroll
+        for (int i = 0; i < 16 / RPI; ++i) {
+            const int r = RPI * i + lane / CPR;  // of the wave's sixteen
+            const bool in = id >= 0 && first + r < s.len;
+            const int ck = (lane % CPR) ^ key_of_k<DP>(16 * wave + r), cv = (lane % CPR) ^ key_of_v<DP>(16 * wave + r);
+            uint8_t *dk = &lds.k[buf][(16 * wave + RPI * i) * ROW], *dv = &lds.v[buf][(16 * wave + RPI * i) * ROW];
+            if (in && 8 * ck < D)
+                load_to_lds(dk, kp + r * a.k_rs + 8 * ck);
+            else
+                *reinterpret_cast<u32v4 *>(dk + 16 * lane) = u32v4{0, 0, 0, 0};
+            if (in && 8 * cv < D)
+                load_to_lds(dv, vp + r * a.v_rs + 8 * cv);
+            else
+                *reinterpret_cast<u32v4 *>(dv + 16 * lane) = u32v4{0, 0, 0, 0};
+        }
+    };
+
+    // LDS addresses of this lane's reads; blocks of 32 (and 16) positions are whole keys apart
+    uint32_t ka[KC], va[DB][2];
+#pragma unroll
+    for (int c = 0; c < KC; ++c) ka[c] = n * ROW + (((2 * c + g) ^ key_of_k<DP>(n)) * 16);
+#pragma unroll
+    for (int c = 0; c < DB; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = lane & 15, r = 8 * h + 4 * g + (i >> 2);
+            const int chunk = 4 * c + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
+            va[c][h] = r * ROW + ((chunk ^ key_of_v<DP>(r)) * 16) + (i & 1) * 8;
+        }
+
+    f32x16 o[DB];
+#pragma unroll
+    for (int c = 0; c < DB; ++c) o[c] = f32x16{};
+    float m = kNone, l = 0.0f;
+
+    int pos0 = s.u0 * kAttnUnit, buf = 0;
+    const int end = min(s.len, s.u1 * kAttnUnit);
+    int id[kAttnWaves];
+#pragma unroll
+    for (int x = 0; x < kAttnWaves; ++x) id[x] = page_of(pos0 + 16 * x);
+    issue(0, pos0, wave == 0 ? id[0] : wave == 1 ? id[1] : wave == 2 ? id[2] : id[3]);
+    while (pos0 < end) {
+        const bool hidden = (id[0] | id[1] | id[2] | id[3]) < 0 || pos0 + kWideTile > s.len;
+        uint32_t pages = 0;  // bit x: positions 16 x .. 16 x + 15 of this tile are a page's
+#pragma unroll
+        for (int x = 0; x < kAttnWaves; ++x) {
+            pages |= id[x] >= 0 ? 1u << x : 0u;
+            id[x] = page_of(pos0 + kWideTile + 16 * x);
+        }
+        wait_loads_to_lds();
+        __syncthreads();  // this tile is there, and nobody reads the one before it any more
+        if (pos0 + kWideTile < end)
+            issue(buf ^ 1, pos0 + kWideTile, wave == 0 ? id[0] : wave == 1 ? id[1] : wave == 2 ? id[2] : id[3]);
+
+        f32x16 sc[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            sc[b] = f32x16{};
+            const uint8_t *p = &lds.k[buf][(part * NB + b) * 32 * ROW];
+#pragma unroll
+            for (int c = 0; c < KC; ++c) sc[b] = mma32<T>(*reinterpret_cast<const u32v4 *>(p + ka[c]), q[c], sc[b]);
+        }
+        if (hidden) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int at = 32 * (part * NB + b) + 8 * (r >> 2) + 4 * g + (r & 3);
+                    if (pos0 + at >= s.len || !((pages >> (at >> 4)) & 1)) sc[b][r] = kNone;
+                }
+        }
+        float top = kNone;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) top = fmaxf(top, fmaxf(sc[b][r], sc[b][r + 1]));
+        top *= a.scale_log2;
+        if (__any(top > m + 8.0f)) {  // as above: the shift is raised only by more than 2^8
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float up = fmaxf(m, top);
+            const float f = up == m ? 1.0f : __builtin_amdgcn_exp2f(m - up);
+            m = up;
+            l *= f;
+#pragma unroll
+            for (int c = 0; c < DB; ++c) o[c] *= f;
+        }
+        const float shift = m == kNone ? 0.0f : m;
+        u32v4 p[NB][2];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                f32x8 w;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][8 * h + r], a.scale_log2, -shift));
+                    l += w[r];
+                }
+                p[b][h] = __builtin_bit_cast(u32v4, __builtin_convertvector(w, typename Vec8<T>::type));
+            }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t *vp = &lds.v[buf][(32 * (part * NB + b) + 16 * h) * ROW];
+#pragma unroll
+                for (int c = 0; c < DB; ++c) {
+                    const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds_u8 *)(vp + va[c][0])));
+                    const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds_u8 *)(vp + va[c][1])));
+                    o[c] = mma32<T>(u32v4{x.x, x.y, y.x, y.y}, p[b][h], o[c]);
+                }
+            }
+        pos0 += kWideTile;
+        buf ^= 1;
+    }
+
+    l += __shfl_xor(l, 32);
+    if constexpr (PARTS == 2) {  // the second wave of the same rows hands over through LDS
+        constexpr int PAD = DP + 4;
+        float *box = reinterpret_cast<float *>(&lds) + (wave % WQ) * (32 * PAD);
+        float2 *ml = reinterpret_cast<float2 *>(reinterpret_cast<float *>(&lds) + WQ * 32 * PAD) + 32 * (wave % WQ);
+        static_assert((WQ * 32 * PAD + 2 * 32 * WQ) * 4 <= sizeof(WideLds<DP>), "the join fits the tiles' LDS");
+        __syncthreads();
+        if (part == 1) {
+#pragma unroll
+            for (int c = 0; c < DB; ++c)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    *reinterpret_cast<f32x4 *>(box + n * PAD + 32 * c + 8 * r + 4 * g) =
+                        f32x4{o[c][4 * r], o[c][4 * r + 1], o[c][4 * r + 2], o[c][4 * r + 3]};
+            if (g == 0) ml[n] = make_float2(m, l);
+        }
+        __syncthreads();
+        if (part == 0) {
+            const float2 x = ml[n];
+            const float up = fmaxf(m, x.x);
+            const float f0 = m == kNone ? 0.0f : __builtin_amdgcn_exp2f(m - up), f1 = x.x == kNone ? 0.0f : __builtin_amdgcn_exp2f(x.x - up);
+            m = up;
+            l = l * f0 + x.y * f1;
+#pragma unroll
+            for (int c = 0; c < DB; ++c)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const f32x4 y = *reinterpret_cast<const f32x4 *>(box + n * PAD + 32 * c + 8 * r + 4 * g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[c][4 * r + e] = o[c][4 * r + e] * f0 + y[e] * f1;
+                }
+        }
+    }
+    if (part == 0 && row < s.n_rows) {
+        const int at = 32 * (wave % WQ) + n;
+        if (g == 0) s.pml[at] = make_float2(m, l);
+        float *po = s.po + (int64_t)at * DP;
+#pragma unroll
+        for (int c = 0; c < DB; ++c)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *reinterpret_cast<f32x4 *>(po + 32 * c + 8 * r + 4 * g) =
+                    f32x4{o[c][4 * r], o[c][4 * r + 1], o[c][4 * r + 2], o[c][4 * r + 3]};
+    }
+    __syncthreads();  // LDS is free for the next item
+}
+
 // Query tokens of sequence b: first token and count, cut to what exists.
 __device__ __forceinline__ int2 seq_tokens(const AttnArgs &a, int b) {
     const int t0 = min(max(a.q_starts[b], 0), a.n_tokens), t1 = min(max(a.q_starts[b + 1], t0), a.n_tokens);
@@ -310,10 +564,13 @@ __device__ __forceinline__ int2 seq_tokens(const AttnArgs &a, int b) {
 }
 __device__ __forceinline__ int seq_len(const AttnArgs &a, int b) { return min(max(a.lens[b], 0), a.cap); }
 
-template <class T, int DP, int NQP, int NQS>
-__global__ __launch_bounds__(kAttnThreads) void attn_split_kernel(AttnArgs a) {
-    constexpr int MP = 16 * NQP, MS = 16 * NQS;
-    __shared__ AttnLds<DP> lds;
+// MP, MS: query rows of a tile in the prefix (16, 32: from registers; 64, 128: through LDS) and in a
+// suffix (16, 32).
+template <class T, int DP, int MP, int MS>
+__global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_kernel(AttnArgs a) {
+    constexpr bool WIDE = MP > 32;
+    constexpr size_t LDS = WIDE && sizeof(WideLds<DP>) > sizeof(AttnLds<DP>) ? sizeof(WideLds<DP>) : sizeof(AttnLds<DP>);
+    __shared__ alignas(16) uint8_t lds[LDS];
     __shared__ int32_t units[kAttnMaxSeqs + 1], items[kAttnMaxSeqs + 1];
     __shared__ int32_t wave_sum[kAttnWaves][2];
     __shared__ int32_t first_seq;
@@ -357,7 +614,8 @@ __global__ __launch_bounds__(kAttnThreads) void attn_split_kernel(AttnArgs a) {
         eu += un[x], ei += it[x];
         if (b == a.n_seqs - 1) units[a.n_seqs] = eu, items[a.n_seqs] = ei;
     }
-    // Equal shares. A unit of the prefix costs its NQP tiles of 16 rows, one of a suffix NQS.
+    // Equal shares by the cost of a unit.
+    constexpr int NQP = MP <= 32 ? 2 : MP == 64 ? 3 : 4, NQS = 2;
     const int up = (a.prefix_len + kAttnUnit - 1) / kAttnUnit, total_p = a.kv_heads * a.tiles_p * up;
     int qp = 1, qs = 1, wp = total_p, ws = total_s;
     if (wp + ws > a.n_wgs) {
@@ -378,7 +636,11 @@ __global__ __launch_bounds__(kAttnThreads) void attn_split_kernel(AttnArgs a) {
             a.sched[kSchedHead + a.n_seqs + 1 + b] = items[b];
         }
     }
+    // Workgroup b runs on XCD b % 8: neighbours in the dealing, which read the same keys for other rows,
+    // share one XCD's L2.
     int w = blockIdx.x;
+    const int per = gridDim.x >> 3;
+    if (w < 8 * per) w = (w & 7) * per + (w >> 3);
     AttnSpan s;
     if (w < wp) {
         int u = w * qp;
@@ -397,7 +659,10 @@ __global__ __launch_bounds__(kAttnThreads) void attn_split_kernel(AttnArgs a) {
             s.u1 = min(up, at + stop - u);
             s.po = a.part_o + (int64_t)(item + w) * (MP * DP);
             s.pml = a.part_ml + (int64_t)(item + w) * MP;
-            attend<T, NQP, DP>(a, s, lds);
+            if constexpr (WIDE)
+                attend_wide<T, DP, MP / 32>(a, s, reinterpret_cast<WideLds<DP> &>(lds));
+            else
+                attend<T, NQP, DP>(a, s, reinterpret_cast<AttnLds<DP> &>(lds));
             u += s.u1 - s.u0;
         }
         return;
@@ -434,7 +699,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_split_kernel(AttnArgs a) {
         s.u1 = min(ub, at + stop - u);
         s.po = a.part_o + a.part_s + piece * (MS * DP);
         s.pml = a.part_ml + a.ml_s + piece * MS;
-        attend<T, NQS, DP>(a, s, lds);
+        attend<T, NQS, DP>(a, s, reinterpret_cast<AttnLds<DP> &>(lds));
         u += s.u1 - s.u0;
     }
 }
@@ -523,27 +788,26 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int
             sum == 0.0f ? kNone : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
 }
 
-template <class T, int DP, int NQP, int NQS>
+template <class T, int DP, int MP, int MS>
 static int run_attn(const AttnArgs &a, hipStream_t st) {
-    attn_split_kernel<T, DP, NQP, NQS><<<(unsigned)a.n_wgs, kAttnThreads, 0, st>>>(a);
+    attn_split_kernel<T, DP, MP, MS><<<(unsigned)a.n_wgs, kAttnThreads, 0, st>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
-    attn_join_kernel<T, DP><<<(unsigned)((int64_t)a.n_seqs * a.max_q * a.q_heads), kAttnThreads, 0, st>>>(a, 16 * NQP, 16 * NQS);
+    attn_join_kernel<T, DP><<<(unsigned)((int64_t)a.n_seqs * a.max_q * a.q_heads), kAttnThreads, 0, st>>>(a, MP, MS);
     return (int)hipGetLastError();
 }
 
-// nqp, nqs: tiles of 16 query rows that one workgroup holds, in the prefix and in a suffix.
 template <class T, int DP>
-static int run_attn_tiles(const AttnArgs &a, int32_t nqp, int32_t nqs, hipStream_t st) {
-    if (nqs == 1) {
-        if (nqp == 1) return run_attn<T, DP, 1, 1>(a, st);
-        if (nqp == 2) return run_attn<T, DP, 2, 1>(a, st);
-        if constexpr (DP <= 128) return run_attn<T, DP, 4, 1>(a, st);
-    } else {
-        if (nqp == 2) return run_attn<T, DP, 2, 2>(a, st);
-        if constexpr (DP <= 128) return run_attn<T, DP, 4, 2>(a, st);
+static int run_attn_tiles(const AttnArgs &a, int32_t mp, int32_t ms, hipStream_t st) {
+    if (ms == 16) {
+        if (mp == 16) return run_attn<T, DP, 16, 16>(a, st);
+        if (mp == 32) return run_attn<T, DP, 32, 16>(a, st);
+        if (mp == 64) return run_attn<T, DP, 64, 16>(a, st);
+        return run_attn<T, DP, 128, 16>(a, st);
     }
-    return (int)hipErrorInvalidValue;
+    if (mp == 32) return run_attn<T, DP, 32, 32>(a, st);
+    if (mp == 64) return run_attn<T, DP, 64, 32>(a, st);
+    return run_attn<T, DP, 128, 32>(a, st);
 }
 
 }  // namespace bpw

@@ -3,10 +3,10 @@
 
 namespace bpw {
 
-int launch_attn_d128(const AttnArgs &a, int32_t dtype, int32_t nqp, int32_t nqs, void *stream) {
+int launch_attn_d128(const AttnArgs &a, int32_t dtype, int32_t mp, int32_t ms, void *stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (dtype == 1) return run_attn_tiles<__bf16, 128>(a, nqp, nqs, s);
-    return run_attn_tiles<_Float16, 128>(a, nqp, nqs, s);
+    if (dtype == 1) return run_attn_tiles<__bf16, 128>(a, mp, ms, s);
+    return run_attn_tiles<_Float16, 128>(a, mp, ms, s);
 }
 
 }  // namespace bpw

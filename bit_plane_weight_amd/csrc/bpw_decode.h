@@ -74,9 +74,9 @@ struct AttnArgs {
 };
 constexpr int kSchedHead = 8;  // units per prefix item, prefix units per workgroup, suffix units per workgroup
 
-int launch_attn_d64(const AttnArgs &a, int32_t dtype, int32_t nqp, int32_t nqs, void *stream);
-int launch_attn_d128(const AttnArgs &a, int32_t dtype, int32_t nqp, int32_t nqs, void *stream);
-int launch_attn_d256(const AttnArgs &a, int32_t dtype, int32_t nqp, int32_t nqs, void *stream);
+int launch_attn_d64(const AttnArgs &a, int32_t dtype, int32_t mp, int32_t ms, void *stream);
+int launch_attn_d128(const AttnArgs &a, int32_t dtype, int32_t mp, int32_t ms, void *stream);
+int launch_attn_d256(const AttnArgs &a, int32_t dtype, int32_t mp, int32_t ms, void *stream);
 
 // ---------------------------------------------------------------- draft verification
 

@@ -219,7 +219,7 @@ namespace {
 constexpr int32_t kWgs = 512;  // two workgroups for each of the 256 CUs
 
 struct AttnShape {
-    int32_t dp, nqp, nqs;
+    int32_t dp, mp, ms;
     int32_t group, tiles_p;
     int64_t cap, pieces_p, pieces_s;
     int32_t n_wgs;
@@ -254,9 +254,9 @@ bpw_status attn_shape(const bpw_attn_shared_prefix_args *a, AttnShape *s) {
     const int64_t rows_p = (int64_t)a->n_tokens * s->group;
     const int64_t max_q = a->max_q < a->n_tokens ? a->max_q : (a->n_tokens > 0 ? a->n_tokens : 1);
     const int64_t rows_s = max_q * s->group;
-    s->nqs = rows_s <= 16 ? 1 : 2;
-    s->nqp = a->prefix_len == 0 || rows_p <= 16 * s->nqs ? s->nqs : rows_p <= 32 || s->dp == 256 ? 2 : 4;
-    const int64_t mp = 16 * s->nqp, ms = 16 * s->nqs;
+    s->ms = rows_s <= 16 ? 16 : 32;
+    s->mp = a->prefix_len == 0 || rows_p <= s->ms ? s->ms : rows_p <= 32 ? 32 : rows_p <= 64 ? 64 : 128;
+    const int64_t mp = s->mp, ms = s->ms;
     const int64_t tiles_p = (rows_p + mp - 1) / mp, tiles_s = (rows_s + ms - 1) / ms;
     const int64_t up = (a->prefix_len + bpw::kAttnUnit - 1) / bpw::kAttnUnit;
     const int64_t us = (s->cap + bpw::kAttnUnit - 1) / bpw::kAttnUnit;
@@ -352,11 +352,11 @@ bpw_status bpw_attn_shared_prefix(const bpw_attn_shared_prefix_args *a, void *d_
     k.sched = reinterpret_cast<int32_t *>(ws);
     k.part_o = reinterpret_cast<float *>(ws + s.po);
     k.part_ml = reinterpret_cast<float2 *>(ws + s.pml);
-    k.part_s = s.pieces_p * 16 * s.nqp * s.dp;
-    k.ml_s = s.pieces_p * 16 * s.nqp;
-    const int e = s.dp == 64    ? bpw::launch_attn_d64(k, c.dtype, s.nqp, s.nqs, stream)
-                  : s.dp == 128 ? bpw::launch_attn_d128(k, c.dtype, s.nqp, s.nqs, stream)
-                                : bpw::launch_attn_d256(k, c.dtype, s.nqp, s.nqs, stream);
+    k.part_s = s.pieces_p * s.mp * s.dp;
+    k.ml_s = s.pieces_p * s.mp;
+    const int e = s.dp == 64    ? bpw::launch_attn_d64(k, c.dtype, s.mp, s.ms, stream)
+                  : s.dp == 128 ? bpw::launch_attn_d128(k, c.dtype, s.mp, s.ms, stream)
+                                : bpw::launch_attn_d256(k, c.dtype, s.mp, s.ms, stream);
     return hip_status(e, "attention launch");
 }
 

@@ -275,6 +275,13 @@ class Attn:
     ([5, 1], [64, 70], 6, 3, 192, 1024, 90, BF16),
     ([1, 7], [31, 32], 3, 3, 24, 16, 48, F16),
     ([2] * 40, [3 + 7 * i for i in range(40)], 8, 2, 64, 16, 1400, BF16),
+    # prefix rows of 33 .. 64 and beyond: through LDS, with every padding of the head and ragged last tiles of rows
+    ([1] * 17, [5] * 17, 8, 2, 128, 16, 333, F16),
+    ([3] * 13, [40 + i for i in range(13)], 12, 2, 128, 64, 65, BF16),
+    ([4] * 10, [16] * 10, 4, 1, 80, 32, 128, F16),
+    ([1] * 45, [1] * 45, 6, 2, 48, 16, 63, BF16),
+    ([2] * 10, [70] * 10, 6, 2, 256, 16, 190, BF16),
+    ([5] * 9, [70] * 9, 12, 2, 200, 128, 131, F16),
 ])
 @pytest.mark.parametrize("layout", ["hnd", "nhd"])
 def test_attention(dev, n_q, lens, Hq, Hk, D, P, prefix, dt, layout):
@@ -323,6 +330,30 @@ def test_attention_runtime_values_out_of_range(dev):
     a.plan().run()
     torch.cuda.synchronize()
     a.check("starts")
+
+
+@pytest.mark.parametrize("n,D", [(9, 64), (40, 128), (9, 256)])
+def test_attention_wide_prefix_with_missing_pages(dev, n, D):
+    """The same for a prefix that many rows share: the first, a middle and the last page do not exist."""
+    a = Attn(dev, [1] * n, [3] * n, 16, 2, D, 16, 165, F16, seed=n)
+    a.prefix_pages[0], a.prefix_pages[4], a.prefix_pages[5], a.prefix_pages[10] = -1, 2 ** 31 - 1, -2 ** 31, a.k.shape[0]
+    a.plan().run()
+    torch.cuda.synchronize()
+    a.check()
+    a.prefix_pages.fill_(-1)
+    a.len_t.zero_()
+    a.plan().run()
+    torch.cuda.synchronize()
+    a.check("nothing")
+
+
+def test_attention_wide_peaked_and_wide_scores(dev):
+    a = Attn(dev, [2] * 20, [9] * 20, 8, 2, 128, 16, 517, BF16, seed=29)
+    a.k *= torch.linspace(0.1, 6, a.k.shape[0], device=dev).to(BF16)[:, None, None, None]
+    for a.scale in (2.0, 1e-30):
+        a.plan().run()
+        torch.cuda.synchronize()
+        a.check(str(a.scale))
 
 
 def test_attention_peaked_and_wide_scores(dev):
