@@ -336,10 +336,16 @@ __device__ __forceinline__ f32x16 mma32<_Float16>(u32v4 a, u32v4 b, f32x16 c) {
 }
 
 // 16 bytes a lane from memory to LDS at `dst` (the same in all lanes) + 16 * lane. Waited for by vmcnt.
-typedef __attribute__((address_space(1))) const void global_cvoid;
-typedef __attribute__((address_space(3))) void lds_void;
+// Written as one asm block (m0, which holds the LDS address, is put back) because the compiler makes every later
+// LDS read wait for loads to LDS that it knows of, whatever part of LDS they write; the block writes no register.
 __device__ __forceinline__ void load_to_lds(void *dst, const void *src) {
-    __builtin_amdgcn_global_load_lds((global_cvoid *)src, (lds_void *)dst, 16, 0, 0);
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(size_t)(lds_u8 *)dst);
+    uint32_t keep;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off\n\ts_mov_b32 m0, %0"
+        : "=&s"(keep)
+        : "s"(at), "v"(src)
+        : "memory");
 }
 __device__ __forceinline__ void wait_loads_to_lds() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
@@ -394,11 +400,21 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
         const int first = pos0 + 16 * wave;
         const T *kp = kbase + (int64_t)id * a.k_ps + (int64_t)(first & pmask) * a.k_rs;
         const T *vp = vbase + (int64_t)id * a.v_ps + (int64_t)(first & pmask) * a.v_rs;
+        if (id >= 0 && first + 16 <= s.len && D == DP) {
+#pragma unroll
+            for (int i = 0; i < 16 / RPI; ++i) {
+                const int r = RPI * i + lane / CPR;
+                const int ck = (lane % CPR) ^ key_of_k<DP>(r), cv = (lane % CPR) ^ key_of_v<DP>(r);
+                load_to_lds(&lds.k[buf][(16 * wave + RPI * i) * ROW], kp + r * a.k_rs + 8 * ck);
+                load_to_lds(&lds.v[buf][(16 * wave + RPI * i) * ROW], vp + r * a.v_rs + 8 * cv);
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < 16 / RPI; ++i) {
             const int r = RPI * i + lane / CPR;  // of the wave's sixteen
             const bool in = id >= 0 && first + r < s.len;
-            const int ck = (lane % CPR) ^ key_of_k<DP>(16 * wave + r), cv = (lane % CPR) ^ key_of_v<DP>(16 * wave + r);
+            const int ck = (lane % CPR) ^ key_of_k<DP>(r), cv = (lane % CPR) ^ key_of_v<DP>(r);
             uint8_t *dk = &lds.k[buf][(16 * wave + RPI * i) * ROW], *dv = &lds.v[buf][(16 * wave + RPI * i) * ROW];
             if (in && 8 * ck < D)
                 load_to_lds(dk, kp + r * a.k_rs + 8 * ck);
@@ -448,14 +464,41 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
         if (pos0 + kWideTile < end)
             issue(buf ^ 1, pos0 + kWideTile, wave == 0 ? id[0] : wave == 1 ? id[1] : wave == 2 ? id[2] : id[3]);
 
+        // Operands are read from LDS a group of products ahead: the reads of group x + 1 run under the products
+        // of group x (the scheduling barriers keep the compiler from sinking each read to its use).
         f32x16 sc[NB];
+        {
+            constexpr int GK = 4, NG = NB * KC / GK;
+            u32v4 kf[2][GK];
+            auto read_k = [&](int x, u32v4 (&f)[GK]) {
+                const uint8_t *p = &lds.k[buf][(part * NB + x * GK / KC) * 32 * ROW];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            sc[b] = f32x16{};
-            const uint8_t *p = &lds.k[buf][(part * NB + b) * 32 * ROW];
+                for (int c = 0; c < GK; ++c) f[c] = *reinterpret_cast<const u32v4 *>(p + ka[(x * GK + c) % KC]);
+            };
+            read_k(0, kf[0]);
 #pragma unroll
-            for (int c = 0; c < KC; ++c) sc[b] = mma32<T>(*reinterpret_cast<const u32v4 *>(p + ka[c]), q[c], sc[b]);
+            for (int x = 0; x < NG; ++x) {
+                if (x + 1 < NG) read_k(x + 1, kf[(x + 1) & 1]);
+                __builtin_amdgcn_sched_barrier(0);
+                const int b = x * GK / KC;
+                if (x * GK % KC == 0) sc[b] = f32x16{};
+#pragma unroll
+                for (int c = 0; c < GK; ++c) sc[b] = mma32<T>(kf[x & 1][c], q[(x * GK + c) % KC], sc[b]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
+        u32v4 vf[2][DB];
+        auto read_v = [&](int x, u32v4 (&f)[DB]) {  // positions 16 x .. 16 x + 15 of this wave's blocks
+            const uint8_t *vp = &lds.v[buf][(32 * part * NB + 16 * x) * ROW];
+#pragma unroll
+            for (int c = 0; c < DB; ++c) {
+                const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds_u8 *)(vp + va[c][0])));
+                const u32x2 z = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds_u8 *)(vp + va[c][1])));
+                f[c] = u32v4{y.x, y.y, z.x, z.y};
+            }
+        };
+        read_v(0, vf[0]);
+        __builtin_amdgcn_sched_barrier(0);
         if (hidden) {
 #pragma unroll
             for (int b = 0; b < NB; ++b)
@@ -495,17 +538,13 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
                 p[b][h] = __builtin_bit_cast(u32v4, __builtin_convertvector(w, typename Vec8<T>::type));
             }
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int x = 0; x < 2 * NB; ++x) {
+            if (x + 1 < 2 * NB) read_v(x + 1, vf[(x + 1) & 1]);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint8_t *vp = &lds.v[buf][(32 * (part * NB + b) + 16 * h) * ROW];
-#pragma unroll
-                for (int c = 0; c < DB; ++c) {
-                    const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds_u8 *)(vp + va[c][0])));
-                    const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds_u8 *)(vp + va[c][1])));
-                    o[c] = mma32<T>(u32v4{x.x, x.y, y.x, y.y}, p[b][h], o[c]);
-                }
-            }
+            for (int c = 0; c < DB; ++c) o[c] = mma32<T>(vf[x & 1][c], p[x >> 1][x & 1], o[c]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         pos0 += kWideTile;
         buf ^= 1;
     }
@@ -615,14 +654,14 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_ke
         if (b == a.n_seqs - 1) units[a.n_seqs] = eu, items[a.n_seqs] = ei;
     }
     // Equal shares by the cost of a unit.
-    constexpr int NQP = MP <= 32 ? 2 : MP == 64 ? 3 : 4, NQS = 2;
+    constexpr int COST_P = MP <= 32 ? 2 : MP == 64 ? 3 : 4, COST_S = 2;
     const int up = (a.prefix_len + kAttnUnit - 1) / kAttnUnit, total_p = a.kv_heads * a.tiles_p * up;
     int qp = 1, qs = 1, wp = total_p, ws = total_s;
     if (wp + ws > a.n_wgs) {
-        int share = (int)(((int64_t)total_p * NQP + (int64_t)total_s * NQS + a.n_wgs - 1) / a.n_wgs);
+        int share = (int)(((int64_t)total_p * COST_P + (int64_t)total_s * COST_S + a.n_wgs - 1) / a.n_wgs);
         do {
-            qp = max(1, share / NQP);
-            qs = max(1, share / NQS);
+            qp = max(1, share / COST_P);
+            qs = max(1, share / COST_S);
             wp = (total_p + qp - 1) / qp;
             ws = (total_s + qs - 1) / qs;
             share += 1 + share / 16;
@@ -662,7 +701,7 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_ke
             if constexpr (WIDE)
                 attend_wide<T, DP, MP / 32>(a, s, reinterpret_cast<WideLds<DP> &>(lds));
             else
-                attend<T, NQP, DP>(a, s, reinterpret_cast<AttnLds<DP> &>(lds));
+                attend<T, MP / 16, DP>(a, s, reinterpret_cast<AttnLds<DP> &>(lds));
             u += s.u1 - s.u0;
         }
         return;
@@ -699,7 +738,7 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_ke
         s.u1 = min(ub, at + stop - u);
         s.po = a.part_o + a.part_s + piece * (MS * DP);
         s.pml = a.part_ml + a.ml_s + piece * MS;
-        attend<T, NQS, DP>(a, s, reinterpret_cast<AttnLds<DP> &>(lds));
+        attend<T, MS / 16, DP>(a, s, reinterpret_cast<AttnLds<DP> &>(lds));
         u += s.u1 - s.u0;
     }
 }
