@@ -4,8 +4,9 @@
 // Mathematics. For a query row q and positions i: s_i = scale <q, K_i>; with a running maximum m and sum
 // l = sum exp(s_i - m), o = sum exp(s_i - m) V_i, parts over disjoint positions join exactly:
 // m = max m_p, l = sum exp(m_p - m) l_p, o = sum exp(m_p - m) o_p. So the positions of one
-// (segment, key/value head, tile of query rows) are cut into units of kAttnUnit, units are dealt to the
-// workgroups in equal contiguous runs, and a second launch joins the parts in order.
+// (segment, key/value head, tile of query rows) - an item - are cut into units, units are dealt to the waves (or
+// workgroups, for prefixes that many rows share) in equal contiguous runs, and a second launch joins
+// the parts in order.
 //
 // The rows of a tile are the queries that read the same keys: the heads of one group, times the query
 // tokens of a sequence, and in the prefix times all sequences, so the prefix is read once for them.
@@ -19,7 +20,8 @@
 //  - values are read row-wise in the same numbering (lane: 8 positions x 8 elements) and turned by
 //    v_perm_b32 (32 for 64 elements), tile c of V^T holding elements 8 m + c, so that a lane's results are
 //    8 neighbours of the output row.
-// No LDS is used until the four waves of a workgroup join their parts.
+// No LDS is used and no wave waits for another. Keys and values are loaded non-temporally, as they are read once:
+// 964 MB over four sequences take 155 us so and 174 us without.
 #pragma once
 
 #include "bpw_decode.h"
@@ -38,7 +40,7 @@ __device__ __forceinline__ f32x4 mma<_Float16>(u32v4 a, u32v4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// The work of one workgroup on one item: units [u0, u1) of a page list for a tile of query rows.
+// The work of one wave or workgroup on one item: positions [pos0, pos1) of a page list for a tile of query rows.
 struct AttnSpan {
     const int32_t *pages;
     int32_t len;       // positions of the segment
@@ -48,27 +50,50 @@ struct AttnSpan {
     int32_t head;      // key/value head
     int32_t row0;      // first row of the tile
     int32_t n_rows;    // rows of all tiles
-    int32_t u0, u1;
+    int32_t pos0, pos1;
     float *po;         // results of the tile: [rows][DP]
     float2 *pml;       // [rows]
 };
 
 constexpr float kNone = -__builtin_inff();
+constexpr float kShiftLimit = 1024.0f;  // float16 weights reach 65504
 
-// LDS of the join of four waves: 16 rows of outputs, and the maxima and sums of all rows.
-template <int DP>
-struct AttnLds {
-    float o[kAttnWaves][16][DP + 4];
-    float2 ml[kAttnWaves][64];
+// Pages of the positions to come, one granule of 16 positions a lane (pages hold a multiple of 16, so a granule
+// never straddles two): two runs of 64 granules, the second loaded while the first is in use, so that
+// no load of keys waits for a page number.
+struct AttnPages {
+    int32_t cur, next;  // page, or -1: past the end, or not a page of the cache
+    int32_t base;       // first granule of `cur`
+
+    __device__ __forceinline__ int32_t fetch(const AttnArgs &a, const AttnSpan &s, int granule) const {
+        const int pos = 16 * (granule + (int)(threadIdx.x & 63));
+        int32_t id = -1;
+        if (pos < s.len) id = s.pages[pos >> a.page_log2];
+        return (uint32_t)id < (uint32_t)a.n_pages ? id : -1;
+    }
+    __device__ __forceinline__ void start(const AttnArgs &a, const AttnSpan &s, int pos) {
+        base = pos >> 4;
+        cur = fetch(a, s, base);
+        next = fetch(a, s, base + 64);
+    }
+    // Page of granule `granule`, which is at most 64 past the last one asked for. The same in all lanes.
+    __device__ __forceinline__ int32_t of(const AttnArgs &a, const AttnSpan &s, int granule) {
+        if (granule >= base + 64) {
+            base += 64;
+            cur = next;
+            next = fetch(a, s, base + 64);
+        }
+        return __builtin_amdgcn_readlane(cur, granule - base);
+    }
 };
 
 template <class T, int NQ, int DP>
-__device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s, AttnLds<DP> &lds) {
+__device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s) {
     constexpr int KC = DP / 32;            // key chunks of 32 elements
     constexpr int EL = DP < 128 ? DP / 16 : 8;  // neighbouring elements of a value row in one lane
     constexpr int NH = DP / (16 * EL);     // such runs
     constexpr int VW = EL / 2;             // their words
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
     const int n = lane & 15, g = lane >> 4;
     const int D = a.head_dim, pmask = (1 << a.page_log2) - 1;
 
@@ -112,20 +137,14 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s, Att
         for (int c = 0; c < NH * EL; ++c) o[i][c] = f32x4{0, 0, 0, 0};
     }
 
-    // page of the 16 positions from `pos` on, or -1: past the end or not a page of the cache. Pages hold
-    // a multiple of 16 positions, so such a tile never straddles two.
-    auto page_of = [&](int pos) -> int {
-        if (pos >= s.len) return -1;
-        const int id = s.pages[pos >> a.page_log2];
-        return (uint32_t)id < (uint32_t)a.n_pages ? id : -1;
-    };
+    AttnPages pages;
     auto load_keys = [&](int pos, int id, u32v4 (&k)[KC]) {
 #pragma unroll
         for (int c = 0; c < KC; ++c) k[c] = u32v4{0, 0, 0, 0};
         if (id >= 0) {
             const T *p = kbase + (int64_t)id * a.k_ps + (int64_t)(pos & pmask) * a.k_rs;
 #pragma unroll
-            for (int c = 0; c < KC; ++c) k[c] = *reinterpret_cast<const u32v4 *>(p + koff[c]);
+            for (int c = 0; c < KC; ++c) k[c] = __builtin_nontemporal_load(reinterpret_cast<const u32v4 *>(p + koff[c]));
         }
     };
     auto load_values = [&](int pos, int id, uint32_t (&v)[4][NH][VW]) {
@@ -137,10 +156,10 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s, Att
                 for (int h = 0; h < NH; ++h) {
                     const T *e = p + r * a.v_rs + voff[h];
                     if constexpr (VW == 4) {
-                        const u32v4 w = *reinterpret_cast<const u32v4 *>(e);
+                        const u32v4 w = __builtin_nontemporal_load(reinterpret_cast<const u32v4 *>(e));
                         v[r][h][0] = w.x, v[r][h][1] = w.y, v[r][h][2] = w.z, v[r][h][3] = w.w;
                     } else {
-                        const u32x2 w = *reinterpret_cast<const u32x2 *>(e);
+                        const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(e));
                         v[r][h][0] = w.x, v[r][h][1] = w.y;
                     }
                 }
@@ -154,16 +173,13 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s, Att
         }
     };
 
-    int kv0 = s.u0 * kAttnUnit + wave * kAttnStep;
-    const int end = min(s.len, s.u1 * kAttnUnit);
-    int id0 = -1, id1 = -1;
+    int kv0 = s.pos0;
+    const int end = min(s.len, s.pos1);
     u32v4 k0[KC], k1[KC];
-    if (kv0 < end) {
-        id0 = page_of(kv0);
-        id1 = page_of(kv0 + 16);
-        load_keys(kv0, id0, k0);
-        load_keys(kv0 + 16, id1, k1);
-    }
+    pages.start(a, s, kv0);
+    int id0 = pages.of(a, s, kv0 >> 4), id1 = pages.of(a, s, (kv0 >> 4) + 1);
+    load_keys(kv0, id0, k0);
+    load_keys(kv0 + 16, id1, k1);
     while (kv0 < end) {
         uint32_t v[8][NH][VW];
         load_values(kv0, id0, *reinterpret_cast<uint32_t(*)[4][NH][VW]>(&v[0]));
@@ -185,10 +201,10 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s, Att
                 sc[i][1] = mma<T>(k1[c], q[i][c], sc[i][1]);
             }
         const int here = kv0, c0 = id0, c1 = id1;
-        kv0 += kAttnUnit;
+        kv0 += kAttnStep;
         if (kv0 < end) {  // the next step's keys
-            id0 = page_of(kv0);
-            id1 = page_of(kv0 + 16);
+            id0 = pages.of(a, s, kv0 >> 4);
+            id1 = pages.of(a, s, (kv0 >> 4) + 1);
             load_keys(kv0, id0, k0);
             load_keys(kv0 + 16, id1, k1);
         }
@@ -213,30 +229,35 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s, Att
         u32v4 p[NQ];
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-            float top = kNone;
+            // The weights are taken against a shift, not the exact maximum: while a lane's sum of a step stays
+            // below kShiftLimit no weight has lost anything, in float32 or in 16 bits, and no maximum is formed.
+            // Otherwise (the first step, a score far above all before it, NaN) the shift becomes the maximum.
+            f32x8 w;
+            float sum = 0.0f;
+            const auto weigh = [&](float shift) {
+                sum = 0.0f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) top = fmaxf(top, fmaxf(sc[i][0][r], sc[i][1][r]));
-            top *= a.scale_log2;
-            // The maximum is a common shift of a row, not its exact maximum: it is raised only when a
-            // score exceeds it by 2^8 (weights up to 256 lose nothing in float32, nor in the 16-bit types),
-            // so most steps skip the exchange between lanes and the rescaling of o.
-            if (__any(top > m[i] + 8.0f)) {
+                for (int r = 0; r < 8; ++r) {
+                    w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i][r >> 2][r & 3], a.scale_log2, -shift));
+                    sum += w[r];
+                }
+            };
+            weigh(m[i]);  // (a shift of minus infinity gives infinities or NaN, which take the branch)
+            if (__any(!(sum < kShiftLimit))) {
+                float top = kNone;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) top = fmaxf(top, fmaxf(sc[i][0][r], sc[i][1][r]));
                 top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
+                top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
                 const float up = fmaxf(m[i], top);
                 const float f = up == m[i] ? 1.0f : __builtin_amdgcn_exp2f(m[i] - up);
                 m[i] = up;
                 l[i] *= f;
 #pragma unroll
                 for (int c = 0; c < NH * EL; ++c) o[i][c] *= f;
+                weigh(up == kNone ? 0.0f : up);
             }
-            const float shift = m[i] == kNone ? 0.0f : m[i];
-            f32x8 w;
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i][r >> 2][r & 3], a.scale_log2, -shift));
-                l[i] += w[r];
-            }
+            l[i] += sum;
             // weights in 16 bits: the matrix cores' operand. Its relative error of half a step is averaged
             // over the positions; the sum l is of the unrounded weights.
             p[i] = __builtin_bit_cast(u32v4, __builtin_convertvector(w, typename Vec8<T>::type));
@@ -254,29 +275,14 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s, Att
             }
     }
 
-    // join the four waves
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
         l[i] += __shfl_xor(l[i], 16);
         l[i] += __shfl_xor(l[i], 32);
-        if (g == 0) lds.ml[wave][16 * i + n] = make_float2(m[i], l[i]);
-    }
-    __syncthreads();
-    const int row = threadIdx.x >> 4, part = threadIdx.x & 15;  // 16 threads to a row
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-        float top = kNone, sum = 0.0f;
-        float2 w[kAttnWaves];
-#pragma unroll
-        for (int x = 0; x < kAttnWaves; ++x) {
-            w[x] = lds.ml[x][16 * i + n];
-            top = fmaxf(top, w[x].x);
-        }
-#pragma unroll
-        for (int x = 0; x < kAttnWaves; ++x)
-            if (w[x].x != kNone) sum += w[x].y * __builtin_amdgcn_exp2f(w[x].x - top);
-        const float f = m[i] == kNone ? 0.0f : __builtin_amdgcn_exp2f(m[i] - top);
-        if (threadIdx.x < 16 && s.row0 + 16 * i + n < s.n_rows) s.pml[16 * i + n] = make_float2(top, sum);
+        const int row = 16 * i + n;
+        if (s.row0 + row >= s.n_rows) continue;
+        if (g == 0) s.pml[row] = make_float2(m[i], l[i]);
+        float *po = s.po + row * DP;
 #pragma unroll
         for (int h = 0; h < NH; ++h)
 #pragma unroll
@@ -285,20 +291,9 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s, Att
                 for (int c = 0; c < EL; c += 4) {
                     f32x4 x;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] = o[i][h * EL + c + e][r] * f;
-                    *reinterpret_cast<f32x4 *>(&lds.o[wave][n][16 * EL * h + EL * (4 * g + r) + c]) = x;
+                    for (int e = 0; e < 4; ++e) x[e] = o[i][h * EL + c + e][r];
+                    *reinterpret_cast<f32x4 *>(po + 16 * EL * h + EL * (4 * g + r) + c) = x;
                 }
-        __syncthreads();
-        if (s.row0 + 16 * i + row < s.n_rows) {
-#pragma unroll
-            for (int d = 4 * part; d < DP; d += 64) {
-                f32x4 x = *reinterpret_cast<const f32x4 *>(&lds.o[0][row][d]);
-#pragma unroll
-                for (int y = 1; y < kAttnWaves; ++y) x += *reinterpret_cast<const f32x4 *>(&lds.o[y][row][d]);
-                *reinterpret_cast<f32x4 *>(s.po + (int64_t)(16 * i + row) * DP + d) = x;
-            }
-        }
-        __syncthreads();
     }
 }
 
@@ -323,6 +318,8 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
 constexpr int kWideTile = 64;
+// Costs for the dealing, in steps of one suffix wave: a tile of the prefix, and what an item costs beyond its steps.
+constexpr float kWideCost64 = 0.6f, kWideCost128 = 0.8f, kItemCost = 4.0f;
 
 template <class T>
 __device__ __forceinline__ f32x16 mma32(u32v4 a, u32v4 b, f32x16 c);
@@ -335,16 +332,17 @@ __device__ __forceinline__ f32x16 mma32<_Float16>(u32v4 a, u32v4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// 16 bytes a lane from memory to LDS at `dst` (the same in all lanes) + 16 * lane. Waited for by vmcnt.
+// 16 bytes a lane from `base` (the same in all lanes) + offset to LDS at `dst` (the same) + 16 * lane. Waited for
+// by vmcnt.
 // Written as one asm block (m0, which holds the LDS address, is put back) because the compiler makes every later
 // LDS read wait for loads to LDS that it knows of, whatever part of LDS they write; the block writes no register.
-__device__ __forceinline__ void load_to_lds(void *dst, const void *src) {
+__device__ __forceinline__ void load_to_lds(void *dst, const void *base, uint32_t offset) {
     const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(size_t)(lds_u8 *)dst);
     uint32_t keep;
     asm volatile(
-        "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off\n\ts_mov_b32 m0, %0"
+        "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
         : "=&s"(keep)
-        : "s"(at), "v"(src)
+        : "s"(at), "v"(offset), "s"(base)
         : "memory");
 }
 __device__ __forceinline__ void wait_loads_to_lds() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
@@ -389,11 +387,15 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
     const T *kbase = static_cast<const T *>(a.k) + (int64_t)s.head * a.k_hs;
     const T *vbase = static_cast<const T *>(a.v) + (int64_t)s.head * a.v_hs;
 
-    auto page_of = [&](int pos) -> int {
-        if (pos >= s.len) return -1;
-        const int id = s.pages[pos >> a.page_log2];
-        return (uint32_t)id < (uint32_t)a.n_pages ? id : -1;
-    };
+    AttnPages list;
+    // byte offsets of this lane's chunks within its wave's sixteen rows
+    uint32_t ks[16 / RPI], vs[16 / RPI];
+#pragma unroll
+    for (int i = 0; i < 16 / RPI; ++i) {
+        const int r = RPI * i + lane / CPR;
+        ks[i] = 2 * (r * a.k_rs + 8 * ((lane % CPR) ^ key_of_k<DP>(r)));
+        vs[i] = 2 * (r * a.v_rs + 8 * ((lane % CPR) ^ key_of_v<DP>(r)));
+    }
     // This wave's 16 positions of the tile at `pos0`; hidden positions and elements past head_dim are zeros
     // (a zero weight times whatever memory holds there would not be).
     auto issue = [&](int buf, int pos0, int id) {
@@ -403,10 +405,8 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
         if (id >= 0 && first + 16 <= s.len && D == DP) {
 #pragma unroll
             for (int i = 0; i < 16 / RPI; ++i) {
-                const int r = RPI * i + lane / CPR;
-                const int ck = (lane % CPR) ^ key_of_k<DP>(r), cv = (lane % CPR) ^ key_of_v<DP>(r);
-                load_to_lds(&lds.k[buf][(16 * wave + RPI * i) * ROW], kp + r * a.k_rs + 8 * ck);
-                load_to_lds(&lds.v[buf][(16 * wave + RPI * i) * ROW], vp + r * a.v_rs + 8 * cv);
+                load_to_lds(&lds.k[buf][(16 * wave + RPI * i) * ROW], kp, ks[i]);
+                load_to_lds(&lds.v[buf][(16 * wave + RPI * i) * ROW], vp, vs[i]);
             }
             return;
         }
@@ -417,11 +417,11 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
             const int ck = (lane % CPR) ^ key_of_k<DP>(r), cv = (lane % CPR) ^ key_of_v<DP>(r);
             uint8_t *dk = &lds.k[buf][(16 * wave + RPI * i) * ROW], *dv = &lds.v[buf][(16 * wave + RPI * i) * ROW];
             if (in && 8 * ck < D)
-                load_to_lds(dk, kp + r * a.k_rs + 8 * ck);
+                load_to_lds(dk, kp, ks[i]);
             else
                 *reinterpret_cast<u32v4 *>(dk + 16 * lane) = u32v4{0, 0, 0, 0};
             if (in && 8 * cv < D)
-                load_to_lds(dv, vp + r * a.v_rs + 8 * cv);
+                load_to_lds(dv, vp, vs[i]);
             else
                 *reinterpret_cast<u32v4 *>(dv + 16 * lane) = u32v4{0, 0, 0, 0};
         }
@@ -445,24 +445,19 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
     for (int c = 0; c < DB; ++c) o[c] = f32x16{};
     float m = kNone, l = 0.0f;
 
-    int pos0 = s.u0 * kAttnUnit, buf = 0;
-    const int end = min(s.len, s.u1 * kAttnUnit);
-    int id[kAttnWaves];
-#pragma unroll
-    for (int x = 0; x < kAttnWaves; ++x) id[x] = page_of(pos0 + 16 * x);
-    issue(0, pos0, wave == 0 ? id[0] : wave == 1 ? id[1] : wave == 2 ? id[2] : id[3]);
+    int pos0 = s.pos0, buf = 0;
+    const int end = min(s.len, s.pos1);
+    list.start(a, s, pos0);
+    issue(0, pos0, list.of(a, s, (pos0 >> 4) + wave));
     while (pos0 < end) {
-        const bool hidden = (id[0] | id[1] | id[2] | id[3]) < 0 || pos0 + kWideTile > s.len;
-        uint32_t pages = 0;  // bit x: positions 16 x .. 16 x + 15 of this tile are a page's
+        uint32_t seen = 0;  // bit x: positions 16 x .. 16 x + 15 of this tile are a page's
 #pragma unroll
-        for (int x = 0; x < kAttnWaves; ++x) {
-            pages |= id[x] >= 0 ? 1u << x : 0u;
-            id[x] = page_of(pos0 + kWideTile + 16 * x);
-        }
+        for (int x = 0; x < kAttnWaves; ++x) seen |= list.of(a, s, (pos0 >> 4) + x) >= 0 ? 1u << x : 0u;
+        const bool hidden = seen != 15 || pos0 + kWideTile > s.len;
         wait_loads_to_lds();
         __syncthreads();  // this tile is there, and nobody reads the one before it any more
         if (pos0 + kWideTile < end)
-            issue(buf ^ 1, pos0 + kWideTile, wave == 0 ? id[0] : wave == 1 ? id[1] : wave == 2 ? id[2] : id[3]);
+            issue(buf ^ 1, pos0 + kWideTile, list.of(a, s, (pos0 + kWideTile) / 16 + wave));
 
         // Operands are read from LDS a group of products ahead: the reads of group x + 1 run under the products
         // of group x (the scheduling barriers keep the compiler from sinking each read to its use).
@@ -505,38 +500,47 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int at = 32 * (part * NB + b) + 8 * (r >> 2) + 4 * g + (r & 3);
-                    if (pos0 + at >= s.len || !((pages >> (at >> 4)) & 1)) sc[b][r] = kNone;
+                    if (pos0 + at >= s.len || !((seen >> (at >> 4)) & 1)) sc[b][r] = kNone;
                 }
         }
-        float top = kNone;
+        f32x8 w[NB][2];
+        float sum = 0.0f;
+        const auto weigh = [&](float shift) {
+            float part_sum[2 * NB];
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+            for (int x = 0; x < 2 * NB; ++x) {
+                part_sum[x] = 0.0f;
 #pragma unroll
-            for (int r = 0; r < 16; r += 2) top = fmaxf(top, fmaxf(sc[b][r], sc[b][r + 1]));
-        top *= a.scale_log2;
-        if (__any(top > m + 8.0f)) {  // as above: the shift is raised only by more than 2^8
-            top = fmaxf(top, __shfl_xor(top, 32));
+                for (int r = 0; r < 8; ++r) {
+                    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[x >> 1][8 * (x & 1) + r], a.scale_log2, -shift));
+                    w[x >> 1][x & 1][r] = e;
+                    part_sum[x] += e;
+                }
+            }
+            sum = part_sum[0] + part_sum[1];
+            if constexpr (NB == 2) sum += part_sum[2] + part_sum[3];
+        };
+        weigh(m);
+        if (__any(!(sum < kShiftLimit))) {  // as in the register path
+            float top = kNone;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[b][r]);
+            top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
             const float up = fmaxf(m, top);
             const float f = up == m ? 1.0f : __builtin_amdgcn_exp2f(m - up);
             m = up;
             l *= f;
 #pragma unroll
             for (int c = 0; c < DB; ++c) o[c] *= f;
+            weigh(up == kNone ? 0.0f : up);
         }
-        const float shift = m == kNone ? 0.0f : m;
+        l += sum;
         u32v4 p[NB][2];
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                f32x8 w;
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][8 * h + r], a.scale_log2, -shift));
-                    l += w[r];
-                }
-                p[b][h] = __builtin_bit_cast(u32v4, __builtin_convertvector(w, typename Vec8<T>::type));
-            }
+        for (int x = 0; x < 2 * NB; ++x)
+            p[x >> 1][x & 1] = __builtin_bit_cast(u32v4, __builtin_convertvector(w[x >> 1][x & 1], typename Vec8<T>::type));
 #pragma unroll
         for (int x = 0; x < 2 * NB; ++x) {
             if (x + 1 < 2 * NB) read_v(x + 1, vf[(x + 1) & 1]);
@@ -603,17 +607,24 @@ __device__ __forceinline__ int2 seq_tokens(const AttnArgs &a, int b) {
 }
 __device__ __forceinline__ int seq_len(const AttnArgs &a, int b) { return min(max(a.lens[b], 0), a.cap); }
 
-// MP, MS: query rows of a tile in the prefix (16, 32: from registers; 64, 128: through LDS) and in a
-// suffix (16, 32).
+// What the workgroups know of the sequences, in LDS: [n_seqs + 1] units and items before each, then first token,
+// tokens and length of each.
+struct AttnSeqs {
+    int32_t *units, *items, *tok0, *n_tok, *len;
+    __device__ __forceinline__ AttnSeqs(int32_t *p, int n)
+        : units(p), items(p + n + 1), tok0(p + 2 * (n + 1)), n_tok(p + 3 * (n + 1)), len(p + 4 * (n + 1)) {}
+};
+
+// MP, MS: query rows of a tile in the prefix (16, 32: a wave's, from registers; 64, 128: a workgroup's, through
+// LDS) and in a suffix (16, 32: a wave's).
 template <class T, int DP, int MP, int MS>
 __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_kernel(AttnArgs a) {
     constexpr bool WIDE = MP > 32;
-    constexpr size_t LDS = WIDE && sizeof(WideLds<DP>) > sizeof(AttnLds<DP>) ? sizeof(WideLds<DP>) : sizeof(AttnLds<DP>);
-    __shared__ alignas(16) uint8_t lds[LDS];
-    __shared__ int32_t units[kAttnMaxSeqs + 1], items[kAttnMaxSeqs + 1];
+    constexpr int UNIT_P = WIDE ? kWideTile : kAttnStep;
+    extern __shared__ int32_t dynamic[];
     __shared__ int32_t wave_sum[kAttnWaves][2];
-    __shared__ int32_t first_seq;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    AttnSeqs seqs(dynamic, a.n_seqs);
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     // Units and items (head x tile) before each sequence: four sequences a thread, then a scan.
     int un[4], it[4], su = 0, si = 0;
@@ -622,10 +633,13 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_ke
         const int b = 4 * tid + x;
         un[x] = it[x] = 0;
         if (b < a.n_seqs) {
-            const int n = seq_tokens(a, b).y;
-            const int u = (seq_len(a, b) + kAttnUnit - 1) / kAttnUnit;
-            it[x] = u > 0 ? a.kv_heads * ((n * a.group + MS - 1) / MS) : 0;
+            const int2 tok = seq_tokens(a, b);
+            const int len = seq_len(a, b), u = (len + kAttnStep - 1) / kAttnStep;
+            it[x] = u > 0 ? a.kv_heads * ((tok.y * a.group + MS - 1) / MS) : 0;
             un[x] = it[x] * u;
+            seqs.tok0[b] = tok.x;
+            seqs.n_tok[b] = tok.y;
+            seqs.len[b] = len;
         }
         su += un[x];
         si += it[x];
@@ -637,55 +651,65 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_ke
         if (lane >= d) iu += x, ii += y;
     }
     if (lane == 63) wave_sum[wave][0] = iu, wave_sum[wave][1] = ii;
-    if (tid == 0) first_seq = 0;
     __syncthreads();
-    int total_s = 0;
+    int total_s = 0, items_s = 0;
 #pragma unroll
     for (int x = 0; x < kAttnWaves; ++x) {
         if (x < wave) iu += wave_sum[x][0], ii += wave_sum[x][1];
         total_s += wave_sum[x][0];
+        items_s += wave_sum[x][1];
     }
+    total_s = __builtin_amdgcn_readfirstlane(total_s);
+    items_s = __builtin_amdgcn_readfirstlane(items_s);
     int eu = iu - su, ei = ii - si;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
         const int b = 4 * tid + x;
-        if (b < a.n_seqs) units[b] = eu, items[b] = ei;
+        if (b < a.n_seqs) seqs.units[b] = eu, seqs.items[b] = ei;
         eu += un[x], ei += it[x];
-        if (b == a.n_seqs - 1) units[a.n_seqs] = eu, items[a.n_seqs] = ei;
+        if (b == a.n_seqs - 1) seqs.units[a.n_seqs] = eu, seqs.items[a.n_seqs] = ei;
     }
-    // Equal shares by the cost of a unit.
-    constexpr int COST_P = MP <= 32 ? 2 : MP == 64 ? 3 : 4, COST_S = 2;
-    const int up = (a.prefix_len + kAttnUnit - 1) / kAttnUnit, total_p = a.kv_heads * a.tiles_p * up;
-    int qp = 1, qs = 1, wp = total_p, ws = total_s;
-    if (wp + ws > a.n_wgs) {
-        int share = (int)(((int64_t)total_p * COST_P + (int64_t)total_s * COST_S + a.n_wgs - 1) / a.n_wgs);
-        do {
-            qp = max(1, share / COST_P);
-            qs = max(1, share / COST_S);
+
+    // Equal shares. qp, qs: units of one run; wp, ws: runs. Runs of a suffix are a wave's, runs of the prefix a
+    // workgroup's where WIDE. Costs are in steps of one wave.
+    const int up = (a.prefix_len + UNIT_P - 1) / UNIT_P, total_p = a.kv_heads * a.tiles_p * up;
+    int qp, qs, wp, ws;
+    if constexpr (WIDE) {
+        const float cost_s = total_s > 0 ? 1.0f + kItemCost * (float)items_s / (float)total_s : 1.0f;
+        const float cost_p = MP == 64 ? kWideCost64 : kWideCost128;
+        float share = ((float)total_p * cost_p + 0.25f * (float)total_s * cost_s) / (float)a.n_wgs;
+        while (true) {
+            qp = max(1, (int)(share / cost_p));
+            qs = max(1, (int)(share / cost_s));
             wp = (total_p + qp - 1) / qp;
             ws = (total_s + qs - 1) / qs;
-            share += 1 + share / 16;
-        } while (wp + ws > a.n_wgs);
+            if (wp + (ws + 3) / 4 <= a.n_wgs) break;
+            share = share * 1.03f + 1.0f;
+        }
+    } else {
+        qp = qs = max(1, (total_p + total_s + 4 * a.n_wgs - 1) / (4 * a.n_wgs));
+        while (true) {
+            wp = (total_p + qp - 1) / qp;
+            ws = (total_s + qs - 1) / qs;
+            if (wp + ws <= 4 * a.n_wgs) break;
+            qp = ++qs;
+        }
     }
     __syncthreads();
     if (blockIdx.x == 0) {  // what the join needs
         if (tid == 0) a.sched[0] = up, a.sched[1] = qp, a.sched[2] = qs;
         for (int b = tid; b <= a.n_seqs; b += kAttnThreads) {
-            a.sched[kSchedHead + b] = units[b];
-            a.sched[kSchedHead + a.n_seqs + 1 + b] = items[b];
+            a.sched[kSchedHead + b] = seqs.units[b];
+            a.sched[kSchedHead + a.n_seqs + 1 + b] = seqs.items[b];
         }
     }
-    // Workgroup b runs on XCD b % 8: neighbours in the dealing, which read the same keys for other rows,
-    // share one XCD's L2.
-    int w = blockIdx.x;
-    const int per = gridDim.x >> 3;
-    if (w < 8 * per) w = (w & 7) * per + (w >> 3);
     AttnSpan s;
-    if (w < wp) {
+    // Run w of the prefix.
+    const auto prefix = [&](int w, auto &&work) {
         int u = w * qp;
         const int stop = min(total_p, u + qp);
         while (u < stop) {
-            const int item = u / up, at = u - item * up;
+            const int item = u / up, at = u - item * up, n = min(up - at, stop - u);
             s.pages = a.prefix_pages;
             s.len = a.prefix_len;
             s.tok0 = 0;
@@ -694,145 +718,230 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_ke
             s.head = item / a.tiles_p;
             s.row0 = (item - s.head * a.tiles_p) * MP;
             s.n_rows = a.n_tokens * a.group;
-            s.u0 = at;
-            s.u1 = min(up, at + stop - u);
+            s.pos0 = at * UNIT_P;
+            s.pos1 = (at + n) * UNIT_P;
             s.po = a.part_o + (int64_t)(item + w) * (MP * DP);
             s.pml = a.part_ml + (int64_t)(item + w) * MP;
-            if constexpr (WIDE)
-                attend_wide<T, DP, MP / 32>(a, s, reinterpret_cast<WideLds<DP> &>(lds));
-            else
-                attend<T, MP / 16, DP>(a, s, reinterpret_cast<AttnLds<DP> &>(lds));
-            u += s.u1 - s.u0;
+            work();
+            u += n;
         }
-        return;
+    };
+    // Runs are spread over the workgroups first, so that few of them use many CUs.
+    int w = wave * gridDim.x + blockIdx.x;
+    if constexpr (WIDE) {
+        // Workgroup b runs on XCD b % 8: neighbours in the dealing, which read the same keys for other rows,
+        // share one XCD's L2.
+        int x = blockIdx.x;
+        const int per = gridDim.x >> 3;
+        if (x < 8 * per) x = (x & 7) * per + (x >> 3);
+        if (x < wp) {
+            __shared__ WideLds<DP> lds;
+            prefix(x, [&] { attend_wide<T, DP, MP / 32>(a, s, lds); });
+            return;
+        }
+        w = wave * (gridDim.x - wp) + x - wp;
+    } else {
+        if (w < wp) {
+            prefix(w, [&] { attend<T, MP / 16, DP>(a, s); });
+            return;
+        }
+        w -= wp;
     }
-    w -= wp;
     if (w >= ws) return;
     int u = w * qs;
     const int stop = min(total_s, u + qs);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {  // the sequence that holds unit u
-        const int b = 4 * tid + x;
-        if (b < a.n_seqs && units[b] <= u && u < units[b + 1]) first_seq = b;
+    int b = 0;  // the sequence that holds unit u: one lane finds it (the wave's own search: no barrier from here on)
+    {
+        int found = -1;
+        for (int i = lane; i < a.n_seqs; i += 64)
+            if (seqs.units[i] <= u && u < seqs.units[i + 1]) found = i;
+        b = __builtin_amdgcn_readlane(found, __builtin_ctzll(__ballot(found >= 0)));
     }
-    __syncthreads();
-    int b = __builtin_amdgcn_readfirstlane(first_seq);
     while (u < stop) {
-        while (units[b + 1] <= u) ++b;  // past idle sequences
+        while (seqs.units[b + 1] <= u) ++b;  // past idle sequences
         b = __builtin_amdgcn_readfirstlane(b);
-        const int2 tok = seq_tokens(a, b);
-        const int len = seq_len(a, b), ub = (len + kAttnUnit - 1) / kAttnUnit;
-        const int tiles = (tok.y * a.group + MS - 1) / MS;
-        const int rest = u - __builtin_amdgcn_readfirstlane(units[b]);
-        const int item = rest / ub, at = rest - item * ub;
-        const int64_t piece = __builtin_amdgcn_readfirstlane(items[b]) + item + w;
+        const int len = __builtin_amdgcn_readfirstlane(seqs.len[b]), ub = (len + kAttnStep - 1) / kAttnStep;
+        const int n_tok = __builtin_amdgcn_readfirstlane(seqs.n_tok[b]), tiles = (n_tok * a.group + MS - 1) / MS;
+        const int rest = u - __builtin_amdgcn_readfirstlane(seqs.units[b]);
+        const int item = rest / ub, at = rest - item * ub, n = min(ub - at, stop - u);
+        const int64_t piece = __builtin_amdgcn_readfirstlane(seqs.items[b]) + item + w;
         s.pages = a.table + (int64_t)b * a.table_stride;
         s.len = len;
-        s.tok0 = tok.x;
-        s.n_tok = tok.y;
+        s.tok0 = __builtin_amdgcn_readfirstlane(seqs.tok0[b]);
+        s.n_tok = n_tok;
         s.causal = 1;
         s.head = item / tiles;
         s.row0 = (item - s.head * tiles) * MS;
-        s.n_rows = tok.y * a.group;
-        s.u0 = at;
-        s.u1 = min(ub, at + stop - u);
+        s.n_rows = n_tok * a.group;
+        s.pos0 = at * kAttnStep;
+        s.pos1 = (at + n) * kAttnStep;
         s.po = a.part_o + a.part_s + piece * (MS * DP);
         s.pml = a.part_ml + a.ml_s + piece * MS;
-        attend<T, MS / 16, DP>(a, s, reinterpret_cast<AttnLds<DP> &>(lds));
-        u += s.u1 - s.u0;
+        attend<T, MS / 16, DP>(a, s);
+        u += n;
     }
 }
 
-// Joins the parts of one query row: one workgroup to a (sequence, query token, query head). The weights of the
-// parts are formed once in LDS; then DP / 4 threads hold a row, so that several parts are in flight.
+// The parts of one query row: np of the prefix, then ns of its sequence.
+struct AttnParts {
+    int np, ns;
+    int t;                    // token, or -1: none
+    int64_t row_p, row_s;     // first part's row among all rows of parts
+    int mp, ms;
+
+    __device__ __forceinline__ AttnParts(const AttnArgs &a, int mp_, int ms_, int b, int j, int hq) : mp(mp_), ms(ms_) {
+        const int2 tok = seq_tokens(a, b);
+        const int up = a.sched[0], qp = a.sched[1], qs = a.sched[2];
+        const int before_u = a.sched[kSchedHead + b], before_i = a.sched[kSchedHead + a.n_seqs + 1 + b];
+        const int ub = (seq_len(a, b) + kAttnStep - 1) / kAttnStep;
+        const int head = hq / a.group, gi = hq - head * a.group;
+        np = ns = 0;
+        row_p = row_s = 0;
+        t = j < tok.y ? tok.x + j : -1;
+        if (t < 0) return;
+        if (up > 0) {
+            const int row = t * a.group + gi, tile = row / mp, item = head * a.tiles_p + tile;
+            const int w0 = item * up / qp;
+            np = (item * up + up - 1) / qp - w0 + 1;
+            row_p = (int64_t)(item + w0) * mp + row - tile * mp;
+        }
+        if (ub > 0) {
+            const int row = j * a.group + gi, tile = row / ms, item = head * ((tok.y * a.group + ms - 1) / ms) + tile;
+            const int u0 = before_u + item * ub, w0 = u0 / qs;
+            ns = (u0 + ub - 1) / qs - w0 + 1;
+            row_s = (int64_t)(before_i + item + w0) * ms + row - tile * ms;
+        }
+    }
+    __device__ __forceinline__ float2 ml(const AttnArgs &a, int k) const {
+        return k < np ? a.part_ml[row_p + (int64_t)k * mp] : a.part_ml[a.ml_s + row_s + (int64_t)(k - np) * ms];
+    }
+    template <int DP>
+    __device__ __forceinline__ const float *o(const AttnArgs &a, int k) const {
+        return k < np ? a.part_o + (row_p + (int64_t)k * mp) * DP : a.part_o + a.part_s + (row_s + (int64_t)(k - np) * ms) * DP;
+    }
+};
+
+// Four elements of a row of out, its lse. top: log2 units. A sum of zero: nothing seen. (NaN is not zero.)
+template <class T>
+__device__ __forceinline__ void write_out(const AttnArgs &a, int t, int hq, int d, f32x4 acc, float top, float sum) {
+    if (d < a.head_dim) {
+        typedef T T4 __attribute__((ext_vector_type(4)));
+        T *out = static_cast<T *>(a.out) + (int64_t)t * a.o_ts + (int64_t)hq * a.o_hs + d;
+        *reinterpret_cast<T4 *>(out) = __builtin_convertvector(acc * (sum == 0.0f ? 0.0f : 1.0f / sum), T4);
+    }
+    if (d == 0 && a.lse)
+        a.lse[(int64_t)t * a.q_heads + hq] = sum == 0.0f ? kNone : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) x = fmaxf(x, __shfl_xor(x, d));
+    return x;
+}
+__device__ __forceinline__ float wave_add(float x) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
+    return x;
+}
+
+constexpr int kJoinRows = 1024;
+
+// Joins the parts of a query row, few rows: one workgroup to a (sequence, query token, query head). The weights
+// of the parts are formed once in LDS; then DP / 4 threads hold a row, so that many parts are in flight.
 template <class T, int DP>
 __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int mp, int ms) {
     constexpr int LANES = DP / 4, GROUPS = kAttnThreads / LANES;
-    __shared__ float weight[2 * kAttnMaxWgs + 2];
+    __shared__ float weight[kAttnWaves * kAttnWgs + 2];
     __shared__ f32x4 sums[GROUPS][LANES];
-    __shared__ float red[kAttnWaves];
+    __shared__ float red[2][kAttnWaves];
     const int tid = threadIdx.x;
-    const int hq = blockIdx.x % a.q_heads, bj = blockIdx.x / a.q_heads, j = bj % a.max_q, b = bj / a.max_q;
-    const int2 tok = seq_tokens(a, b);
-    if (j >= tok.y) return;
-    const int t = tok.x + j, head = hq / a.group, gi = hq - head * a.group;
-    const int up = a.sched[0], qp = a.sched[1], qs = a.sched[2];
-    int np = 0, ns = 0;
-    int64_t first_p = 0, first_s = 0;  // pieces
-    int row_p = 0, row_s = 0;
-    if (up > 0) {
-        const int row = t * a.group + gi, tile = row / mp, item = head * a.tiles_p + tile;
-        const int w0 = item * up / qp, w1 = (item * up + up - 1) / qp;
-        np = w1 - w0 + 1;
-        first_p = item + w0;
-        row_p = row - tile * mp;
-    }
-    const int ub = (seq_len(a, b) + kAttnUnit - 1) / kAttnUnit;
-    if (ub > 0) {
-        const int tiles = (tok.y * a.group + ms - 1) / ms;
-        const int row = j * a.group + gi, tile = row / ms, item = head * tiles + tile;
-        const int u0 = a.sched[kSchedHead + b] + item * ub;
-        const int w0 = u0 / qs, w1 = (u0 + ub - 1) / qs;
-        ns = w1 - w0 + 1;
-        first_s = a.sched[kSchedHead + a.n_seqs + 1 + b] + item + w0;
-        row_s = row - tile * ms;
-    }
-    auto ml_of = [&](int k) -> float2 {
-        return k < np ? a.part_ml[(first_p + k) * mp + row_p] : a.part_ml[a.ml_s + (first_s + k - np) * ms + row_s];
-    };
-    const int parts = np + ns;
+    const int hq = blockIdx.x % a.q_heads, bj = blockIdx.x / a.q_heads;
+    const AttnParts p(a, mp, ms, bj / a.max_q, bj % a.max_q, hq);
+    if (p.t < 0) return;
+    const int parts = p.np + p.ns;
     float top = kNone;
-    for (int k = tid; k < parts; k += kAttnThreads) top = fmaxf(top, ml_of(k).x);
-#pragma unroll
-    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-    if ((tid & 63) == 0) red[tid >> 6] = top;
+    for (int k = tid; k < parts; k += kAttnThreads) top = fmaxf(top, p.ml(a, k).x);
+    top = wave_max(top);
+    if ((tid & 63) == 0) red[0][tid >> 6] = top;
     __syncthreads();
-    top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    __syncthreads();
+    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
     float sum = 0.0f;
     for (int k = tid; k < parts; k += kAttnThreads) {
-        const float2 x = ml_of(k);
+        const float2 x = p.ml(a, k);
         const float f = x.x == kNone ? 0.0f : __builtin_amdgcn_exp2f(x.x - top);
         weight[k] = f;
         sum += x.x == kNone ? 0.0f : f * x.y;
     }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
-    if ((tid & 63) == 0) red[tid >> 6] = sum;
+    sum = wave_add(sum);
+    if ((tid & 63) == 0) red[1][tid >> 6] = sum;
     __syncthreads();
-    sum = (red[0] + red[1]) + (red[2] + red[3]);
+    sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
     const int gr = tid / LANES, ln = tid - gr * LANES;
     f32x4 acc = {0, 0, 0, 0};
 #pragma unroll 4
-    for (int k = gr; k < parts; k += GROUPS) {
-        const float *p = k < np ? a.part_o + ((first_p + k) * mp + row_p) * DP
-                                : a.part_o + a.part_s + ((first_s + k - np) * ms + row_s) * DP;
-        const float f = weight[k];
-        const f32x4 x = *reinterpret_cast<const f32x4 *>(p + 4 * ln);
-        acc += x * f;
-    }
+    for (int k = gr; k < parts; k += GROUPS) acc += *reinterpret_cast<const f32x4 *>(p.template o<DP>(a, k) + 4 * ln) * weight[k];
     sums[gr][ln] = acc;
     __syncthreads();
-    if (gr == 0 && 4 * ln < a.head_dim) {
+    if (gr) return;
 #pragma unroll
-        for (int y = 1; y < GROUPS; ++y) acc += sums[y][ln];
-        // nothing seen: zeros. (A NaN sum is not equal to zero and goes through.)
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        T *out = static_cast<T *>(a.out) + (int64_t)t * a.o_ts + (int64_t)hq * a.o_hs + 4 * ln;
-        typedef T T4 __attribute__((ext_vector_type(4)));
-        *reinterpret_cast<T4 *>(out) = __builtin_convertvector(acc * inv, T4);
+    for (int y = 1; y < GROUPS; ++y) acc += sums[y][ln];
+    write_out<T>(a, p.t, hq, 4 * ln, acc, top, sum);
+}
+
+// Many rows, which have few parts each: one wave to a row, no barriers.
+template <class T, int DP>
+__global__ __launch_bounds__(kAttnThreads) void attn_join_rows_kernel(AttnArgs a, int mp, int ms, int rows) {
+    constexpr int LANES = DP / 4, GROUPS = 64 / LANES;
+    const int lane = threadIdx.x & 63;
+    const int r = __builtin_amdgcn_readfirstlane(blockIdx.x * kAttnWaves + (threadIdx.x >> 6));
+    if (r >= rows) return;
+    const int hq = r % a.q_heads, bj = r / a.q_heads;
+    const AttnParts p(a, mp, ms, bj / a.max_q, bj % a.max_q, hq);
+    if (p.t < 0) return;
+    const int parts = p.np + p.ns;
+    float top = kNone;
+    for (int k = lane; k < parts; k += 64) top = fmaxf(top, p.ml(a, k).x);
+    top = wave_max(top);
+    const int gr = lane / LANES, ln = lane - gr * LANES;
+    f32x4 acc = {0, 0, 0, 0};
+    float sum = 0.0f;
+    for (int k0 = 0; k0 < parts; k0 += 64) {
+        const float2 x = k0 + lane < parts ? p.ml(a, k0 + lane) : make_float2(kNone, 0.0f);
+        const float f = x.x == kNone ? 0.0f : __builtin_amdgcn_exp2f(x.x - top);
+        sum += x.x == kNone ? 0.0f : f * x.y;
+        const int n = min(64, parts - k0);
+        for (int k = 0; k < n; k += 4 * GROUPS) {  // four loads of each lane in flight
+            f32x4 y[4];
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = k + i * GROUPS + gr, mine = min(at, n - 1);
+                y[i] = *reinterpret_cast<const f32x4 *>(p.template o<DP>(a, k0 + mine) + 4 * ln);
+                w[i] = __shfl(f, mine);
+                if (at >= n) w[i] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc += y[i] * w[i];
+        }
     }
-    if (tid == 0 && a.lse)
-        a.lse[(int64_t)t * a.q_heads + hq] =
-            sum == 0.0f ? kNone : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+    sum = wave_add(sum);
+#pragma unroll
+    for (int d = LANES; d < 64; d <<= 1)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor(acc[e], d);
+    if (gr == 0) write_out<T>(a, p.t, hq, 4 * ln, acc, top, sum);
 }
 
 template <class T, int DP, int MP, int MS>
 static int run_attn(const AttnArgs &a, hipStream_t st) {
-    attn_split_kernel<T, DP, MP, MS><<<(unsigned)a.n_wgs, kAttnThreads, 0, st>>>(a);
+    attn_split_kernel<T, DP, MP, MS><<<(unsigned)a.n_wgs, kAttnThreads, (size_t)(5 * (a.n_seqs + 1)) * 4, st>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
-    attn_join_kernel<T, DP><<<(unsigned)((int64_t)a.n_seqs * a.max_q * a.q_heads), kAttnThreads, 0, st>>>(a, MP, MS);
+    const int rows = a.n_seqs * a.max_q * a.q_heads;
+    if (rows >= kJoinRows)
+        attn_join_rows_kernel<T, DP><<<(unsigned)((rows + kAttnWaves - 1) / kAttnWaves), kAttnThreads, 0, st>>>(a, MP, MS, rows);
+    else
+        attn_join_kernel<T, DP><<<(unsigned)rows, kAttnThreads, 0, st>>>(a, MP, MS);
     return (int)hipGetLastError();
 }
 

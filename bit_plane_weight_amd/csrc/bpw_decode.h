@@ -43,10 +43,9 @@ int launch_heads(const HeadsArgs &a, int32_t dt_in, int32_t dt_out, bool vec, vo
 
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = 64 * kAttnWaves;
-constexpr int kAttnStep = 32;                      // positions one wave takes at a time
-constexpr int kAttnUnit = kAttnStep * kAttnWaves;  // positions of one unit of work
+constexpr int kAttnStep = 32;                      // positions a wave takes at a time: its unit of work
 constexpr int kAttnMaxSeqs = 1024;
-constexpr int kAttnMaxWgs = 1024;
+constexpr int kAttnWgs = 512;                      // most workgroups of a launch: two to each of 256 CUs
 
 struct AttnArgs {
     const void *q;
@@ -72,7 +71,7 @@ struct AttnArgs {
     int64_t part_s;          // offset (floats) of the suffix pieces in part_o
     int64_t ml_s;            // and in part_ml
 };
-constexpr int kSchedHead = 8;  // units per prefix item, prefix units per workgroup, suffix units per workgroup
+constexpr int kSchedHead = 8;  // units of a prefix item, units of a run of the prefix, of the suffixes
 
 int launch_attn_d64(const AttnArgs &a, int32_t dtype, int32_t mp, int32_t ms, void *stream);
 int launch_attn_d128(const AttnArgs &a, int32_t dtype, int32_t mp, int32_t ms, void *stream);

@@ -216,8 +216,6 @@ bpw_status bpw_kv_append(const bpw_kv_append_args *a, void *stream) {
 
 namespace {
 
-constexpr int32_t kWgs = 512;  // two workgroups for each of the 256 CUs
-
 struct AttnShape {
     int32_t dp, mp, ms;
     int32_t group, tiles_p;
@@ -258,17 +256,19 @@ bpw_status attn_shape(const bpw_attn_shared_prefix_args *a, AttnShape *s) {
     s->mp = a->prefix_len == 0 || rows_p <= s->ms ? s->ms : rows_p <= 32 ? 32 : rows_p <= 64 ? 64 : 128;
     const int64_t mp = s->mp, ms = s->ms;
     const int64_t tiles_p = (rows_p + mp - 1) / mp, tiles_s = (rows_s + ms - 1) / ms;
-    const int64_t up = (a->prefix_len + bpw::kAttnUnit - 1) / bpw::kAttnUnit;
-    const int64_t us = (s->cap + bpw::kAttnUnit - 1) / bpw::kAttnUnit;
+    const int64_t up = (a->prefix_len + bpw::kAttnStep - 1) / bpw::kAttnStep;
+    const int64_t us = (s->cap + bpw::kAttnStep - 1) / bpw::kAttnStep;
     const int64_t items_p = c.kv_heads * tiles_p, items_s = (int64_t)a->n_seqs * c.kv_heads * tiles_s;
     const double work = (double)items_p * (double)up + (double)items_s * (double)us;
     if (work >= 2.0e9 || (double)a->n_seqs * (double)max_q * a->q.heads >= 2.0e9)
         return fail(BPW_E_UNSUPPORTED, "%s: more work than one launch deals out", who);
     s->tiles_p = (int32_t)tiles_p;
     const int64_t most = items_p * up + items_s * us;
-    s->n_wgs = (int32_t)(most < 2 ? 2 : most < kWgs ? most : kWgs);
-    s->pieces_p = up > 0 ? items_p + s->n_wgs : 0;
-    s->pieces_s = us > 0 ? items_s + s->n_wgs : 0;
+    s->n_wgs = (int32_t)(most < 2 ? 2 : most < bpw::kAttnWgs ? most : bpw::kAttnWgs);
+    // one part per item and per run (a wave's, or a workgroup's where the prefix is wide)
+    const int64_t waves = (int64_t)bpw::kAttnWaves * s->n_wgs;
+    s->pieces_p = up > 0 ? items_p + (mp > 32 ? s->n_wgs : waves) : 0;
+    s->pieces_s = us > 0 ? items_s + waves : 0;
     s->sched = up256((size_t)(bpw::kSchedHead + 2 * (a->n_seqs + 1)) * 4);
     s->po = s->sched;
     const size_t rows = (size_t)(s->pieces_p * mp + s->pieces_s * ms);
