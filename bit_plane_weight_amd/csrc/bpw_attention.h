@@ -24,6 +24,8 @@
 // 964 MB over four sequences take 155 us so and 174 us without.
 #pragma once
 
+#include <type_traits>
+
 #include "bpw_decode.h"
 #include "bpw_elem.h"
 
@@ -62,28 +64,30 @@ constexpr float kShiftLimit = 1024.0f;  // float16 weights reach 65504
 // never straddles two): two runs of 64 granules, the second loaded while the first is in use, so that
 // no load of keys waits for a page number.
 struct AttnPages {
-    int32_t cur, next;  // page, or -1: past the end, or not a page of the cache
+    int32_t cur, next;  // as in the list; -1 past the end
     int32_t base;       // first granule of `cur`
 
     __device__ __forceinline__ int32_t fetch(const AttnArgs &a, const AttnSpan &s, int granule) const {
         const int pos = 16 * (granule + (int)(threadIdx.x & 63));
         int32_t id = -1;
         if (pos < s.len) id = s.pages[pos >> a.page_log2];
-        return (uint32_t)id < (uint32_t)a.n_pages ? id : -1;
+        return id;
     }
     __device__ __forceinline__ void start(const AttnArgs &a, const AttnSpan &s, int pos) {
         base = pos >> 4;
         cur = fetch(a, s, base);
         next = fetch(a, s, base + 64);
     }
-    // Page of granule `granule`, which is at most 64 past the last one asked for. The same in all lanes.
+    // Page of granule `granule`, which is at most 64 past the last one asked for, or -1: past the end, or not a
+    // page of the cache. The same in all lanes.
     __device__ __forceinline__ int32_t of(const AttnArgs &a, const AttnSpan &s, int granule) {
         if (granule >= base + 64) {
             base += 64;
             cur = next;
             next = fetch(a, s, base + 64);
         }
-        return __builtin_amdgcn_readlane(cur, granule - base);
+        const int32_t id = __builtin_amdgcn_readlane(cur, granule - base);
+        return (uint32_t)id < (uint32_t)a.n_pages ? id : -1;
     }
 };
 
@@ -317,9 +321,8 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
-constexpr int kWideTile = 64;
 // Costs for the dealing, in steps of one suffix wave: a tile of the prefix, and what an item costs beyond its steps.
-constexpr float kWideCost64 = 0.6f, kWideCost128 = 0.8f, kItemCost = 4.0f;
+constexpr float kWideCost64 = 0.8f, kWideCost128 = 1.0f, kItemCost = 4.0f;
 
 template <class T>
 __device__ __forceinline__ f32x16 mma32(u32v4 a, u32v4 b, f32x16 c);
@@ -332,18 +335,37 @@ __device__ __forceinline__ f32x16 mma32<_Float16>(u32v4 a, u32v4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// 16 bytes a lane from `base` (the same in all lanes) + offset to LDS at `dst` (the same) + 16 * lane. Waited for
-// by vmcnt.
-// Written as one asm block (m0, which holds the LDS address, is put back) because the compiler makes every later
-// LDS read wait for loads to LDS that it knows of, whatever part of LDS they write; the block writes no register.
-__device__ __forceinline__ void load_to_lds(void *dst, const void *base, uint32_t offset) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(size_t)(lds_u8 *)dst);
+// Loads straight to LDS: N times 16 bytes a lane, the i-th from `base` (the same in all lanes) + offset[i] to LDS at
+// `dst` (the same) + 1024 i + 16 * lane. Waited for by vmcnt. Written as asm (m0, which holds the LDS
+// address, is put back) because the compiler makes every later LDS read wait for loads to LDS that it knows
+// of, whatever part of LDS they write; the asm writes no register that a load fills. An instruction's
+// offset moves both of its addresses, so the i-th lane offset is given 1024 i less.
+template <int N>
+__device__ __forceinline__ void load_to_lds(uint32_t dst, const void *base, const uint32_t (&offset)[N]) {
     uint32_t keep;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
-        : "=&s"(keep)
-        : "s"(at), "v"(offset), "s"(base)
-        : "memory");
+    if constexpr (N == 4)
+        asm volatile(
+            "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+            "global_load_lds_dwordx4 %2, %6\n\tglobal_load_lds_dwordx4 %3, %6 offset:1024\n\t"
+            "global_load_lds_dwordx4 %4, %6 offset:2048\n\tglobal_load_lds_dwordx4 %5, %6 offset:3072\n\t"
+            "s_mov_b32 m0, %0"
+            : "=&s"(keep)
+            : "s"(dst), "v"(offset[0]), "v"(offset[1]), "v"(offset[2]), "v"(offset[3]), "s"(base)
+            : "memory");
+    else if constexpr (N == 2)
+        asm volatile(
+            "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+            "global_load_lds_dwordx4 %2, %4\n\tglobal_load_lds_dwordx4 %3, %4 offset:1024\n\t"
+            "s_mov_b32 m0, %0"
+            : "=&s"(keep)
+            : "s"(dst), "v"(offset[0]), "v"(offset[1]), "s"(base)
+            : "memory");
+    else
+        asm volatile(
+            "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
+            : "=&s"(keep)
+            : "s"(dst), "v"(offset[0]), "s"(base)
+            : "memory");
 }
 __device__ __forceinline__ void wait_loads_to_lds() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
@@ -387,44 +409,70 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
     const T *kbase = static_cast<const T *>(a.k) + (int64_t)s.head * a.k_hs;
     const T *vbase = static_cast<const T *>(a.v) + (int64_t)s.head * a.v_hs;
 
-    AttnPages list;
-    // byte offsets of this lane's chunks within its wave's sixteen rows
-    uint32_t ks[16 / RPI], vs[16 / RPI];
+    constexpr int LOADS = 16 / RPI, GROUP = LOADS < 4 ? LOADS : 4;  // loads of a wave's sixteen rows, of one asm block
+    const uint32_t lds_k = (uint32_t)(size_t)(lds_u8 *)lds.k, lds_v = (uint32_t)(size_t)(lds_u8 *)lds.v;
+    // byte offsets of this lane's chunks within its wave's sixteen rows (less 1024 for each place in its block)
+    uint32_t ks[LOADS], vs[LOADS];
 #pragma unroll
-    for (int i = 0; i < 16 / RPI; ++i) {
+    for (int i = 0; i < LOADS; ++i) {
         const int r = RPI * i + lane / CPR;
-        ks[i] = 2 * (r * a.k_rs + 8 * ((lane % CPR) ^ key_of_k<DP>(r)));
-        vs[i] = 2 * (r * a.v_rs + 8 * ((lane % CPR) ^ key_of_v<DP>(r)));
+        ks[i] = 2 * (r * a.k_rs + 8 * ((lane % CPR) ^ key_of_k<DP>(r))) - 1024 * (i % GROUP);
+        vs[i] = 2 * (r * a.v_rs + 8 * ((lane % CPR) ^ key_of_v<DP>(r))) - 1024 * (i % GROUP);
     }
-    // This wave's 16 positions of the tile at `pos0`; hidden positions and elements past head_dim are zeros
-    // (a zero weight times whatever memory holds there would not be).
-    auto issue = [&](int buf, int pos0, int id) {
-        const int first = pos0 + 16 * wave;
-        const T *kp = kbase + (int64_t)id * a.k_ps + (int64_t)(first & pmask) * a.k_rs;
-        const T *vp = vbase + (int64_t)id * a.v_ps + (int64_t)(first & pmask) * a.v_rs;
-        if (id >= 0 && first + 16 <= s.len && D == DP) {
+    // Pages, a granule of 16 positions a lane: the byte addresses of the granules of 16 tiles, and which of them are
+    // there; the page numbers of the 16 tiles after.
+    int32_t next;
+    uint64_t kat, vat, there;
+    const auto fetch = [&](int pos) {
+        const int at = pos + 16 * lane;
+        next = -1;
+        if (at < s.len) next = s.pages[at >> a.page_log2];
+    };
+    const auto turn_pages = [&](int pos) {
+        const bool in = (uint32_t)next < (uint32_t)a.n_pages;
+        const int64_t id = in ? next : 0;
+        const int64_t first = (pos + 16 * lane) & pmask;
+        kat = (uint64_t)(kbase + id * a.k_ps + first * a.k_rs);
+        vat = (uint64_t)(vbase + id * a.v_ps + first * a.v_rs);
+        there = __ballot(in);
+        fetch(pos + 1024);
+    };
+    const auto lane_of = [](uint64_t x, int l) {
+        return (const uint8_t *)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(x >> 32), l) << 32) |
+                                 (uint32_t)__builtin_amdgcn_readlane((uint32_t)x, l));
+    };
+    // Moves tile `pos` to LDS, this wave's 16 positions of it: hidden positions and elements past head_dim become
+    // zeros (a zero weight times whatever memory holds there would not be one). Gives which granules are there.
+    const auto issue = [&](int buf, int pos) -> uint32_t {
+        if (((pos - s.pos0) & 1023) == 0) turn_pages(pos);
+        const int tile = ((pos - s.pos0) >> 4) & 63, first = pos + 16 * wave;
+        const uint32_t seen = (uint32_t)(there >> tile) & 15;
+        const uint8_t *kp = lane_of(kat, tile + wave), *vp = lane_of(vat, tile + wave);
+        const uint32_t at = buf * (kWideTile * ROW) + 16 * wave * ROW;
+        if (seen == 15 && pos + kWideTile <= s.len && D == DP) {
 #pragma unroll
-            for (int i = 0; i < 16 / RPI; ++i) {
-                load_to_lds(&lds.k[buf][(16 * wave + RPI * i) * ROW], kp, ks[i]);
-                load_to_lds(&lds.v[buf][(16 * wave + RPI * i) * ROW], vp, vs[i]);
+            for (int i = 0; i < LOADS; i += GROUP) {
+                load_to_lds<GROUP>(lds_k + at + 1024 * i, kp, reinterpret_cast<const uint32_t(&)[GROUP]>(ks[i]));
+                load_to_lds<GROUP>(lds_v + at + 1024 * i, vp, reinterpret_cast<const uint32_t(&)[GROUP]>(vs[i]));
             }
-            return;
+            return seen;
         }
 #pragma unroll
-        for (int i = 0; i < 16 / RPI; ++i) {
+        for (int i = 0; i < LOADS; ++i) {
             const int r = RPI * i + lane / CPR;  // of the wave's sixteen
-            const bool in = id >= 0 && first + r < s.len;
+            const bool in = ((seen >> wave) & 1) && first + r < s.len;
             const int ck = (lane % CPR) ^ key_of_k<DP>(r), cv = (lane % CPR) ^ key_of_v<DP>(r);
-            uint8_t *dk = &lds.k[buf][(16 * wave + RPI * i) * ROW], *dv = &lds.v[buf][(16 * wave + RPI * i) * ROW];
+            const uint32_t ko[1] = {ks[i] + 1024 * (i % GROUP)}, vo[1] = {vs[i] + 1024 * (i % GROUP)};
             if (in && 8 * ck < D)
-                load_to_lds(dk, kp, ks[i]);
+                load_to_lds<1>(lds_k + at + 1024 * i, kp, ko);
             else
-                *reinterpret_cast<u32v4 *>(dk + 16 * lane) = u32v4{0, 0, 0, 0};
+                *reinterpret_cast<u32v4 *>(&lds.k[buf][16 * wave * ROW + 1024 * i + 16 * lane]) = u32v4{0, 0, 0, 0};
             if (in && 8 * cv < D)
-                load_to_lds(dv, vp, vs[i]);
+                load_to_lds<1>(lds_v + at + 1024 * i, vp, vo);
             else
-                *reinterpret_cast<u32v4 *>(dv + 16 * lane) = u32v4{0, 0, 0, 0};
+                *reinterpret_cast<u32v4 *>(&lds.v[buf][16 * wave * ROW + 1024 * i + 16 * lane]) = u32v4{0, 0, 0, 0};
         }
+        return seen;
     };
 
     // LDS addresses of this lane's reads; blocks of 32 (and 16) positions are whole keys apart
@@ -445,19 +493,18 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
     for (int c = 0; c < DB; ++c) o[c] = f32x16{};
     float m = kNone, l = 0.0f;
 
-    int pos0 = s.pos0, buf = 0;
     const int end = min(s.len, s.pos1);
-    list.start(a, s, pos0);
-    issue(0, pos0, list.of(a, s, (pos0 >> 4) + wave));
-    while (pos0 < end) {
-        uint32_t seen = 0;  // bit x: positions 16 x .. 16 x + 15 of this tile are a page's
-#pragma unroll
-        for (int x = 0; x < kAttnWaves; ++x) seen |= list.of(a, s, (pos0 >> 4) + x) >= 0 ? 1u << x : 0u;
+    int pos0 = s.pos0;
+    fetch(pos0);
+    uint32_t seen_next = issue(0, pos0);
+    // Tile `pos0`, which lies in LDS buffer BUF.
+    const auto tile = [&](auto which) {
+        constexpr int buf = decltype(which)::value;
+        const uint32_t seen = seen_next;
         const bool hidden = seen != 15 || pos0 + kWideTile > s.len;
         wait_loads_to_lds();
         __syncthreads();  // this tile is there, and nobody reads the one before it any more
-        if (pos0 + kWideTile < end)
-            issue(buf ^ 1, pos0 + kWideTile, list.of(a, s, (pos0 + kWideTile) / 16 + wave));
+        if (pos0 + kWideTile < end) seen_next = issue(buf ^ 1, pos0 + kWideTile);
 
         // Operands are read from LDS a group of products ahead: the reads of group x + 1 run under the products
         // of group x (the scheduling barriers keep the compiler from sinking each read to its use).
@@ -550,7 +597,12 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
             __builtin_amdgcn_sched_barrier(0);
         }
         pos0 += kWideTile;
-        buf ^= 1;
+    };
+    while (true) {
+        tile(std::integral_constant<int, 0>{});
+        if (pos0 >= end) break;
+        tile(std::integral_constant<int, 1>{});
+        if (pos0 >= end) break;
     }
 
     l += __shfl_xor(l, 32);
@@ -670,86 +722,97 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_ke
         if (b == a.n_seqs - 1) seqs.units[a.n_seqs] = eu, seqs.items[a.n_seqs] = ei;
     }
 
-    // Equal shares. qp, qs: units of one run; wp, ws: runs. Runs of a suffix are a wave's, runs of the prefix a
-    // workgroup's where WIDE. Costs are in steps of one wave.
+    // The dealing. Narrow prefix: its units and the suffixes' in equal runs, one to a wave, wp and ws of them. Wide
+    // prefix: the host has cut every item alike (so that workgroups that read the same keys for other rows go
+    // through them together) into pieces, and each XCD's workgroups take `per_xcd` of them in turns; then the
+    // waves take the suffixes, those of workgroups that had one piece less (`idle`) more of them. qf, qb: units of
+    // a run of an idle and of a busy workgroup's wave.
+    int wp = 0, ws = 0, qf, qb, idle = 0;
     const int up = (a.prefix_len + UNIT_P - 1) / UNIT_P, total_p = a.kv_heads * a.tiles_p * up;
-    int qp, qs, wp, ws;
+    const int pieces = a.kv_heads * a.tiles_p * a.splits, per_xcd = (pieces + 7) / 8, wgs_xcd = gridDim.x >> 3;
+    const int turns = WIDE ? (per_xcd + wgs_xcd - 1) / wgs_xcd : 0, busy_xcd = per_xcd - (turns - 1) * wgs_xcd;
     if constexpr (WIDE) {
+        idle = 8 * (wgs_xcd - busy_xcd);
         const float cost_s = total_s > 0 ? 1.0f + kItemCost * (float)items_s / (float)total_s : 1.0f;
-        const float cost_p = MP == 64 ? kWideCost64 : kWideCost128;
-        float share = ((float)total_p * cost_p + 0.25f * (float)total_s * cost_s) / (float)a.n_wgs;
-        while (true) {
-            qp = max(1, (int)(share / cost_p));
-            qs = max(1, (int)(share / cost_s));
-            wp = (total_p + qp - 1) / qp;
-            ws = (total_s + qs - 1) / qs;
-            if (wp + (ws + 3) / 4 <= a.n_wgs) break;
-            share = share * 1.03f + 1.0f;
+        const int more = (int)((float)a.split_units * (MP == 64 ? kWideCost64 : kWideCost128) / cost_s);
+        const int64_t first = (int64_t)4 * idle * more;  // units that the idle ones take meanwhile
+        if (total_s <= first) {
+            qf = max(1, (total_s + 4 * idle - 1) / (4 * idle));
+            qb = 1;
+        } else {
+            qb = (total_s - (int)first + 4 * (int)gridDim.x - 1) / (4 * (int)gridDim.x);
+            qf = qb + more;
         }
     } else {
-        qp = qs = max(1, (total_p + total_s + 4 * a.n_wgs - 1) / (4 * a.n_wgs));
+        qf = qb = max(1, (total_p + total_s + 4 * (int)gridDim.x - 1) / (4 * (int)gridDim.x));
         while (true) {
-            wp = (total_p + qp - 1) / qp;
-            ws = (total_s + qs - 1) / qs;
-            if (wp + ws <= 4 * a.n_wgs) break;
-            qp = ++qs;
+            wp = (total_p + qb - 1) / qb;
+            ws = (total_s + qb - 1) / qb;
+            if (wp + ws <= 4 * (int)gridDim.x) break;
+            qf = ++qb;
         }
     }
+    const int runs_f = 4 * idle;
     __syncthreads();
     if (blockIdx.x == 0) {  // what the join needs
-        if (tid == 0) a.sched[0] = up, a.sched[1] = qp, a.sched[2] = qs;
+        if (tid == 0) a.sched[0] = up, a.sched[1] = qf, a.sched[2] = qb, a.sched[3] = runs_f;
         for (int b = tid; b <= a.n_seqs; b += kAttnThreads) {
             a.sched[kSchedHead + b] = seqs.units[b];
             a.sched[kSchedHead + a.n_seqs + 1 + b] = seqs.items[b];
         }
     }
     AttnSpan s;
-    // Run w of the prefix.
-    const auto prefix = [&](int w, auto &&work) {
-        int u = w * qp;
-        const int stop = min(total_p, u + qp);
-        while (u < stop) {
-            const int item = u / up, at = u - item * up, n = min(up - at, stop - u);
-            s.pages = a.prefix_pages;
-            s.len = a.prefix_len;
-            s.tok0 = 0;
-            s.n_tok = a.n_tokens;
-            s.causal = 0;
-            s.head = item / a.tiles_p;
-            s.row0 = (item - s.head * a.tiles_p) * MP;
-            s.n_rows = a.n_tokens * a.group;
-            s.pos0 = at * UNIT_P;
-            s.pos1 = (at + n) * UNIT_P;
-            s.po = a.part_o + (int64_t)(item + w) * (MP * DP);
-            s.pml = a.part_ml + (int64_t)(item + w) * MP;
-            work();
-            u += n;
-        }
-    };
-    // Runs are spread over the workgroups first, so that few of them use many CUs.
-    int w = wave * gridDim.x + blockIdx.x;
+    s.pages = a.prefix_pages;
+    s.len = a.prefix_len;
+    s.tok0 = 0;
+    s.n_tok = a.n_tokens;
+    s.causal = 0;
+    s.n_rows = a.n_tokens * a.group;
+    int w, u, stop;  // this wave's run of the suffixes
     if constexpr (WIDE) {
-        // Workgroup b runs on XCD b % 8: neighbours in the dealing, which read the same keys for other rows,
-        // share one XCD's L2.
-        int x = blockIdx.x;
-        const int per = gridDim.x >> 3;
-        if (x < 8 * per) x = (x & 7) * per + (x >> 3);
-        if (x < wp) {
-            __shared__ WideLds<DP> lds;
-            prefix(x, [&] { attend_wide<T, DP, MP / 32>(a, s, lds); });
-            return;
+        __shared__ WideLds<DP> lds;
+        // Workgroup b runs on XCD b % 8, whose L2 the pieces of one (head, split) share.
+        const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
+        for (int i = at; i < per_xcd; i += wgs_xcd) {
+            const int piece = xcd * per_xcd + i;
+            if (piece >= pieces) break;
+            const int hs = piece / a.tiles_p, tile = piece - hs * a.tiles_p;
+            s.head = hs / a.splits;
+            s.row0 = tile * MP;
+            s.pos0 = (hs - s.head * a.splits) * a.split_units * UNIT_P;
+            s.pos1 = s.pos0 + a.split_units * UNIT_P;
+            s.po = a.part_o + (int64_t)piece * (MP * DP);
+            s.pml = a.part_ml + (int64_t)piece * MP;
+            attend_wide<T, DP, MP / 32>(a, s, lds);
         }
-        w = wave * (gridDim.x - wp) + x - wp;
+        const bool busy = at < busy_xcd;
+        w = busy ? runs_f + wave * 8 * busy_xcd + xcd + 8 * at : wave * idle + xcd + 8 * (at - busy_xcd);
+        u = w < runs_f ? w * qf : runs_f * qf + (w - runs_f) * qb;
+        stop = min(total_s, u + (w < runs_f ? qf : qb));
     } else {
+        // Runs are spread over the workgroups first, so that few of them use many CUs.
+        w = wave * gridDim.x + blockIdx.x;
         if (w < wp) {
-            prefix(w, [&] { attend<T, MP / 16, DP>(a, s); });
+            int v = w * qb;
+            const int last = min(total_p, v + qb);
+            while (v < last) {
+                const int item = v / up, at = v - item * up, n = min(up - at, last - v);
+                s.head = item / a.tiles_p;
+                s.row0 = (item - s.head * a.tiles_p) * MP;
+                s.pos0 = at * UNIT_P;
+                s.pos1 = (at + n) * UNIT_P;
+                s.po = a.part_o + (int64_t)(item + w) * (MP * DP);
+                s.pml = a.part_ml + (int64_t)(item + w) * MP;
+                attend<T, MP / 16, DP>(a, s);
+                v += n;
+            }
             return;
         }
         w -= wp;
+        u = w * qb;
+        stop = min(total_s, u + qb);
     }
-    if (w >= ws) return;
-    int u = w * qs;
-    const int stop = min(total_s, u + qs);
+    if (u >= stop) return;
     int b = 0;  // the sequence that holds unit u: one lane finds it (the wave's own search: no barrier from here on)
     {
         int found = -1;
@@ -787,11 +850,11 @@ struct AttnParts {
     int np, ns;
     int t;                    // token, or -1: none
     int64_t row_p, row_s;     // first part's row among all rows of parts
-    int mp, ms;
+    int step_p, ms;           // rows from one part to the next
 
-    __device__ __forceinline__ AttnParts(const AttnArgs &a, int mp_, int ms_, int b, int j, int hq) : mp(mp_), ms(ms_) {
+    __device__ __forceinline__ AttnParts(const AttnArgs &a, int mp, int ms_, int b, int j, int hq) : step_p(0), ms(ms_) {
         const int2 tok = seq_tokens(a, b);
-        const int up = a.sched[0], qp = a.sched[1], qs = a.sched[2];
+        const int up = a.sched[0], qf = a.sched[1], qb = a.sched[2], runs_f = a.sched[3];
         const int before_u = a.sched[kSchedHead + b], before_i = a.sched[kSchedHead + a.n_seqs + 1 + b];
         const int ub = (seq_len(a, b) + kAttnStep - 1) / kAttnStep;
         const int head = hq / a.group, gi = hq - head * a.group;
@@ -801,23 +864,31 @@ struct AttnParts {
         if (t < 0) return;
         if (up > 0) {
             const int row = t * a.group + gi, tile = row / mp, item = head * a.tiles_p + tile;
-            const int w0 = item * up / qp;
-            np = (item * up + up - 1) / qp - w0 + 1;
-            row_p = (int64_t)(item + w0) * mp + row - tile * mp;
+            if (mp > 32) {
+                np = (up + a.split_units - 1) / a.split_units;
+                row_p = ((int64_t)head * a.splits * a.tiles_p + tile) * mp + row - tile * mp;
+                step_p = a.tiles_p * mp;
+            } else {
+                const int w0 = item * up / qb;
+                np = (item * up + up - 1) / qb - w0 + 1;
+                row_p = (int64_t)(item + w0) * mp + row - tile * mp;
+                step_p = mp;
+            }
         }
         if (ub > 0) {
             const int row = j * a.group + gi, tile = row / ms, item = head * ((tok.y * a.group + ms - 1) / ms) + tile;
-            const int u0 = before_u + item * ub, w0 = u0 / qs;
-            ns = (u0 + ub - 1) / qs - w0 + 1;
+            const auto run_of = [&](int u) { return u < runs_f * qf ? u / qf : runs_f + (u - runs_f * qf) / qb; };
+            const int u0 = before_u + item * ub, w0 = run_of(u0);
+            ns = run_of(u0 + ub - 1) - w0 + 1;
             row_s = (int64_t)(before_i + item + w0) * ms + row - tile * ms;
         }
     }
     __device__ __forceinline__ float2 ml(const AttnArgs &a, int k) const {
-        return k < np ? a.part_ml[row_p + (int64_t)k * mp] : a.part_ml[a.ml_s + row_s + (int64_t)(k - np) * ms];
+        return k < np ? a.part_ml[row_p + (int64_t)k * step_p] : a.part_ml[a.ml_s + row_s + (int64_t)(k - np) * ms];
     }
     template <int DP>
     __device__ __forceinline__ const float *o(const AttnArgs &a, int k) const {
-        return k < np ? a.part_o + (row_p + (int64_t)k * mp) * DP : a.part_o + a.part_s + (row_s + (int64_t)(k - np) * ms) * DP;
+        return k < np ? a.part_o + (row_p + (int64_t)k * step_p) * DP : a.part_o + a.part_s + (row_s + (int64_t)(k - np) * ms) * DP;
     }
 };
 

@@ -44,6 +44,7 @@ int launch_heads(const HeadsArgs &a, int32_t dt_in, int32_t dt_out, bool vec, vo
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = 64 * kAttnWaves;
 constexpr int kAttnStep = 32;                      // positions a wave takes at a time: its unit of work
+constexpr int kWideTile = 64;                      // positions a workgroup takes at a time of a prefix that many rows share
 constexpr int kAttnMaxSeqs = 1024;
 constexpr int kAttnWgs = 512;                      // most workgroups of a launch: two to each of 256 CUs
 
@@ -64,6 +65,7 @@ struct AttnArgs {
     float scale_log2;
     int32_t n_wgs;
     int32_t tiles_p;         // query tiles of the prefix per kv head
+    int32_t splits, split_units;  // of a wide prefix: equal pieces of an item, units of one
     // workspace
     int32_t *sched;          // kSchedHead words, then units before each sequence, then items before each
     float *part_o;           // [pieces][rows of a tile][padded dim]
@@ -71,7 +73,7 @@ struct AttnArgs {
     int64_t part_s;          // offset (floats) of the suffix pieces in part_o
     int64_t ml_s;            // and in part_ml
 };
-constexpr int kSchedHead = 8;  // units of a prefix item, units of a run of the prefix, of the suffixes
+constexpr int kSchedHead = 8;  // units of a prefix item, units of the two lengths of runs, runs of the first
 
 int launch_attn_d64(const AttnArgs &a, int32_t dtype, int32_t mp, int32_t ms, void *stream);
 int launch_attn_d128(const AttnArgs &a, int32_t dtype, int32_t mp, int32_t ms, void *stream);

@@ -218,11 +218,13 @@ namespace {
 
 struct AttnShape {
     int32_t dp, mp, ms;
-    int32_t group, tiles_p;
+    int32_t group, tiles_p, splits, split_units;
     int64_t cap, pieces_p, pieces_s;
     int32_t n_wgs;
     size_t sched, po, pml, total;  // workspace: bytes of the schedule, offsets of the parts, all
 };
+
+constexpr int64_t kPieceCost = 3;  // tiles that one more piece of a wide prefix costs (queries in, parts out)
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -234,6 +236,8 @@ bpw_status attn_shape(const bpw_attn_shared_prefix_args *a, AttnShape *s) {
     if ((st = check_kv(c, who))) return st;
     if (c.head_dim < 8 || c.head_dim > 256 || c.head_dim % 8)
         return fail(BPW_E_UNSUPPORTED, "%s: head_dim %d is not a multiple of 8 in [8, 256]", who, (int)c.head_dim);
+    if (c.k_row_stride < c.head_dim || c.v_row_stride < c.head_dim)
+        return fail(BPW_E_INVAL, "%s: cache row strides below head_dim %d: rows would overlap", who, (int)c.head_dim);
     if (a->n_tokens < 0 || a->n_tokens > (1 << 24)) return fail(BPW_E_INVAL, "%s: n_tokens %d outside [0, 2^24]", who, (int)a->n_tokens);
     if (a->n_seqs < 1 || a->n_seqs > bpw::kAttnMaxSeqs)
         return fail(BPW_E_UNSUPPORTED, "%s: n_seqs %d outside [1, %d]", who, (int)a->n_seqs, (int)bpw::kAttnMaxSeqs);
@@ -265,9 +269,27 @@ bpw_status attn_shape(const bpw_attn_shared_prefix_args *a, AttnShape *s) {
     s->tiles_p = (int32_t)tiles_p;
     const int64_t most = items_p * up + items_s * us;
     s->n_wgs = (int32_t)(most < 2 ? 2 : most < bpw::kAttnWgs ? most : bpw::kAttnWgs);
-    // one part per item and per run (a wave's, or a workgroup's where the prefix is wide)
+    s->splits = s->split_units = 0;
+    if (mp > 32) {
+        // Pieces of a wide prefix: items cut alike, in as many as end soonest (whole turns of all workgroups),
+        // counting for each piece what it costs beyond its tiles.
+        s->n_wgs = (s->n_wgs + 7) / 8 * 8;
+        const int64_t tiles = (a->prefix_len + bpw::kWideTile - 1) / bpw::kWideTile;
+        int64_t best = INT64_MAX;
+        for (int64_t n = 1; n <= tiles && n <= 64; ++n) {
+            const int64_t turns = (items_p * n + s->n_wgs - 1) / s->n_wgs, len = (tiles + n - 1) / n;
+            const int64_t cost = turns * (len + kPieceCost);
+            if (cost < best) {
+                best = cost;
+                s->splits = (int32_t)n;
+                s->split_units = (int32_t)len;
+            }
+        }
+        s->splits = (int32_t)((tiles + s->split_units - 1) / s->split_units);
+    }
+    // one part per item and per run, or per piece of a wide prefix
     const int64_t waves = (int64_t)bpw::kAttnWaves * s->n_wgs;
-    s->pieces_p = up > 0 ? items_p + (mp > 32 ? s->n_wgs : waves) : 0;
+    s->pieces_p = mp > 32 ? items_p * s->splits : up > 0 ? items_p + waves : 0;
     s->pieces_s = us > 0 ? items_s + waves : 0;
     s->sched = up256((size_t)(bpw::kSchedHead + 2 * (a->n_seqs + 1)) * 4);
     s->po = s->sched;
@@ -348,6 +370,8 @@ bpw_status bpw_attn_shared_prefix(const bpw_attn_shared_prefix_args *a, void *d_
     k.scale_log2 = a->scale * 1.44269504088896341f;  // scores in units of log 2: v_exp_f32 is 2^x
     k.n_wgs = s.n_wgs;
     k.tiles_p = s.tiles_p;
+    k.splits = s.splits;
+    k.split_units = s.split_units;
     char *ws = static_cast<char *>(d_ws);
     k.sched = reinterpret_cast<int32_t *>(ws);
     k.part_o = reinterpret_cast<float *>(ws + s.po);
