@@ -678,7 +678,39 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_ke
     AttnSeqs seqs(dynamic, a.n_seqs);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-    // Units and items (head x tile) before each sequence: four sequences a thread, then a scan.
+    AttnSpan s;
+    s.pages = a.prefix_pages;
+    s.len = a.prefix_len;
+    s.tok0 = 0;
+    s.n_tok = a.n_tokens;
+    s.causal = 0;
+    s.n_rows = a.n_tokens * a.group;
+
+    // A wide prefix comes first: the host has cut every item (head x tile) alike into pieces, so that workgroups that
+    // read the same keys for other rows go through them together, and each XCD's workgroups (workgroup b runs on
+    // XCD b % 8) take `per_xcd` neighbouring pieces in turns, sharing that XCD's L2. The suffixes come after it.
+    // (Letting half of the workgroups take their suffixes first, to run memory-bound work beside the products,
+    // measured slower: 186 us against 179 for 256 tokens over a prefix of 32768, by spilled registers.)
+    const int up = (a.prefix_len + UNIT_P - 1) / UNIT_P, total_p = a.kv_heads * a.tiles_p * up;
+    const int pieces = a.kv_heads * a.tiles_p * a.splits, per_xcd = (pieces + 7) / 8, wgs_xcd = gridDim.x >> 3;
+    const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
+    if constexpr (WIDE) {
+        __shared__ WideLds<DP> lds;
+        for (int i = at; i < per_xcd; i += wgs_xcd) {
+            const int piece = xcd * per_xcd + i;
+            if (piece >= pieces) break;
+            const int hs = piece / a.tiles_p, tile = piece - hs * a.tiles_p;
+            s.head = hs / a.splits;
+            s.row0 = tile * MP;
+            s.pos0 = (hs - s.head * a.splits) * a.split_units * UNIT_P;
+            s.pos1 = s.pos0 + a.split_units * UNIT_P;
+            s.po = a.part_o + (int64_t)piece * (MP * DP);
+            s.pml = a.part_ml + (int64_t)piece * MP;
+            attend_wide<T, DP, MP / 32>(a, s, lds);
+        }
+    }
+
+    // Units and items before each sequence: four sequences a thread, then a scan.
     int un[4], it[4], su = 0, si = 0;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
@@ -697,12 +729,12 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_ke
         si += it[x];
     }
     int iu = su, ii = si;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
+    for (int d = 1; d < 64 && 4 * d < a.n_seqs; d <<= 1) {  // (few sequences: few lanes hold any)
         const int x = __shfl_up(iu, d), y = __shfl_up(ii, d);
         if (lane >= d) iu += x, ii += y;
     }
-    if (lane == 63) wave_sum[wave][0] = iu, wave_sum[wave][1] = ii;
+    const int top_lane = min(63, (a.n_seqs - 1) / 4);  // (a first wave alone where the scan was cut short)
+    if (lane == top_lane) wave_sum[wave][0] = wave && top_lane < 63 ? 0 : iu, wave_sum[wave][1] = wave && top_lane < 63 ? 0 : ii;
     __syncthreads();
     int total_s = 0, items_s = 0;
 #pragma unroll
@@ -723,20 +755,16 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_ke
     }
 
     // The dealing. Narrow prefix: its units and the suffixes' in equal runs, one to a wave, wp and ws of them. Wide
-    // prefix: the host has cut every item alike (so that workgroups that read the same keys for other rows go
-    // through them together) into pieces, and each XCD's workgroups take `per_xcd` of them in turns; then the
-    // waves take the suffixes, those of workgroups that had one piece less (`idle`) more of them. qf, qb: units of
-    // a run of an idle and of a busy workgroup's wave.
+    // prefix: the waves of workgroups that had one piece less (`idle`) take more of the suffixes. qf, qb: units of a run
+    // of an idle and of a busy workgroup's wave; runs_f: runs of the idle ones, which come first.
     int wp = 0, ws = 0, qf, qb, idle = 0;
-    const int up = (a.prefix_len + UNIT_P - 1) / UNIT_P, total_p = a.kv_heads * a.tiles_p * up;
-    const int pieces = a.kv_heads * a.tiles_p * a.splits, per_xcd = (pieces + 7) / 8, wgs_xcd = gridDim.x >> 3;
     const int turns = WIDE ? (per_xcd + wgs_xcd - 1) / wgs_xcd : 0, busy_xcd = per_xcd - (turns - 1) * wgs_xcd;
     if constexpr (WIDE) {
         idle = 8 * (wgs_xcd - busy_xcd);
         const float cost_s = total_s > 0 ? 1.0f + kItemCost * (float)items_s / (float)total_s : 1.0f;
         const int more = (int)((float)a.split_units * (MP == 64 ? kWideCost64 : kWideCost128) / cost_s);
         const int64_t first = (int64_t)4 * idle * more;  // units that the idle ones take meanwhile
-        if (total_s <= first) {
+        if (idle > 0 && total_s <= first) {
             qf = max(1, (total_s + 4 * idle - 1) / (4 * idle));
             qb = 1;
         } else {
@@ -761,87 +789,66 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_ke
             a.sched[kSchedHead + a.n_seqs + 1 + b] = seqs.items[b];
         }
     }
-    AttnSpan s;
-    s.pages = a.prefix_pages;
-    s.len = a.prefix_len;
-    s.tok0 = 0;
-    s.n_tok = a.n_tokens;
-    s.causal = 0;
-    s.n_rows = a.n_tokens * a.group;
-    int w, u, stop;  // this wave's run of the suffixes
-    if constexpr (WIDE) {
-        __shared__ WideLds<DP> lds;
-        // Workgroup b runs on XCD b % 8, whose L2 the pieces of one (head, split) share.
-        const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
-        for (int i = at; i < per_xcd; i += wgs_xcd) {
-            const int piece = xcd * per_xcd + i;
-            if (piece >= pieces) break;
-            const int hs = piece / a.tiles_p, tile = piece - hs * a.tiles_p;
-            s.head = hs / a.splits;
-            s.row0 = tile * MP;
-            s.pos0 = (hs - s.head * a.splits) * a.split_units * UNIT_P;
-            s.pos1 = s.pos0 + a.split_units * UNIT_P;
-            s.po = a.part_o + (int64_t)piece * (MP * DP);
-            s.pml = a.part_ml + (int64_t)piece * MP;
-            attend_wide<T, DP, MP / 32>(a, s, lds);
+    // This wave's run of the suffixes, run w: units [u, stop).
+    const auto suffixes = [&](int w, int u, int stop) {
+        if (u >= stop) return;
+        int b = 0;  // the sequence that holds unit u: one lane finds it
+        {
+            int found = -1;
+            for (int i = lane; i < a.n_seqs; i += 64)
+                if (seqs.units[i] <= u && u < seqs.units[i + 1]) found = i;
+            b = __builtin_amdgcn_readlane(found, __builtin_ctzll(__ballot(found >= 0)));
         }
+        AttnSpan s;
+        while (u < stop) {
+            while (seqs.units[b + 1] <= u) ++b;  // past idle sequences
+            b = __builtin_amdgcn_readfirstlane(b);
+            const int len = __builtin_amdgcn_readfirstlane(seqs.len[b]), ub = (len + kAttnStep - 1) / kAttnStep;
+            const int n_tok = __builtin_amdgcn_readfirstlane(seqs.n_tok[b]), tiles = (n_tok * a.group + MS - 1) / MS;
+            const int rest = u - __builtin_amdgcn_readfirstlane(seqs.units[b]);
+            const int item = rest / ub, at = rest - item * ub, n = min(ub - at, stop - u);
+            const int64_t part = __builtin_amdgcn_readfirstlane(seqs.items[b]) + item + w;
+            s.pages = a.table + (int64_t)b * a.table_stride;
+            s.len = len;
+            s.tok0 = __builtin_amdgcn_readfirstlane(seqs.tok0[b]);
+            s.n_tok = n_tok;
+            s.causal = 1;
+            s.head = item / tiles;
+            s.row0 = (item - s.head * tiles) * MS;
+            s.n_rows = n_tok * a.group;
+            s.pos0 = at * kAttnStep;
+            s.pos1 = (at + n) * kAttnStep;
+            s.po = a.part_o + a.part_s + part * (MS * DP);
+            s.pml = a.part_ml + a.ml_s + part * MS;
+            attend<T, MS / 16, DP>(a, s);
+            u += n;
+        }
+    };
+    if constexpr (WIDE) {
         const bool busy = at < busy_xcd;
-        w = busy ? runs_f + wave * 8 * busy_xcd + xcd + 8 * at : wave * idle + xcd + 8 * (at - busy_xcd);
-        u = w < runs_f ? w * qf : runs_f * qf + (w - runs_f) * qb;
-        stop = min(total_s, u + (w < runs_f ? qf : qb));
+        const int w = busy ? runs_f + wave * 8 * busy_xcd + xcd + 8 * at : wave * idle + xcd + 8 * (at - busy_xcd);
+        const int u = w < runs_f ? w * qf : runs_f * qf + (w - runs_f) * qb;
+        suffixes(w, u, min(total_s, u + (w < runs_f ? qf : qb)));
     } else {
         // Runs are spread over the workgroups first, so that few of them use many CUs.
-        w = wave * gridDim.x + blockIdx.x;
-        if (w < wp) {
-            int v = w * qb;
-            const int last = min(total_p, v + qb);
-            while (v < last) {
-                const int item = v / up, at = v - item * up, n = min(up - at, last - v);
-                s.head = item / a.tiles_p;
-                s.row0 = (item - s.head * a.tiles_p) * MP;
-                s.pos0 = at * UNIT_P;
-                s.pos1 = (at + n) * UNIT_P;
-                s.po = a.part_o + (int64_t)(item + w) * (MP * DP);
-                s.pml = a.part_ml + (int64_t)(item + w) * MP;
-                attend<T, MP / 16, DP>(a, s);
-                v += n;
-            }
+        const int w = wave * gridDim.x + blockIdx.x;
+        if (w >= wp) {
+            suffixes(w - wp, (w - wp) * qb, min(total_s, (w - wp + 1) * qb));
             return;
         }
-        w -= wp;
-        u = w * qb;
-        stop = min(total_s, u + qb);
-    }
-    if (u >= stop) return;
-    int b = 0;  // the sequence that holds unit u: one lane finds it (the wave's own search: no barrier from here on)
-    {
-        int found = -1;
-        for (int i = lane; i < a.n_seqs; i += 64)
-            if (seqs.units[i] <= u && u < seqs.units[i + 1]) found = i;
-        b = __builtin_amdgcn_readlane(found, __builtin_ctzll(__ballot(found >= 0)));
-    }
-    while (u < stop) {
-        while (seqs.units[b + 1] <= u) ++b;  // past idle sequences
-        b = __builtin_amdgcn_readfirstlane(b);
-        const int len = __builtin_amdgcn_readfirstlane(seqs.len[b]), ub = (len + kAttnStep - 1) / kAttnStep;
-        const int n_tok = __builtin_amdgcn_readfirstlane(seqs.n_tok[b]), tiles = (n_tok * a.group + MS - 1) / MS;
-        const int rest = u - __builtin_amdgcn_readfirstlane(seqs.units[b]);
-        const int item = rest / ub, at = rest - item * ub, n = min(ub - at, stop - u);
-        const int64_t piece = __builtin_amdgcn_readfirstlane(seqs.items[b]) + item + w;
-        s.pages = a.table + (int64_t)b * a.table_stride;
-        s.len = len;
-        s.tok0 = __builtin_amdgcn_readfirstlane(seqs.tok0[b]);
-        s.n_tok = n_tok;
-        s.causal = 1;
-        s.head = item / tiles;
-        s.row0 = (item - s.head * tiles) * MS;
-        s.n_rows = n_tok * a.group;
-        s.pos0 = at * kAttnStep;
-        s.pos1 = (at + n) * kAttnStep;
-        s.po = a.part_o + a.part_s + piece * (MS * DP);
-        s.pml = a.part_ml + a.ml_s + piece * MS;
-        attend<T, MS / 16, DP>(a, s);
-        u += n;
+        int v = w * qb;
+        const int last = min(total_p, v + qb);
+        while (v < last) {
+            const int item = v / up, at = v - item * up, n = min(up - at, last - v);
+            s.head = item / a.tiles_p;
+            s.row0 = (item - s.head * a.tiles_p) * MP;
+            s.pos0 = at * UNIT_P;
+            s.pos1 = (at + n) * UNIT_P;
+            s.po = a.part_o + (int64_t)(item + w) * (MP * DP);
+            s.pml = a.part_ml + (int64_t)(item + w) * MP;
+            attend<T, MP / 16, DP>(a, s);
+            v += n;
+        }
     }
 }
 
@@ -930,6 +937,13 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int
     const AttnParts p(a, mp, ms, bj / a.max_q, bj % a.max_q, hq);
     if (p.t < 0) return;
     const int parts = p.np + p.ns;
+    const int gr = tid / LANES, ln = tid - gr * LANES;
+    f32x4 y[4];  // the first parts' outputs are on their way while the weights are formed
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[i] = f32x4{0, 0, 0, 0};
+        if (gr + i * GROUPS < parts) y[i] = *reinterpret_cast<const f32x4 *>(p.template o<DP>(a, gr + i * GROUPS) + 4 * ln);
+    }
     float top = kNone;
     for (int k = tid; k < parts; k += kAttnThreads) top = fmaxf(top, p.ml(a, k).x);
     top = wave_max(top);
@@ -947,10 +961,12 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int
     if ((tid & 63) == 0) red[1][tid >> 6] = sum;
     __syncthreads();
     sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-    const int gr = tid / LANES, ln = tid - gr * LANES;
     f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (gr + i * GROUPS < parts) acc += y[i] * weight[gr + i * GROUPS];
 #pragma unroll 4
-    for (int k = gr; k < parts; k += GROUPS) acc += *reinterpret_cast<const f32x4 *>(p.template o<DP>(a, k) + 4 * ln) * weight[k];
+    for (int k = gr + 4 * GROUPS; k < parts; k += GROUPS) acc += *reinterpret_cast<const f32x4 *>(p.template o<DP>(a, k) + 4 * ln) * weight[k];
     sums[gr][ln] = acc;
     __syncthreads();
     if (gr) return;
