@@ -679,20 +679,37 @@ class PagedKv:
         return self.c.page_size
 
 
+_raw_stream = None  # torch's current stream of a device as an address, where this torch has that call
+
+
+def _current_stream(device: int) -> int:
+    """The address of torch's current stream: 0.1 us by torch's own accessor, 2.7 us through a Stream object, in
+    calls whose launch takes 4."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(device)
+
+
 class _Bound:
     """Arguments checked and bound once; run() queues the launches on a stream. The tensors named stay
     alive with the plan and are read and written as they are when the work runs, so a plan may be run
     again after their contents change, and its runs captured into a graph."""
 
     def _bind(self, fn: str, args, keep, d_ws=None):
+        t = next(x for x in keep if hasattr(x, "device"))
+        self._device = t.device.index or 0
         self._fn, self._args, self._ref, self._keep = getattr(_lib.lib(), fn), args, ctypes.byref(args), (keep, d_ws)
         self._ws = None if d_ws is None else (_dptr(d_ws), d_ws.numel() * d_ws.element_size())
 
     def run(self, stream=None) -> None:
+        stream = _current_stream(self._device) if stream is None else _stream(stream)
         if self._ws is None:
-            status = self._fn(self._ref, _stream(stream))
+            status = self._fn(self._ref, stream)
         else:
-            status = self._fn(self._ref, self._ws[0], self._ws[1], _stream(stream))
+            status = self._fn(self._ref, self._ws[0], self._ws[1], stream)
         if status:
             _lib.check(status)
 

@@ -986,29 +986,34 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_rows_kernel(AttnArgs a
     const AttnParts p(a, mp, ms, bj / a.max_q, bj % a.max_q, hq);
     if (p.t < 0) return;
     const int parts = p.np + p.ns;
+    const int gr = lane / LANES, ln = lane - gr * LANES;
+    f32x4 y[4];  // four outputs of each lane in flight, the first ones while the weights are formed
+    const auto load = [&](int k, int n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            y[i] = *reinterpret_cast<const f32x4 *>(p.template o<DP>(a, min(k + i * GROUPS + gr, n - 1)) + 4 * ln);
+    };
+    if (parts > 0) load(0, parts);
     float top = kNone;
     for (int k = lane; k < parts; k += 64) top = fmaxf(top, p.ml(a, k).x);
     top = wave_max(top);
-    const int gr = lane / LANES, ln = lane - gr * LANES;
     f32x4 acc = {0, 0, 0, 0};
     float sum = 0.0f;
     for (int k0 = 0; k0 < parts; k0 += 64) {
         const float2 x = k0 + lane < parts ? p.ml(a, k0 + lane) : make_float2(kNone, 0.0f);
-        const float f = x.x == kNone ? 0.0f : __builtin_amdgcn_exp2f(x.x - top);
+        const float f = x.x == kNone ? 0.0f : __builtin_amdgcn_exp2f(x.x - top);  // of part k0 + lane; 0 past the last
         sum += x.x == kNone ? 0.0f : f * x.y;
         const int n = min(64, parts - k0);
-        for (int k = 0; k < n; k += 4 * GROUPS) {  // four loads of each lane in flight
-            f32x4 y[4];
-            float w[4];
+        for (int k = 0; k < n; k += 4 * GROUPS) {
+            f32x4 z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[i] = y[i];
+            if (k0 + k + 4 * GROUPS < parts) load(k0 + k + 4 * GROUPS, parts);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int at = k + i * GROUPS + gr, mine = min(at, n - 1);
-                y[i] = *reinterpret_cast<const f32x4 *>(p.template o<DP>(a, k0 + mine) + 4 * ln);
-                w[i] = __shfl(f, mine);
-                if (at >= n) w[i] = 0.0f;
+                const float w = __shfl(f, (k + i * GROUPS + gr) & 63);
+                if (k + i * GROUPS + gr < n) acc += z[i] * w;
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc += y[i] * w[i];
         }
     }
     sum = wave_add(sum);

@@ -91,6 +91,7 @@ struct VerifyArgs {
     const float *accept_u, *sample_u;
     int32_t *out_tokens, *accepted;
     double *sums;           // [n_seqs][chunks]
+    int32_t *found;         // [n_seqs][2]: drafts accepted, whether one was refused
     int32_t n_seqs, max_drafts, vocab, chunks;
 };
 int launch_verify(const VerifyArgs &a, int32_t dtype, void *stream);

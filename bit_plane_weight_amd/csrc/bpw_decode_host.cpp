@@ -109,6 +109,8 @@ bpw_status run_heads(bpw::HeadsArgs &a, int32_t dt_in, int32_t dt_out, bool vec,
     a.lanes_log2 = vec ? log2_of(D / 16) : log2_of(D / 2);
     if (a.lanes_log2 > 6) a.lanes_log2 = 6;
     const int at_once = bpw::kHeadThreads >> a.lanes_log2;
+    // Many tokens with few heads: as many to a workgroup as one sweep over its lanes holds. (More, so that a last sweep
+    // over 40 heads is fuller, measured no faster: 69.5-72 us against 69.9 for 16384 tokens of 32 + 8 heads of 128.)
     a.tokens_per_wg = a.n_tokens >= 2048 && heads < at_once ? at_once / heads : 1;
     bpw_status st = (bpw_status)bpw::host_check_device();
     if (st) return st;
@@ -224,6 +226,11 @@ struct AttnShape {
     size_t sched, po, pml, total;  // workspace: bytes of the schedule, offsets of the parts, all
 };
 
+// Most work (steps of single waves x padded head size) that a prefix of many rows is given to single waves, whose
+// first results come sooner; beyond it workgroups share the keys. Measured, us a call (waves, workgroups), steps x size:
+// 8 x 64 32-row heads over 1000 positions, 49 k: 17.1, 19.5; 5 x 64 rows of 128 over 512, 20 k: 15.0, 15.9; over 2048,
+// 82 k: 19.3, 17.4; over 4096, 164 k: 27.4, 20.2; 4 x 128 rows of 256 over 1024, 131 k: 41.5, 34.4.
+constexpr int64_t kNarrowWork = 65536;
 constexpr int64_t kPieceCost = 3;  // tiles that one more piece of a wide prefix costs (queries in, parts out)
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -257,10 +264,15 @@ bpw_status attn_shape(const bpw_attn_shared_prefix_args *a, AttnShape *s) {
     const int64_t max_q = a->max_q < a->n_tokens ? a->max_q : (a->n_tokens > 0 ? a->n_tokens : 1);
     const int64_t rows_s = max_q * s->group;
     s->ms = rows_s <= 16 ? 16 : 32;
-    s->mp = a->prefix_len == 0 || rows_p <= s->ms ? s->ms : rows_p <= 32 ? 32 : rows_p <= 64 ? 64 : 128;
+    const int64_t up = (a->prefix_len + bpw::kAttnStep - 1) / bpw::kAttnStep;
+    if (a->prefix_len == 0 || rows_p <= s->ms)
+        s->mp = s->ms;
+    else if (rows_p <= 32 || c.kv_heads * ((rows_p + 31) / 32) * up * s->dp <= kNarrowWork)
+        s->mp = 32;
+    else
+        s->mp = rows_p <= 64 ? 64 : 128;
     const int64_t mp = s->mp, ms = s->ms;
     const int64_t tiles_p = (rows_p + mp - 1) / mp, tiles_s = (rows_s + ms - 1) / ms;
-    const int64_t up = (a->prefix_len + bpw::kAttnStep - 1) / bpw::kAttnStep;
     const int64_t us = (s->cap + bpw::kAttnStep - 1) / bpw::kAttnStep;
     const int64_t items_p = c.kv_heads * tiles_p, items_s = (int64_t)a->n_seqs * c.kv_heads * tiles_s;
     const double work = (double)items_p * (double)up + (double)items_s * (double)us;
@@ -389,7 +401,7 @@ bpw_status bpw_attn_shared_prefix(const bpw_attn_shared_prefix_args *a, void *d_
 size_t bpw_verify_draft_workspace_bytes(int32_t n_seqs, int32_t vocab) {
     if (n_seqs < 1 || vocab < 1 || vocab > (1 << 24)) return 0;
     const size_t chunks = ((size_t)vocab + bpw::kVerifyChunk - 1) / bpw::kVerifyChunk;
-    return up256((size_t)n_seqs * chunks * sizeof(double));
+    return up256((size_t)n_seqs * (chunks * sizeof(double) + 2 * sizeof(int32_t)));
 }
 
 bpw_status bpw_verify_draft(const bpw_verify_draft_args *a, void *d_ws, size_t ws_len, void *stream) {
@@ -429,11 +441,12 @@ bpw_status bpw_verify_draft(const bpw_verify_draft_args *a, void *d_ws, size_t w
     v.sample_u = a->d_sample_u;
     v.out_tokens = a->d_out_tokens;
     v.accepted = a->d_accepted;
+    v.chunks = (a->vocab + bpw::kVerifyChunk - 1) / bpw::kVerifyChunk;
     v.sums = static_cast<double *>(d_ws);
+    v.found = reinterpret_cast<int32_t *>(v.sums + (size_t)a->n_seqs * v.chunks);
     v.n_seqs = a->n_seqs;
     v.max_drafts = a->max_drafts;
     v.vocab = a->vocab;
-    v.chunks = (a->vocab + bpw::kVerifyChunk - 1) / bpw::kVerifyChunk;
     return hip_status(bpw::launch_verify(v, a->dtype, stream), "verify launch");
 }
 

@@ -22,24 +22,39 @@ struct Vec8<__bf16> { typedef bf16x8 type; };
 template <>
 struct Vec8<_Float16> { typedef f16x8 type; };
 
-// Eight consecutive elements, 16-byte aligned, as float32.
+// Eight consecutive elements, 16-byte aligned, as they are in memory and as float32.
 template <class T>
-__device__ __forceinline__ f32x8 load8(const T *p) {
+using Raw8 = typename Vec8<T>::type;
+
+template <class T>
+__device__ __forceinline__ Raw8<T> raw8(const T *p) {
     if constexpr (sizeof(T) == 4) {
         const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
         return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     } else {
-        return __builtin_convertvector(*reinterpret_cast<const typename Vec8<T>::type *>(p), f32x8);
+        return *reinterpret_cast<const Raw8<T> *>(p);
     }
 }
 
+template <class V>
+__device__ __forceinline__ f32x8 as_f32(V x) {
+    return __builtin_convertvector(x, f32x8);
+}
+
+template <class T>
+__device__ __forceinline__ f32x8 load8(const T *p) {
+    return as_f32(raw8(p));
+}
+
+// Stored non-temporally: what a prompt's heads write is not read again by this launch (16384 tokens of 40 heads of
+// 128 in bf16: 69.5 us, 73.1 with ordinary stores).
 template <class T>
 __device__ __forceinline__ void store8(T *p, f32x8 x) {
     if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<f32x4 *>(p) = __builtin_shufflevector(x, x, 0, 1, 2, 3);
-        *reinterpret_cast<f32x4 *>(p + 4) = __builtin_shufflevector(x, x, 4, 5, 6, 7);
+        __builtin_nontemporal_store(__builtin_shufflevector(x, x, 0, 1, 2, 3), reinterpret_cast<f32x4 *>(p));
+        __builtin_nontemporal_store(__builtin_shufflevector(x, x, 4, 5, 6, 7), reinterpret_cast<f32x4 *>(p + 4));
     } else {
-        *reinterpret_cast<typename Vec8<T>::type *>(p) = __builtin_convertvector(x, typename Vec8<T>::type);
+        __builtin_nontemporal_store(__builtin_convertvector(x, typename Vec8<T>::type), reinterpret_cast<typename Vec8<T>::type *>(p));
     }
 }
 

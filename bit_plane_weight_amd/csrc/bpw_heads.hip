@@ -98,23 +98,25 @@ __global__ __launch_bounds__(kHeadThreads) void heads_vec_kernel(HeadsArgs a) {
 
     int u = threadIdx.x >> a.lanes_log2;
     HeadRow<TI, TO> r;
-    f32x8 x0 = {}, x1 = {};
+    Raw8<TI> n0, n1;
     int t = 0;
-    if (u < total) {  // the first head's loads leave before the angles are formed
+    const auto fetch = [&] {
         t = u / heads;
         r = head_row<TI, TO>(a, t0 + t, u - t * heads);
-        x0 = load8(r.in + i0);
-        x1 = load8(r.in + i1);
-    }
+        n0 = raw8(r.in + i0);
+        n1 = raw8(r.in + i1);
+    };
+    if (u < total) fetch();  // the first head's loads leave before the angles are formed
     fill_turns(a, t0, nt, cs);
     __syncthreads();
     while (u < total) {
+        f32x8 x0 = as_f32(n0), x1 = as_f32(n1);
         if (r.gain) {
             float s = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) s = __builtin_fmaf(x0[e], x0[e], __builtin_fmaf(x1[e], x1[e], s));
             s = lanes_sum(in ? s : 0.0f, a.lanes_log2);
-            const float f = 1.0f / sqrtf(s / (float)a.head_dim + a.eps);
+            const float f = rsqrtf(s / (float)a.head_dim + a.eps);
             x0 = x0 * f * load8(r.gain + i0);
             x1 = x1 * f * load8(r.gain + i1);
         }
@@ -150,12 +152,7 @@ __global__ __launch_bounds__(kHeadThreads) void heads_vec_kernel(HeadsArgs a) {
             store8(r.out + i1, x1);
         }
         u += step;
-        if (u < total) {
-            t = u / heads;
-            r = head_row<TI, TO>(a, t0 + t, u - t * heads);
-            x0 = load8(r.in + i0);
-            x1 = load8(r.in + i1);
-        }
+        if (u < total) fetch();
     }
 }
 
@@ -180,7 +177,7 @@ __global__ __launch_bounds__(kHeadThreads) void heads_any_kernel(HeadsArgs a) {
                 const float x = (float)r.in[2 * p], y = (float)r.in[2 * p + 1];
                 s = __builtin_fmaf(x, x, __builtin_fmaf(y, y, s));
             }
-            f = 1.0f / sqrtf(lanes_sum(s, a.lanes_log2) / (float)a.head_dim + a.eps);
+            f = rsqrtf(lanes_sum(s, a.lanes_log2) / (float)a.head_dim + a.eps);
         }
         for (int p = c; p < pairs; p += lanes) {
             const bool split = p < half && !a.interleaved;

@@ -10,13 +10,16 @@
 // Bound: HBM, one row of p and one of q per sequence; for one sequence the two launches. A row is cut into
 // chunks of kVerifyChunk entries, one workgroup each, so that one sequence's rows are read by many CUs;
 // the second launch (one workgroup per sequence) finds the chunk that holds the border from the chunks' sums
-// and walks that chunk alone. Sums have a fixed order whatever the launch.
+// and walks that chunk alone. Sums have a fixed order whatever the launch: a lane's four neighbours, the lanes of
+// a wave, the sixteen wave rounds of a chunk, the chunks.
 #include "bpw_decode.h"
 #include "bpw_elem.h"
 
 namespace bpw {
 
-constexpr int kPer = kVerifyChunk / kVerifyThreads;  // entries of one thread
+constexpr int kRounds = kVerifyChunk / (4 * kVerifyThreads);  // a wave takes 256 neighbours at a time, four a lane
+constexpr int kSubs = 4 * kRounds;                            // wave rounds of a chunk
+constexpr int kSub = 256;                                     // entries of one
 
 // What sequence b draws from: drafts accepted, whether one was refused, the rows.
 template <class T>
@@ -31,19 +34,22 @@ struct Drawn {
 template <class T>
 __device__ __forceinline__ Drawn<T> accept(const VerifyArgs &a, int b) {
     const int lane = threadIdx.x & 63;
-    const int most = a.n_draft ? min(max(a.n_draft[b], 0), a.max_drafts) : a.max_drafts;
+    const int given = a.n_draft ? a.n_draft[b] : a.max_drafts;  // (loaded beside the tokens)
     const T *t = static_cast<const T *>(a.target) + (int64_t)b * a.t_seq;
     const T *d = static_cast<const T *>(a.draft) + (int64_t)b * a.d_seq;
     bool ok = false;
     int x = -1;
-    if (lane < most) {
+    if (lane < a.max_drafts) {
         x = a.tokens[(int64_t)b * a.max_drafts + lane];
+        const float u = a.accept_u[(int64_t)b * a.max_drafts + lane];
         if (x >= 0 && x < a.vocab) {
             const double p = (double)(float)t[lane * a.t_step + x];
             const double q = a.draft ? (double)(float)d[lane * a.d_step + x] : 1.0;
-            ok = (double)a.accept_u[(int64_t)b * a.max_drafts + lane] * q < p;
+            ok = (double)u * q < p;
         }
     }
+    const int most = min(max(given, 0), a.max_drafts);
+    ok = ok && lane < most;
     const uint64_t no = ~__ballot(ok);
     Drawn<T> r;
     r.n = no ? min((int)__builtin_ctzll(no), most) : most;
@@ -54,15 +60,43 @@ __device__ __forceinline__ Drawn<T> accept(const VerifyArgs &a, int b) {
     return r;
 }
 
-// The mass of an entry: rest == true takes the draft's away.
 template <class T>
-__device__ __forceinline__ double mass(const Drawn<T> &r, bool rest, int i) {
-    double m = (double)(float)r.p[i];
-    if (rest) {
-        if (r.q) m -= (double)(float)r.q[i];
-        else if (i == r.x) m = 0.0;  // p - 1 is never positive
+__device__ __forceinline__ Drawn<T> drawn_from(const VerifyArgs &a, int b, int n, bool refused) {
+    Drawn<T> r;
+    r.n = n;
+    r.refused = refused;
+    r.x = refused ? a.tokens[(int64_t)b * a.max_drafts + n] : -1;
+    r.p = static_cast<const T *>(a.target) + (int64_t)b * a.t_seq + n * a.t_step;
+    r.q = refused && a.draft ? static_cast<const T *>(a.draft) + (int64_t)b * a.d_seq + n * a.d_step : nullptr;
+    return r;
+}
+
+// Four neighbours of a row from entry i on; zeros past the vocabulary.
+template <class T>
+__device__ __forceinline__ void four(const T *row, int i, int vocab, float (&x)[4]) {
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    if (((uintptr_t)row & (sizeof(T4) - 1)) == 0 && i + 4 <= vocab) {
+        const T4 v = *reinterpret_cast<const T4 *>(row + i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = (float)v[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = i + e < vocab ? (float)row[i + e] : 0.0f;
     }
-    return m > 0.0 && m < __builtin_inf() ? m : 0.0;
+}
+
+// The masses of this lane's entries of round j of a chunk; rest: the draft's are taken away.
+template <class T>
+__device__ __forceinline__ void masses(const VerifyArgs &a, const Drawn<T> &r, bool rest, int i, double (&m)[4]) {
+    float p[4], q[4] = {0, 0, 0, 0};
+    four(r.p, i, a.vocab, p);
+    if (rest && r.q) four(r.q, i, a.vocab, q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        double x = (double)p[e] - (double)q[e];
+        if (rest && !r.q && i + e == r.x) x = 0.0;  // p - 1 is never positive
+        m[e] = x > 0.0 && x < __builtin_inf() ? x : 0.0;
+    }
 }
 
 __device__ __forceinline__ double wave_sum(double s) {
@@ -71,132 +105,122 @@ __device__ __forceinline__ double wave_sum(double s) {
     return s;
 }
 
-// Sum of the chunk's masses, the same in every thread: thread sums in entry order, then a tree. Entry
-// c * kVerifyChunk + e * kVerifyThreads + tid for e = 0 .. kPer - 1.
+// First entry of this lane in wave round `sub` (0 .. kSubs - 1, in the order of entries) of chunk c.
+__device__ __forceinline__ int entry_of(int c, int sub) { return c * kVerifyChunk + sub * kSub + 4 * (threadIdx.x & 63); }
+
+// The sums of the chunk's wave rounds, in LDS (a wave makes kRounds of them); a barrier makes them seen.
 template <class T>
-__device__ __forceinline__ double chunk_sum(const VerifyArgs &a, const Drawn<T> &r, bool rest, int c, double *red) {
-    double s = 0.0;
-    const int i0 = c * kVerifyChunk + threadIdx.x;
+__device__ __forceinline__ void sub_sums(const VerifyArgs &a, const Drawn<T> &r, bool rest, int c, double *subs) {
+    const int wave = threadIdx.x >> 6;
+    double m[kRounds][4];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        const int i = i0 + e * kVerifyThreads;
-        if (i < a.vocab) s += mass(r, rest, i);
+    for (int j = 0; j < kRounds; ++j) masses(a, r, rest, entry_of(c, wave * kRounds + j), m[j]);
+#pragma unroll
+    for (int j = 0; j < kRounds; ++j) {
+        const double s = wave_sum((m[j][0] + m[j][1]) + (m[j][2] + m[j][3]));
+        if ((threadIdx.x & 63) == 0) subs[wave * kRounds + j] = s;
     }
-    s = wave_sum(s);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
-    __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+__device__ __forceinline__ double sum_of(const double *subs) {
+    double s = 0.0;
+#pragma unroll
+    for (int j = 0; j < kSubs; ++j) s += subs[j];
+    return s;
 }
 
 template <class T>
 __global__ __launch_bounds__(kVerifyThreads) void verify_sums_kernel(VerifyArgs a) {
-    __shared__ double red[4];
+    __shared__ double subs[kSubs];
     const int b = blockIdx.y, c = blockIdx.x;
     const Drawn<T> r = accept<T>(a, b);
-    const double s = chunk_sum(a, r, r.refused, c, red);
-    if (threadIdx.x == 0) a.sums[(int64_t)b * a.chunks + c] = s;
+    sub_sums(a, r, r.refused, c, subs);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        a.sums[(int64_t)b * a.chunks + c] = sum_of(subs);
+        if (c == 0) a.found[2 * b] = r.n, a.found[2 * b + 1] = r.refused;
+    }
 }
 
-// First index of the workgroup's threads for which `hit` holds, or -1.
-__device__ __forceinline__ int first_hit(bool hit, int *red) {
-    const uint64_t w = __ballot(hit);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = w ? (int)threadIdx.x + __builtin_ctzll(w) : -1;
-    __syncthreads();
-    return red[0] >= 0 ? red[0] : red[1] >= 0 ? red[1] : red[2] >= 0 ? red[2] : red[3];
-}
-__device__ __forceinline__ int last_hit(bool hit, int *red) {
-    const uint64_t w = __ballot(hit);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = w ? (int)threadIdx.x + 63 - __builtin_clzll(w) : -1;
-    __syncthreads();
-    return red[3] >= 0 ? red[3] : red[2] >= 0 ? red[2] : red[1] >= 0 ? red[1] : red[0];
-}
-
-// Sum before this thread's value over the workgroup.
-__device__ __forceinline__ double before(double v, double *red) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Running sums over up to 64 lanes, and the first lane whose running sum exceeds the border (or, if none does, the last
+// with a positive value): that lane, or -1 if none is positive, and the sum before it.
+__device__ __forceinline__ int border_lane(double v, double run, double border, double &before, double &after) {
     double inc = v;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const double x = __shfl_up(inc, d);
-        if (lane >= d) inc += x;
+        if ((int)(threadIdx.x & 63) >= d) inc += x;
     }
-    __syncthreads();
-    if (lane == 63) red[wave] = inc;
-    __syncthreads();
-    double base = 0.0;
-    for (int w = 0; w < wave; ++w) base += red[w];
-    return base + (inc - v);
+    after = run + __shfl(inc, 63);
+    const uint64_t some = __ballot(v > 0.0), over = __ballot(v > 0.0 && run + inc > border);
+    const int lane = over ? __builtin_ctzll(over) : some ? 63 - __builtin_clzll(some) : -1;
+    before = lane < 0 ? run : run + __shfl(inc - v, lane < 0 ? 0 : lane);
+    return lane;
 }
 
 template <class T>
 __global__ __launch_bounds__(kVerifyThreads) void verify_draw_kernel(VerifyArgs a) {
-    __shared__ double red[4];
-    __shared__ int ired[4], found;
-    extern __shared__ double sums[];  // [chunks], then running sums
-    const int b = blockIdx.x, tid = threadIdx.x;
-    const Drawn<T> r = accept<T>(a, b);
-    bool rest = r.refused;
+    __shared__ double subs[kSubs];
+    extern __shared__ double sums[];  // [chunks]
+    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+    const int n = a.found[2 * b];
+    const Drawn<T> r = drawn_from<T>(a, b, n, a.found[2 * b + 1] != 0);
     for (int c = tid; c < a.chunks; c += kVerifyThreads) sums[c] = a.sums[(int64_t)b * a.chunks + c];
     __syncthreads();
-    double total = 0.0;
-    for (int c = 0; c < a.chunks; ++c) total += sums[c];
+    bool rest = r.refused;
+    double total = 0.0;  // every wave by itself, the same
+    for (int c0 = 0; c0 < a.chunks; c0 += 64) total += wave_sum(c0 + lane < a.chunks ? sums[c0 + lane] : 0.0);
     if (rest && total == 0.0) {  // nothing left after the draft's mass: the target's row itself
         rest = false;
         for (int c = 0; c < a.chunks; ++c) {
-            const double s = chunk_sum(a, r, rest, c, red);
-            if (tid == 0) sums[c] = s;
-            total += s;
+            sub_sums(a, r, rest, c, subs);
+            __syncthreads();
+            if (tid == 0) sums[c] = sum_of(subs);
+            __syncthreads();
         }
-        __syncthreads();
+        for (int c0 = 0; c0 < a.chunks; c0 += 64) total += wave_sum(c0 + lane < a.chunks ? sums[c0 + lane] : 0.0);
     }
     int token = -1;
     if (total > 0.0) {
         const double border = (double)a.sample_u[b] * total;
         // the first chunk whose running sum exceeds the border, else the last with mass
-        double run = 0.0, base = 0.0;
-        int at = -1;
-        for (int c = 0; c < a.chunks; ++c) {
-            if (sums[c] > 0.0) {
-                at = c;
-                base = run;
+        double run = 0.0, base = 0.0, before, after;
+        int chunk = -1;
+        for (int c0 = 0; c0 < a.chunks; c0 += 64) {
+            const int l = border_lane(c0 + lane < a.chunks ? sums[c0 + lane] : 0.0, run, border, before, after);
+            if (l >= 0) {
+                chunk = c0 + l;
+                base = before;
+                if (before + sums[chunk] > border) break;
             }
-            run += sums[c];
-            if (run > border) break;
+            run = after;
         }
-        // inside it: kPer neighbours a thread
-        double m[kPer], mine = 0.0;
-        const int i0 = at * kVerifyChunk + tid * kPer;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            m[e] = i0 + e < a.vocab ? mass(r, rest, i0 + e) : 0.0;
-            mine += m[e];
-        }
-        double cum = base + before(mine, red);
+        // in it the wave round, and in that the entry
+        sub_sums(a, r, rest, chunk, subs);
+        __syncthreads();
+        int l = border_lane(lane < kSubs ? subs[lane] : 0.0, base, border, before, after);
+        const int sub = l;
+        double m[4];
+        const int i = entry_of(chunk, sub);
+        masses(a, r, rest, i, m);
+        l = border_lane((m[0] + m[1]) + (m[2] + m[3]), before, border, before, after);
+        // the lane's own entry: the first over the border, else its last with mass (the sums' order can put the border
+        // past the last)
+        double cum = before;
         int hit = -1, last = -1;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
+        for (int e = 0; e < 4; ++e) {
             cum += m[e];
             if (m[e] > 0.0) {
                 if (hit < 0 && cum > border) hit = e;
                 last = e;
             }
         }
-        int who = first_hit(hit >= 0, ired);
-        if (who < 0) {  // the sums' order put the border past the chunk's last entry
-            who = last_hit(last >= 0, ired);
-            hit = last;
-        }
-        if (tid == who) found = i0 + hit;
-        __syncthreads();
-        token = found;
+        token = __shfl(i + (hit >= 0 ? hit : last), l);
     }
     for (int i = tid; i <= a.max_drafts; i += kVerifyThreads)
-        a.out_tokens[(int64_t)b * (a.max_drafts + 1) + i] =
-            i < r.n ? a.tokens[(int64_t)b * a.max_drafts + i] : i == r.n ? token : -1;
-    if (tid == 0) a.accepted[b] = r.n;
+        a.out_tokens[(int64_t)b * (a.max_drafts + 1) + i] = i < n ? a.tokens[(int64_t)b * a.max_drafts + i] : i == n ? token : -1;
+    if (tid == 0) a.accepted[b] = n;
 }
 
 template <class T>
