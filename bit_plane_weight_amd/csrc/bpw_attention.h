@@ -42,6 +42,31 @@ __device__ __forceinline__ f32x4 mma<_Float16>(u32v4 a, u32v4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// c + the sum of eight 16-bit weights, in float32.
+template <class T>
+__device__ __forceinline__ float sum8(u32v4 p, float c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = p[i];
+        if constexpr (__is_same(T, __bf16)) {
+            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+            c = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, x), bf16x2{(__bf16)1.0f, (__bf16)1.0f}, c, false);
+        } else {
+            typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+            c = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, x), f16x2{(_Float16)1.0f, (_Float16)1.0f}, c, false);
+        }
+    }
+    return c;
+}
+
+// Not zero if a 16-bit half of x is infinite or NaN (and for some finite ones above an infinite one).
+template <class T>
+__device__ __forceinline__ uint32_t maybe_not_finite(uint32_t x) {
+    constexpr uint32_t ones = __is_same(T, __bf16) ? 0x7F807F80u : 0x7C007C00u;
+    const uint32_t y = (x & ones) ^ ones;  // a half of zero: exponent all ones
+    return (y - 0x00010001u) & ~y & 0x80008000u;
+}
+
 // The work of one wave or workgroup on one item: positions [pos0, pos1) of a page list for a tile of query rows.
 struct AttnSpan {
     const int32_t *pages;
@@ -54,7 +79,7 @@ struct AttnSpan {
     int32_t n_rows;    // rows of all tiles
     int32_t pos0, pos1;
     float *po;         // results of the tile: [rows][DP]
-    float2 *pml;       // [rows]
+    float4 *pml;       // [rows]: shift (log2 units), sum of the weights, sum of the rounded weights
 };
 
 constexpr float kNone = -__builtin_inff();
@@ -132,11 +157,11 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s) {
     const T *vbase = static_cast<const T *>(a.v) + (int64_t)s.head * a.v_hs;
 
     f32x4 o[NQ][NH * EL];
-    float m[NQ], l[NQ];
+    float m[NQ], l[NQ], lr[NQ];
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
         m[i] = kNone;
-        l[i] = 0.0f;
+        l[i] = lr[i] = 0.0f;
 #pragma unroll
         for (int c = 0; c < NH * EL; ++c) o[i][c] = f32x4{0, 0, 0, 0};
     }
@@ -212,7 +237,9 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s) {
             load_keys(kv0, id0, k0);
             load_keys(kv0 + 16, id1, k1);
         }
+        bool odd = false;  // a value that only some rows see is not finite
         if (here + kAttnStep > all_see || (c0 | c1) < 0) {
+            uint32_t found = 0;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -227,8 +254,14 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s) {
                         for (int h = 0; h < NH; ++h)
 #pragma unroll
                             for (int w = 0; w < VW; ++w) v[4 * t + r][h][w] = 0;
+                    } else if (pos >= all_see) {
+#pragma unroll
+                        for (int h = 0; h < NH; ++h)
+#pragma unroll
+                            for (int w = 0; w < VW; ++w) found |= maybe_not_finite<T>(v[4 * t + r][h][w]);
                     }
                 }
+            odd = __any(found != 0);
         }
         u32v4 p[NQ];
 #pragma unroll
@@ -257,35 +290,72 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s) {
                 const float f = up == m[i] ? 1.0f : __builtin_amdgcn_exp2f(m[i] - up);
                 m[i] = up;
                 l[i] *= f;
+                lr[i] *= f;
 #pragma unroll
                 for (int c = 0; c < NH * EL; ++c) o[i][c] *= f;
                 weigh(up == kNone ? 0.0f : up);
             }
             l[i] += sum;
-            // weights in 16 bits: the matrix cores' operand. Its relative error of half a step is averaged
-            // over the positions; the sum l is of the unrounded weights.
+            // Weights in 16 bits: the matrix cores' operand. Half a step of relative error each, averaged over the
+            // positions; o is divided by the sum of the weights as rounded, so that errors that they share (weights
+            // nearly alike round alike) cancel. lse takes the sum of the unrounded ones.
             p[i] = __builtin_bit_cast(u32v4, __builtin_convertvector(w, typename Vec8<T>::type));
+            lr[i] = sum8<T>(p[i], lr[i]);
         }
+        // Tile c of V^T (elements 8 m + c of run h): two positions of one element from two words.
+        const auto turned = [&](int h, int c) {
+            u32v4 f;
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
+            for (int w = 0; w < 4; ++w)
+                f[w] = __builtin_amdgcn_perm(v[2 * w + 1][h][c >> 1], v[2 * w][h][c >> 1], c & 1 ? 0x07060302u : 0x05040100u);
+            return f;
+        };
+        if (!odd) {
 #pragma unroll
-            for (int c = 0; c < EL; ++c) {
-                u32v4 f;
-                const uint32_t sel = c & 1 ? 0x07060302u : 0x05040100u;
+            for (int h = 0; h < NH; ++h)
 #pragma unroll
-                for (int w = 0; w < 4; ++w) f[w] = __builtin_amdgcn_perm(v[2 * w + 1][h][c >> 1], v[2 * w][h][c >> 1], sel);
+                for (int c = 0; c < EL; ++c) {
+                    const u32v4 f = turned(h, c);
 #pragma unroll
-                for (int i = 0; i < NQ; ++i) o[i][h * EL + c] = mma<T>(f, p[i], o[i][h * EL + c]);
+                    for (int i = 0; i < NQ; ++i) o[i][h * EL + c] = mma<T>(f, p[i], o[i][h * EL + c]);
+                }
+        } else {
+            // One query token at a time, the last first: the values that it does not see are set to zero, and only its
+            // rows take the result.
+            const int last = min(s.n_tok, (s.row0 + 16 * NQ - 1) / a.group + 1);
+            for (int j = last - 1; j >= s.row0 / a.group; --j) {
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    if (here + 16 * (x >> 2) + 4 * g + (x & 3) >= s.len - (s.n_tok - 1 - j)) {
+#pragma unroll
+                        for (int h = 0; h < NH; ++h)
+#pragma unroll
+                            for (int w = 0; w < VW; ++w) v[x][h][w] = 0;
+                    }
+#pragma unroll
+                for (int h = 0; h < NH; ++h)
+#pragma unroll
+                    for (int c = 0; c < EL; ++c) {
+                        const u32v4 f = turned(h, c);
+#pragma unroll
+                        for (int i = 0; i < NQ; ++i) {
+                            const f32x4 x = mma<T>(f, p[i], o[i][h * EL + c]);
+                            if ((s.row0 + 16 * i + n) / a.group == j) o[i][h * EL + c] = x;
+                        }
+                    }
             }
+        }
     }
 
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
         l[i] += __shfl_xor(l[i], 16);
         l[i] += __shfl_xor(l[i], 32);
+        lr[i] += __shfl_xor(lr[i], 16);
+        lr[i] += __shfl_xor(lr[i], 32);
         const int row = 16 * i + n;
         if (s.row0 + row >= s.n_rows) continue;
-        if (g == 0) s.pml[row] = make_float2(m[i], l[i]);
+        if (g == 0) s.pml[row] = make_float4(m[i], l[i], lr[i], 0.0f);
         float *po = s.po + row * DP;
 #pragma unroll
         for (int h = 0; h < NH; ++h)
@@ -491,7 +561,7 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
     f32x16 o[DB];
 #pragma unroll
     for (int c = 0; c < DB; ++c) o[c] = f32x16{};
-    float m = kNone, l = 0.0f;
+    float m = kNone, l = 0.0f, lr = 0.0f;
 
     const int end = min(s.len, s.pos1);
     int pos0 = s.pos0;
@@ -579,6 +649,7 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
             const float f = up == m ? 1.0f : __builtin_amdgcn_exp2f(m - up);
             m = up;
             l *= f;
+            lr *= f;
 #pragma unroll
             for (int c = 0; c < DB; ++c) o[c] *= f;
             weigh(up == kNone ? 0.0f : up);
@@ -586,8 +657,10 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
         l += sum;
         u32v4 p[NB][2];
 #pragma unroll
-        for (int x = 0; x < 2 * NB; ++x)
+        for (int x = 0; x < 2 * NB; ++x) {
             p[x >> 1][x & 1] = __builtin_bit_cast(u32v4, __builtin_convertvector(w[x >> 1][x & 1], typename Vec8<T>::type));
+            lr = sum8<T>(p[x >> 1][x & 1], lr);
+        }
 #pragma unroll
         for (int x = 0; x < 2 * NB; ++x) {
             if (x + 1 < 2 * NB) read_v(x + 1, vf[(x + 1) & 1]);
@@ -606,11 +679,12 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
     }
 
     l += __shfl_xor(l, 32);
+    lr += __shfl_xor(lr, 32);
     if constexpr (PARTS == 2) {  // the second wave of the same rows hands over through LDS
         constexpr int PAD = DP + 4;
         float *box = reinterpret_cast<float *>(&lds) + (wave % WQ) * (32 * PAD);
-        float2 *ml = reinterpret_cast<float2 *>(reinterpret_cast<float *>(&lds) + WQ * 32 * PAD) + 32 * (wave % WQ);
-        static_assert((WQ * 32 * PAD + 2 * 32 * WQ) * 4 <= sizeof(WideLds<DP>), "the join fits the tiles' LDS");
+        float4 *ml = reinterpret_cast<float4 *>(reinterpret_cast<float *>(&lds) + WQ * 32 * PAD) + 32 * (wave % WQ);
+        static_assert((WQ * 32 * PAD + 4 * 32 * WQ) * 4 <= sizeof(WideLds<DP>), "the join fits the tiles' LDS");
         __syncthreads();
         if (part == 1) {
 #pragma unroll
@@ -619,15 +693,16 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
                 for (int r = 0; r < 4; ++r)
                     *reinterpret_cast<f32x4 *>(box + n * PAD + 32 * c + 8 * r + 4 * g) =
                         f32x4{o[c][4 * r], o[c][4 * r + 1], o[c][4 * r + 2], o[c][4 * r + 3]};
-            if (g == 0) ml[n] = make_float2(m, l);
+            if (g == 0) ml[n] = make_float4(m, l, lr, 0.0f);
         }
         __syncthreads();
         if (part == 0) {
-            const float2 x = ml[n];
+            const float4 x = ml[n];
             const float up = fmaxf(m, x.x);
             const float f0 = m == kNone ? 0.0f : __builtin_amdgcn_exp2f(m - up), f1 = x.x == kNone ? 0.0f : __builtin_amdgcn_exp2f(x.x - up);
             m = up;
             l = l * f0 + x.y * f1;
+            lr = lr * f0 + x.z * f1;
 #pragma unroll
             for (int c = 0; c < DB; ++c)
 #pragma unroll
@@ -640,7 +715,7 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
     }
     if (part == 0 && row < s.n_rows) {
         const int at = 32 * (wave % WQ) + n;
-        if (g == 0) s.pml[at] = make_float2(m, l);
+        if (g == 0) s.pml[at] = make_float4(m, l, lr, 0.0f);
         float *po = s.po + (int64_t)at * DP;
 #pragma unroll
         for (int c = 0; c < DB; ++c)
@@ -890,7 +965,7 @@ struct AttnParts {
             row_s = (int64_t)(before_i + item + w0) * ms + row - tile * ms;
         }
     }
-    __device__ __forceinline__ float2 ml(const AttnArgs &a, int k) const {
+    __device__ __forceinline__ float4 ml(const AttnArgs &a, int k) const {
         return k < np ? a.part_ml[row_p + (int64_t)k * step_p] : a.part_ml[a.ml_s + row_s + (int64_t)(k - np) * ms];
     }
     template <int DP>
@@ -901,11 +976,11 @@ struct AttnParts {
 
 // Four elements of a row of out, its lse. top: log2 units. A sum of zero: nothing seen. (NaN is not zero.)
 template <class T>
-__device__ __forceinline__ void write_out(const AttnArgs &a, int t, int hq, int d, f32x4 acc, float top, float sum) {
+__device__ __forceinline__ void write_out(const AttnArgs &a, int t, int hq, int d, f32x4 acc, float top, float sum, float rounded) {
     if (d < a.head_dim) {
         typedef T T4 __attribute__((ext_vector_type(4)));
         T *out = static_cast<T *>(a.out) + (int64_t)t * a.o_ts + (int64_t)hq * a.o_hs + d;
-        *reinterpret_cast<T4 *>(out) = __builtin_convertvector(acc * (sum == 0.0f ? 0.0f : 1.0f / sum), T4);
+        *reinterpret_cast<T4 *>(out) = __builtin_convertvector(acc * (sum == 0.0f ? 0.0f : 1.0f / rounded), T4);
     }
     if (d == 0 && a.lse)
         a.lse[(int64_t)t * a.q_heads + hq] = sum == 0.0f ? kNone : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
@@ -931,7 +1006,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int
     constexpr int LANES = DP / 4, GROUPS = kAttnThreads / LANES;
     __shared__ float weight[kAttnWaves * kAttnWgs + 2];
     __shared__ f32x4 sums[GROUPS][LANES];
-    __shared__ float red[2][kAttnWaves];
+    __shared__ float red[3][kAttnWaves];
     const int tid = threadIdx.x;
     const int hq = blockIdx.x % a.q_heads, bj = blockIdx.x / a.q_heads;
     const AttnParts p(a, mp, ms, bj / a.max_q, bj % a.max_q, hq);
@@ -950,17 +1025,20 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int
     if ((tid & 63) == 0) red[0][tid >> 6] = top;
     __syncthreads();
     top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    float sum = 0.0f;
+    float sum = 0.0f, rounded = 0.0f;
     for (int k = tid; k < parts; k += kAttnThreads) {
-        const float2 x = p.ml(a, k);
+        const float4 x = p.ml(a, k);
         const float f = x.x == kNone ? 0.0f : __builtin_amdgcn_exp2f(x.x - top);
         weight[k] = f;
         sum += x.x == kNone ? 0.0f : f * x.y;
+        rounded += x.x == kNone ? 0.0f : f * x.z;
     }
     sum = wave_add(sum);
-    if ((tid & 63) == 0) red[1][tid >> 6] = sum;
+    rounded = wave_add(rounded);
+    if ((tid & 63) == 0) red[1][tid >> 6] = sum, red[2][tid >> 6] = rounded;
     __syncthreads();
     sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    rounded = (red[2][0] + red[2][1]) + (red[2][2] + red[2][3]);
     f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -972,7 +1050,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int
     if (gr) return;
 #pragma unroll
     for (int y = 1; y < GROUPS; ++y) acc += sums[y][ln];
-    write_out<T>(a, p.t, hq, 4 * ln, acc, top, sum);
+    write_out<T>(a, p.t, hq, 4 * ln, acc, top, sum, rounded);
 }
 
 // Many rows, which have few parts each: one wave to a row, no barriers.
@@ -998,11 +1076,12 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_rows_kernel(AttnArgs a
     for (int k = lane; k < parts; k += 64) top = fmaxf(top, p.ml(a, k).x);
     top = wave_max(top);
     f32x4 acc = {0, 0, 0, 0};
-    float sum = 0.0f;
+    float sum = 0.0f, rounded = 0.0f;
     for (int k0 = 0; k0 < parts; k0 += 64) {
-        const float2 x = k0 + lane < parts ? p.ml(a, k0 + lane) : make_float2(kNone, 0.0f);
+        const float4 x = k0 + lane < parts ? p.ml(a, k0 + lane) : make_float4(kNone, 0.0f, 0.0f, 0.0f);
         const float f = x.x == kNone ? 0.0f : __builtin_amdgcn_exp2f(x.x - top);  // of part k0 + lane; 0 past the last
         sum += x.x == kNone ? 0.0f : f * x.y;
+        rounded += x.x == kNone ? 0.0f : f * x.z;
         const int n = min(64, parts - k0);
         for (int k = 0; k < n; k += 4 * GROUPS) {
             f32x4 z[4];
@@ -1017,11 +1096,12 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_rows_kernel(AttnArgs a
         }
     }
     sum = wave_add(sum);
+    rounded = wave_add(rounded);
 #pragma unroll
     for (int d = LANES; d < 64; d <<= 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor(acc[e], d);
-    if (gr == 0) write_out<T>(a, p.t, hq, 4 * ln, acc, top, sum);
+    if (gr == 0) write_out<T>(a, p.t, hq, 4 * ln, acc, top, sum, rounded);
 }
 
 template <class T, int DP, int MP, int MS>

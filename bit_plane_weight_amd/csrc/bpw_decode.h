@@ -68,9 +68,9 @@ struct AttnArgs {
     int32_t splits, split_units;  // of a wide prefix: equal pieces of an item, units of one
     // workspace
     int32_t *sched;          // kSchedHead words, then units before each sequence, then items before each
-    float *part_o;           // [pieces][rows of a tile][padded dim]
-    float2 *part_ml;         // [pieces][rows of a tile]: running maximum (log2 units) and sum
-    int64_t part_s;          // offset (floats) of the suffix pieces in part_o
+    float *part_o;           // [parts][rows of a tile][padded dim]
+    float4 *part_ml;         // [parts][rows of a tile]: shift (log2 units), sum of the weights, sum of the rounded ones
+    int64_t part_s;          // offset (floats) of the suffixes' parts in part_o
     int64_t ml_s;            // and in part_ml
 };
 constexpr int kSchedHead = 8;  // units of a prefix item, units of the two lengths of runs, runs of the first

@@ -307,7 +307,7 @@ bpw_status attn_shape(const bpw_attn_shared_prefix_args *a, AttnShape *s) {
     s->po = s->sched;
     const size_t rows = (size_t)(s->pieces_p * mp + s->pieces_s * ms);
     s->pml = s->po + up256(rows * (size_t)s->dp * 4);
-    s->total = s->pml + up256(rows * 8);
+    s->total = s->pml + up256(rows * 16);
     return BPW_OK;
 }
 
@@ -387,7 +387,7 @@ bpw_status bpw_attn_shared_prefix(const bpw_attn_shared_prefix_args *a, void *d_
     char *ws = static_cast<char *>(d_ws);
     k.sched = reinterpret_cast<int32_t *>(ws);
     k.part_o = reinterpret_cast<float *>(ws + s.po);
-    k.part_ml = reinterpret_cast<float2 *>(ws + s.pml);
+    k.part_ml = reinterpret_cast<float4 *>(ws + s.pml);
     k.part_s = s.pieces_p * s.mp * s.dp;
     k.ml_s = s.pieces_p * s.mp;
     const int e = s.dp == 64    ? bpw::launch_attn_d64(k, c.dtype, s.mp, s.ms, stream)

@@ -382,6 +382,33 @@ def test_attention_nan_and_infinity_where_seen(dev):
     assert torch.isnan(got[0, :2]).all() and not torch.isnan(got[0, 2:]).any() and not torch.isnan(got[1]).any()
 
 
+@pytest.mark.parametrize("Hq,Hk,D,n,dt", [(3, 1, 64, 5, BF16), (8, 2, 128, 3, F16), (12, 2, 80, 7, BF16), (4, 4, 256, 9, F16)])
+def test_attention_values_that_are_not_finite_in_later_drafts(dev, Hq, Hk, D, n, dt):
+    """NaN and infinities in the values of drafts: the tokens before them are as without, the others show them.
+    The drafts lie across the end of a 32-position step."""
+    a = Attn(dev, [n, 2], [32 + n // 2, 40], Hq, Hk, D, 16, 21, dt, seed=D + n)
+    L = a.lens[0]
+    a.plan().run()
+    clean = a.out.clone()
+    row = lambda pos: (a.table[0, pos // 16].long(), slice(None), pos % 16)  # noqa: E731
+    a.v[row(L - 1)] = float("nan")
+    a.v[row(L - 2)] = float("inf")
+    a.plan().run()
+    torch.cuda.synchronize()
+    got = a.out.float()
+    assert torch.equal(a.out[n:].view(torch.int16), clean[n:].view(torch.int16))  # the other sequence
+    keep = n - 2  # tokens that see neither
+    assert torch.isfinite(got[:keep]).all() and not torch.isfinite(got[n - 2]).any() and torch.isnan(got[n - 1]).all()
+    a.out = a.out[:keep]
+    a.lse, a.q = a.lse[:keep], a.q[:keep]  # the reference of those alone: drafts they do not see cut off
+    a.n_q, a.lens = [keep], [L - 2]
+    a.table, a.len_t = a.table[:1], torch.tensor([L - 2], dtype=torch.int32, device=dev)
+    a.starts = torch.tensor([0, keep], dtype=torch.int32, device=dev)
+    a.v[row(L - 1)] = float("nan")
+    a.v[row(L - 2)] = float("nan")
+    a.check()
+
+
 def test_attention_offsets_past_32_bits(dev):
     """Pages further apart than 2^31 elements."""
     P, Hk, D, far = 16, 2, 64, 2 ** 31 + 4096
