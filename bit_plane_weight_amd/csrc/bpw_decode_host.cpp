@@ -276,7 +276,7 @@ bpw_status attn_shape(const bpw_attn_shared_prefix_args *a, AttnShape *s) {
     const int64_t us = (s->cap + bpw::kAttnStep - 1) / bpw::kAttnStep;
     const int64_t items_p = c.kv_heads * tiles_p, items_s = (int64_t)a->n_seqs * c.kv_heads * tiles_s;
     const double work = (double)items_p * (double)up + (double)items_s * (double)us;
-    if (work >= 2.0e9 || (double)a->n_seqs * (double)max_q * a->q.heads >= 2.0e9)
+    if (work >= 2.0e9 || rows_p * c.kv_heads >= INT32_MAX || (double)a->n_seqs * (double)max_q * a->q.heads >= 2.0e9)
         return fail(BPW_E_UNSUPPORTED, "%s: more work than one launch deals out", who);
     s->tiles_p = (int32_t)tiles_p;
     const int64_t most = items_p * up + items_s * us;

@@ -489,6 +489,26 @@ def test_step_in_a_graph(dev):
         assert torch.equal(got.view(torch.int16), a.out.view(torch.int16))
 
 
+def test_attention_most_sequences(dev):
+    """The most sequences a call takes, with the largest tables in LDS beside the largest tiles."""
+    n = 1024
+    a = Attn(dev, [1] * n, [1 + i % 3 for i in range(n)], 2, 1, 256, 16, 130, BF16, seed=31)
+    a.plan().run()
+    torch.cuda.synchronize()
+    a.check()
+
+
+def test_speculative_step_example(dev):
+    """The operators together, from ternary projections to accepted tokens."""
+    import importlib.util
+    import os
+    from conftest import ROOT
+    spec = importlib.util.spec_from_file_location("speculative_step", os.path.join(ROOT, "examples", "speculative_step.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.main(["--sequences", "4", "--drafts", "3", "--prefix", "200", "--suffix", "40", "--check"])
+
+
 # ------------------------------------------------------------------------------ draft verification
 
 
