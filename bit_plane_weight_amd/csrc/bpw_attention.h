@@ -803,13 +803,8 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_ke
         su += un[x];
         si += it[x];
     }
-    int iu = su, ii = si;
-    for (int d = 1; d < 64 && 4 * d < a.n_seqs; d <<= 1) {  // (few sequences: few lanes hold any)
-        const int x = __shfl_up(iu, d), y = __shfl_up(ii, d);
-        if (lane >= d) iu += x, ii += y;
-    }
-    const int top_lane = min(63, (a.n_seqs - 1) / 4);  // (a first wave alone where the scan was cut short)
-    if (lane == top_lane) wave_sum[wave][0] = wave && top_lane < 63 ? 0 : iu, wave_sum[wave][1] = wave && top_lane < 63 ? 0 : ii;
+    int iu = scan_add(su), ii = scan_add(si);
+    if (lane == 63) wave_sum[wave][0] = iu, wave_sum[wave][1] = ii;
     __syncthreads();
     int total_s = 0, items_s = 0;
 #pragma unroll
@@ -984,17 +979,6 @@ __device__ __forceinline__ void write_out(const AttnArgs &a, int t, int hq, int 
     }
     if (d == 0 && a.lse)
         a.lse[(int64_t)t * a.q_heads + hq] = sum == 0.0f ? kNone : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
-}
-
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) x = fmaxf(x, __shfl_xor(x, d));
-    return x;
-}
-__device__ __forceinline__ float wave_add(float x) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
-    return x;
 }
 
 constexpr int kJoinRows = 1024;

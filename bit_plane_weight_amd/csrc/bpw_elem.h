@@ -58,4 +58,58 @@ __device__ __forceinline__ void store8(T *p, f32x8 x) {
     }
 }
 
+// Cross-lane steps by DPP: a few cycles each, where a shuffle through LDS costs a round trip.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ int dpp(int x) {  // 0 where a lane has no source
+    return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float dpp(float x) {
+    return __builtin_bit_cast(float, dpp<CTRL, ROWS>(__builtin_bit_cast(int, x)));
+}
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ double dpp(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = dpp<CTRL, ROWS>((int)(uint32_t)u), hi = dpp<CTRL, ROWS>((int)(uint32_t)(u >> 32));
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ float read_lane(float x, int l) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), l));
+}
+__device__ __forceinline__ double read_lane(double x, int l) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, l), hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), l);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// Sums over lanes 0 .. l in lane l: shifts by 1, 2, 4, 8 within rows of 16, then the last lane of a row to the next one,
+// and lane 31 to the upper half.
+template <class V>
+__device__ __forceinline__ V scan_add(V x) {
+    x += dpp<0x111>(x);
+    x += dpp<0x112>(x);
+    x += dpp<0x114>(x);
+    x += dpp<0x118>(x);
+    x += dpp<0x142, 0xA>(x);
+    x += dpp<0x143, 0xC>(x);
+    return x;
+}
+
+// Maximum and sum over the wave, in every lane: pairs, quads, mirrored eights and sixteens, then the four rows.
+__device__ __forceinline__ float wave_max(float x) {
+    x = fmaxf(x, dpp<0xB1>(x));
+    x = fmaxf(x, dpp<0x4E>(x));
+    x = fmaxf(x, dpp<0x141>(x));
+    x = fmaxf(x, dpp<0x140>(x));
+    return fmaxf(fmaxf(read_lane(x, 0), read_lane(x, 16)), fmaxf(read_lane(x, 32), read_lane(x, 48)));
+}
+template <class V>
+__device__ __forceinline__ V wave_add(V x) {
+    x += dpp<0xB1>(x);
+    x += dpp<0x4E>(x);
+    x += dpp<0x141>(x);
+    x += dpp<0x140>(x);
+    return (read_lane(x, 0) + read_lane(x, 16)) + (read_lane(x, 32) + read_lane(x, 48));
+}
+
 }  // namespace bpw

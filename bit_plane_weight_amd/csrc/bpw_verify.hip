@@ -54,7 +54,7 @@ __device__ __forceinline__ Drawn<T> accept(const VerifyArgs &a, int b) {
     Drawn<T> r;
     r.n = no ? min((int)__builtin_ctzll(no), most) : most;
     r.refused = r.n < most;
-    r.x = __shfl(x, r.n & 63);
+    r.x = __builtin_amdgcn_readlane(x, r.n & 63);
     r.p = t + r.n * a.t_step;
     r.q = r.refused && a.draft ? d + r.n * a.d_step : nullptr;
     return r;
@@ -99,12 +99,6 @@ __device__ __forceinline__ void masses(const VerifyArgs &a, const Drawn<T> &r, b
     }
 }
 
-__device__ __forceinline__ double wave_sum(double s) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
-    return s;
-}
-
 // First entry of this lane in wave round `sub` (0 .. kSubs - 1, in the order of entries) of chunk c.
 __device__ __forceinline__ int entry_of(int c, int sub) { return c * kVerifyChunk + sub * kSub + 4 * (threadIdx.x & 63); }
 
@@ -117,7 +111,7 @@ __device__ __forceinline__ void sub_sums(const VerifyArgs &a, const Drawn<T> &r,
     for (int j = 0; j < kRounds; ++j) masses(a, r, rest, entry_of(c, wave * kRounds + j), m[j]);
 #pragma unroll
     for (int j = 0; j < kRounds; ++j) {
-        const double s = wave_sum((m[j][0] + m[j][1]) + (m[j][2] + m[j][3]));
+        const double s = wave_add((m[j][0] + m[j][1]) + (m[j][2] + m[j][3]));
         if ((threadIdx.x & 63) == 0) subs[wave * kRounds + j] = s;
     }
 }
@@ -145,16 +139,11 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_sums_kernel(VerifyArgs 
 // Running sums over up to 64 lanes, and the first lane whose running sum exceeds the border (or, if none does, the last
 // with a positive value): that lane, or -1 if none is positive, and the sum before it.
 __device__ __forceinline__ int border_lane(double v, double run, double border, double &before, double &after) {
-    double inc = v;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double x = __shfl_up(inc, d);
-        if ((int)(threadIdx.x & 63) >= d) inc += x;
-    }
-    after = run + __shfl(inc, 63);
+    const double inc = scan_add(v);
+    after = run + read_lane(inc, 63);
     const uint64_t some = __ballot(v > 0.0), over = __ballot(v > 0.0 && run + inc > border);
     const int lane = over ? __builtin_ctzll(over) : some ? 63 - __builtin_clzll(some) : -1;
-    before = lane < 0 ? run : run + __shfl(inc - v, lane < 0 ? 0 : lane);
+    before = lane < 0 ? run : run + read_lane(inc - v, lane < 0 ? 0 : lane);
     return lane;
 }
 
@@ -169,7 +158,7 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_draw_kernel(VerifyArgs 
     __syncthreads();
     bool rest = r.refused;
     double total = 0.0;  // every wave by itself, the same
-    for (int c0 = 0; c0 < a.chunks; c0 += 64) total += wave_sum(c0 + lane < a.chunks ? sums[c0 + lane] : 0.0);
+    for (int c0 = 0; c0 < a.chunks; c0 += 64) total += wave_add(c0 + lane < a.chunks ? sums[c0 + lane] : 0.0);
     if (rest && total == 0.0) {  // nothing left after the draft's mass: the target's row itself
         rest = false;
         for (int c = 0; c < a.chunks; ++c) {
@@ -178,7 +167,7 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_draw_kernel(VerifyArgs 
             if (tid == 0) sums[c] = sum_of(subs);
             __syncthreads();
         }
-        for (int c0 = 0; c0 < a.chunks; c0 += 64) total += wave_sum(c0 + lane < a.chunks ? sums[c0 + lane] : 0.0);
+        for (int c0 = 0; c0 < a.chunks; c0 += 64) total += wave_add(c0 + lane < a.chunks ? sums[c0 + lane] : 0.0);
     }
     int token = -1;
     if (total > 0.0) {
@@ -216,7 +205,7 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_draw_kernel(VerifyArgs 
                 last = e;
             }
         }
-        token = __shfl(i + (hit >= 0 ? hit : last), l);
+        token = __builtin_amdgcn_readlane(i + (hit >= 0 ? hit : last), l);
     }
     for (int i = tid; i <= a.max_drafts; i += kVerifyThreads)
         a.out_tokens[(int64_t)b * (a.max_drafts + 1) + i] = i < n ? a.tokens[(int64_t)b * a.max_drafts + i] : i == n ? token : -1;
