@@ -392,7 +392,7 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
 // Costs for the dealing, in steps of one suffix wave: a tile of the prefix, and what an item costs beyond its steps.
-constexpr float kWideCost64 = 0.8f, kWideCost128 = 1.0f, kItemCost = 4.0f;
+constexpr float kWideCost64 = 0.5f, kWideCost128 = 0.6f, kItemCost = 4.0f;
 
 template <class T>
 __device__ __forceinline__ f32x16 mma32(u32v4 a, u32v4 b, f32x16 c);
@@ -753,6 +753,18 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_ke
     AttnSeqs seqs(dynamic, a.n_seqs);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
+    // The sequences' tokens and lengths, read ahead of everything else (each thread reads back its own).
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int b = 4 * tid + x;
+        if (b < a.n_seqs) {
+            const int2 tok = seq_tokens(a, b);
+            seqs.tok0[b] = tok.x;
+            seqs.n_tok[b] = tok.y;
+            seqs.len[b] = seq_len(a, b);
+        }
+    }
+
     AttnSpan s;
     s.pages = a.prefix_pages;
     s.len = a.prefix_len;
@@ -792,13 +804,9 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_ke
         const int b = 4 * tid + x;
         un[x] = it[x] = 0;
         if (b < a.n_seqs) {
-            const int2 tok = seq_tokens(a, b);
-            const int len = seq_len(a, b), u = (len + kAttnStep - 1) / kAttnStep;
-            it[x] = u > 0 ? a.kv_heads * ((tok.y * a.group + MS - 1) / MS) : 0;
+            const int u = (seqs.len[b] + kAttnStep - 1) / kAttnStep;
+            it[x] = u > 0 ? a.kv_heads * ((seqs.n_tok[b] * a.group + MS - 1) / MS) : 0;
             un[x] = it[x] * u;
-            seqs.tok0[b] = tok.x;
-            seqs.n_tok[b] = tok.y;
-            seqs.len[b] = len;
         }
         su += un[x];
         si += it[x];

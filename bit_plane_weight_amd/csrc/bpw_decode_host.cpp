@@ -231,7 +231,8 @@ struct AttnShape {
 // 8 x 64 32-row heads over 1000 positions, 49 k: 17.1, 19.5; 5 x 64 rows of 128 over 512, 20 k: 15.0, 15.9; over 2048,
 // 82 k: 19.3, 17.4; over 4096, 164 k: 27.4, 20.2; 4 x 128 rows of 256 over 1024, 131 k: 41.5, 34.4.
 constexpr int64_t kNarrowWork = 65536;
-constexpr int64_t kPieceCost = 3;  // tiles that one more piece of a wide prefix costs (queries in, parts out)
+constexpr int64_t kPieceCost = 3;   // tiles that a piece of a wide prefix costs beyond its own (queries in, parts out)
+constexpr int64_t kBusyCost = 32;   // tiles that all workgroups being busy with pieces costs
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -283,14 +284,17 @@ bpw_status attn_shape(const bpw_attn_shared_prefix_args *a, AttnShape *s) {
     s->n_wgs = (int32_t)(most < 2 ? 2 : most < bpw::kAttnWgs ? most : bpw::kAttnWgs);
     s->splits = s->split_units = 0;
     if (mp > 32) {
-        // Pieces of a wide prefix: items cut alike, in as many as end soonest (whole turns of all workgroups),
-        // counting for each piece what it costs beyond its tiles.
+        // Pieces of a wide prefix: items cut alike, in as many as end soonest: whole turns of all workgroups, each
+        // piece costing some tiles beyond its own, and workgroups with a piece being lost to the suffixes (and to
+        // memory traffic) meanwhile. Measured without that last term, us a call, 64 sequences of 20 + 5 heads of 128
+        // over a prefix of 4096 with some 1000 positions each: 60.6 (320 pieces), with it 56.6 (110); over 16384:
+        // 72.6 (430), 59.9 (200).
         s->n_wgs = (s->n_wgs + 7) / 8 * 8;
         const int64_t tiles = (a->prefix_len + bpw::kWideTile - 1) / bpw::kWideTile;
         int64_t best = INT64_MAX;
         for (int64_t n = 1; n <= tiles && n <= 64; ++n) {
             const int64_t turns = (items_p * n + s->n_wgs - 1) / s->n_wgs, len = (tiles + n - 1) / n;
-            const int64_t cost = turns * (len + kPieceCost);
+            const int64_t cost = turns * (len + kPieceCost) * s->n_wgs + kBusyCost * items_p * n;
             if (cost < best) {
                 best = cost;
                 s->splits = (int32_t)n;
