@@ -576,98 +576,119 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
         __syncthreads();  // this tile is there, and nobody reads the one before it any more
         if (pos0 + kWideTile < end) seen_next = issue(buf ^ 1, pos0 + kWideTile);
 
-        // Operands are read from LDS a group of products ahead: the reads of group x + 1 run under the products
-        // of group x (the scheduling barriers keep the compiler from sinking each read to its use).
+        // The tile's blocks of 32 positions, one after another: a block's weights are formed beside the products of
+        // the next block's scores and of the last block's values, which wait for nothing of them. Operands are read
+        // from LDS a group of products ahead.
+        constexpr int GK = 4, NGB = KC / GK, NG = NB * NGB;
         f32x16 sc[NB];
-        {
-            constexpr int GK = 4, NG = NB * KC / GK;
-            u32v4 kf[2][GK];
-            auto read_k = [&](int x, u32v4 (&f)[GK]) {
-                const uint8_t *p = &lds.k[buf][(part * NB + x * GK / KC) * 32 * ROW];
+        u32v4 kf[2][GK], vf[2][DB], p[NB][2];
+        const auto read_k = [&](int x) {
+            const uint8_t *q0 = &lds.k[buf][(part * NB + x / NGB) * 32 * ROW];
 #pragma unroll
-                for (int c = 0; c < GK; ++c) f[c] = *reinterpret_cast<const u32v4 *>(p + ka[(x * GK + c) % KC]);
-            };
-            read_k(0, kf[0]);
-#pragma unroll
-            for (int x = 0; x < NG; ++x) {
-                if (x + 1 < NG) read_k(x + 1, kf[(x + 1) & 1]);
-                __builtin_amdgcn_sched_barrier(0);
-                const int b = x * GK / KC;
-                if (x * GK % KC == 0) sc[b] = f32x16{};
-#pragma unroll
-                for (int c = 0; c < GK; ++c) sc[b] = mma32<T>(kf[x & 1][c], q[(x * GK + c) % KC], sc[b]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-        u32v4 vf[2][DB];
-        auto read_v = [&](int x, u32v4 (&f)[DB]) {  // positions 16 x .. 16 x + 15 of this wave's blocks
-            const uint8_t *vp = &lds.v[buf][(32 * part * NB + 16 * x) * ROW];
+            for (int c = 0; c < GK; ++c) kf[x & 1][c] = *reinterpret_cast<const u32v4 *>(q0 + ka[(x * GK + c) % KC]);
+        };
+        const auto read_v = [&](int x) {  // positions 16 x .. 16 x + 15 of this wave's blocks
+            const uint8_t *v0 = &lds.v[buf][(32 * part * NB + 16 * x) * ROW];
 #pragma unroll
             for (int c = 0; c < DB; ++c) {
-                const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds_u8 *)(vp + va[c][0])));
-                const u32x2 z = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds_u8 *)(vp + va[c][1])));
-                f[c] = u32v4{y.x, y.y, z.x, z.y};
+                const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds_u8 *)(v0 + va[c][0])));
+                const u32x2 z = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds_u8 *)(v0 + va[c][1])));
+                vf[x & 1][c] = u32v4{y.x, y.y, z.x, z.y};
             }
         };
-        read_v(0, vf[0]);
-        __builtin_amdgcn_sched_barrier(0);
-        if (hidden) {
+        const auto scores = [&](int b) {
+            sc[b] = f32x16{};
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+            for (int x = b * NGB; x < (b + 1) * NGB; ++x) {
+                if (x + 1 < NG) read_k(x + 1);
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int at = 32 * (part * NB + b) + 8 * (r >> 2) + 4 * g + (r & 3);
-                    if (pos0 + at >= s.len || !((seen >> (at >> 4)) & 1)) sc[b][r] = kNone;
-                }
-        }
-        f32x8 w[NB][2];
-        float sum = 0.0f;
-        const auto weigh = [&](float shift) {
-            float part_sum[2 * NB];
+                for (int c = 0; c < GK; ++c) sc[b] = mma32<T>(kf[x & 1][c], q[(x * GK + c) % KC], sc[b]);
+            }
+        };
+        const auto values = [&](int b) {
 #pragma unroll
-            for (int x = 0; x < 2 * NB; ++x) {
-                part_sum[x] = 0.0f;
+            for (int x = 2 * b; x < 2 * b + 2; ++x) {
+                if (x + 1 < 2 * NB) read_v(x + 1);
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[x >> 1][8 * (x & 1) + r], a.scale_log2, -shift));
-                    w[x >> 1][x & 1][r] = e;
-                    part_sum[x] += e;
-                }
+                for (int c = 0; c < DB; ++c) o[c] = mma32<T>(vf[x & 1][c], p[b][x & 1], o[c]);
+            }
+        };
+        f32x8 w[2];
+        float sum;
+        const auto hide = [&](int b) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int at = 32 * (part * NB + b) + 8 * (r >> 2) + 4 * g + (r & 3);
+                if (pos0 + at >= s.len || !((seen >> (at >> 4)) & 1)) sc[b][r] = kNone;
+            }
+        };
+        const auto weigh = [&](int b, float shift) {
+            float part_sum[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][r], a.scale_log2, -shift));
+                w[r >> 3][r & 7] = e;
+                part_sum[r >> 3] += e;
             }
             sum = part_sum[0] + part_sum[1];
-            if constexpr (NB == 2) sum += part_sum[2] + part_sum[3];
         };
-        weigh(m);
-        if (__any(!(sum < kShiftLimit))) {  // as in the register path
-            float top = kNone;
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
+        const auto settle = [&](int b) {  // the shift raised where it has to be, as in the narrow path; weights in 16 bits
+            if (__any(!(sum < kShiftLimit))) {
+                float top = kNone;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[b][r]);
-            top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
-            const float up = fmaxf(m, top);
-            const float f = up == m ? 1.0f : __builtin_amdgcn_exp2f(m - up);
-            m = up;
-            l *= f;
-            lr *= f;
+                top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
+                const float up = fmaxf(m, top);
+                const float f = up == m ? 1.0f : __builtin_amdgcn_exp2f(m - up);
+                m = up;
+                l *= f;
+                lr *= f;
 #pragma unroll
-            for (int c = 0; c < DB; ++c) o[c] *= f;
-            weigh(up == kNone ? 0.0f : up);
-        }
-        l += sum;
-        u32v4 p[NB][2];
+                for (int c = 0; c < DB; ++c) o[c] *= f;
+                weigh(b, up == kNone ? 0.0f : up);
+            }
+            l += sum;
 #pragma unroll
-        for (int x = 0; x < 2 * NB; ++x) {
-            p[x >> 1][x & 1] = __builtin_bit_cast(u32v4, __builtin_convertvector(w[x >> 1][x & 1], typename Vec8<T>::type));
-            lr = sum8<T>(p[x >> 1][x & 1], lr);
-        }
+            for (int h = 0; h < 2; ++h) {
+                p[b][h] = __builtin_bit_cast(u32v4, __builtin_convertvector(w[h], typename Vec8<T>::type));
+                lr = sum8<T>(p[b][h], lr);
+            }
+        };
+        // Where a SIMD holds one wave (DP = 256): one product, then VALU instructions that issue while it runs. A wave
+        // issues in order, so the order in the program is what overlaps: 102 us with it, 114 without (64 tokens of
+        // 32 heads over 16384 positions). With two waves a SIMD the other one fills in: 179 us without it, 185 with.
+        const auto alternate = [](auto products) {
+            if constexpr (DP > 128) {
 #pragma unroll
-        for (int x = 0; x < 2 * NB; ++x) {
-            if (x + 1 < 2 * NB) read_v(x + 1, vf[(x + 1) & 1]);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int c = 0; c < DB; ++c) o[c] = mma32<T>(vf[x & 1][c], p[x >> 1][x & 1], o[c]);
-            __builtin_amdgcn_sched_barrier(0);
+                for (int i = 0; i < decltype(products)::value; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 7, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        read_k(0);
+        scores(0);
+        read_v(0);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (NB == 2) {
+            if (hidden) hide(0);
+            weigh(0, m);
+            scores(1);
+            alternate(std::integral_constant<int, KC>{});
+            settle(0);
+            if (hidden) hide(1);
+            values(0);
+            weigh(1, m);
+            alternate(std::integral_constant<int, 2 * DB>{});
+            settle(1);
+            values(1);
+        } else {
+            if (hidden) hide(0);
+            weigh(0, m);
+            settle(0);
+            values(0);
         }
         pos0 += kWideTile;
     };
