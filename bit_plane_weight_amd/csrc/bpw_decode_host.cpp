@@ -226,10 +226,10 @@ struct AttnShape {
     size_t sched, po, pml, total;  // workspace: bytes of the schedule, offsets of the parts, all
 };
 
-// Most work (steps of single waves x padded head size) that a prefix of many rows is given to single waves, whose
-// first results come sooner; beyond it workgroups share the keys. Measured, us a call (waves, workgroups), steps x size:
-// 8 x 64 32-row heads over 1000 positions, 49 k: 17.1, 19.5; 5 x 64 rows of 128 over 512, 20 k: 15.0, 15.9; over 2048,
-// 82 k: 19.3, 17.4; over 4096, 164 k: 27.4, 20.2; 4 x 128 rows of 256 over 1024, 131 k: 41.5, 34.4.
+// Most work (steps of single waves x padded head size) that a prefix of more than 16 rows is given to single waves,
+// whose first results come sooner; beyond it workgroups share the keys through LDS. Measured, us a call (waves, workgroups):
+// 8 x 96 rows of 64 over 1000 positions, 49 k: 16.6, 19.5; 8 x 32 rows of 128 over 2000, 129 k: 18.1, 15.7; 5 x 64 rows of
+// 128 over 1024, 82 k: 16.8, 15.1; 8 x 32 rows of 64 over 8000, 128 k: 17.9, 16.1.
 constexpr int64_t kNarrowWork = 65536;
 constexpr int64_t kPieceCost = 3;   // tiles that a piece of a wide prefix costs beyond its own (queries in, parts out)
 constexpr int64_t kBusyCost = 32;   // tiles that all workgroups being busy with pieces costs
@@ -259,17 +259,18 @@ bpw_status attn_shape(const bpw_attn_shared_prefix_args *a, AttnShape *s) {
     s->group = a->q.heads / c.kv_heads;
     s->dp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
     s->cap = (int64_t)a->max_pages * c.page_size;
-    // Tiles of 16 query rows that one workgroup holds: enough for the rows that share a segment's keys, up
-    // to what the registers hold.
+    // Query rows of a tile: 16 of a suffix's (32 for heads of up to 64), or of a prefix that few rows share or that is
+    // little work; else 64 or 128 rows share a prefix's keys through LDS.
     const int64_t rows_p = (int64_t)a->n_tokens * s->group;
     const int64_t max_q = a->max_q < a->n_tokens ? a->max_q : (a->n_tokens > 0 ? a->n_tokens : 1);
     const int64_t rows_s = max_q * s->group;
-    s->ms = rows_s <= 16 ? 16 : 32;
+    s->ms = rows_s <= 16 || s->dp > 64 ? 16 : 32;
     const int64_t up = (a->prefix_len + bpw::kAttnStep - 1) / bpw::kAttnStep;
+    const int narrow = s->dp > 64 ? 16 : 32;
     if (a->prefix_len == 0 || rows_p <= s->ms)
         s->mp = s->ms;
-    else if (rows_p <= 32 || c.kv_heads * ((rows_p + 31) / 32) * up * s->dp <= kNarrowWork)
-        s->mp = 32;
+    else if (rows_p <= 16 || c.kv_heads * ((rows_p + narrow - 1) / narrow) * up * s->dp <= kNarrowWork)
+        s->mp = narrow;
     else
         s->mp = rows_p <= 64 ? 64 : 128;
     const int64_t mp = s->mp, ms = s->ms;
