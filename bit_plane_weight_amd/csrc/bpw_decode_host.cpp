@@ -336,7 +336,8 @@ bpw_status bpw_attn_shared_prefix(const bpw_attn_shared_prefix_args *a, void *d_
     if (a->q.heads != a->out.heads) return fail(BPW_E_INVAL, "%s: out has another head count than q", who);
     if (a->q.dtype != c.dtype || a->out.dtype != c.dtype)
         return fail(BPW_E_UNSUPPORTED, "%s: q and out need the cache's type", who);
-    if (!(std::isfinite(a->scale) && a->scale > 0.0f)) return fail(BPW_E_INVAL, "%s: scale is not finite and positive", who);
+    const float scale_log2 = a->scale * 1.44269504088896341f;  // scores in units of log 2: v_exp_f32 is 2^x
+    if (!(std::isfinite(scale_log2) && scale_log2 > 0.0f)) return fail(BPW_E_INVAL, "%s: scale is not finite and positive", who);
     if (!wide(a->q.d, c.dtype, a->q.token_stride, a->q.head_stride, 0) ||
         !wide(a->out.d, c.dtype, a->out.token_stride, a->out.head_stride, 0) ||
         !wide(c.d_k, c.dtype, c.k_page_stride, c.k_head_stride, c.k_row_stride) ||
@@ -384,7 +385,7 @@ bpw_status bpw_attn_shared_prefix(const bpw_attn_shared_prefix_args *a, void *d_
     k.n_pages = c.n_pages;
     k.prefix_len = (int32_t)a->prefix_len;
     k.cap = (int32_t)s.cap;
-    k.scale_log2 = a->scale * 1.44269504088896341f;  // scores in units of log 2: v_exp_f32 is 2^x
+    k.scale_log2 = scale_log2;
     k.n_wgs = s.n_wgs;
     k.tiles_p = s.tiles_p;
     k.splits = s.splits;

@@ -7,7 +7,8 @@
 // Differences of float32 are formed and summed in float64: a running sum of 128256 float32 in float32
 // would move the border by thousands of steps.
 //
-// Bound: HBM, one row of p and one of q per sequence; for one sequence the two launches. A row is cut into
+// Bound: HBM, one row of p and one of q per sequence (64 sequences of 128256 entries: 65.7 MB in 13 us, after two
+// dependent gathers), then the draw's latency (7.6 us; 4.4 for one sequence). A row is cut into
 // chunks of kVerifyChunk entries, one workgroup each, so that one sequence's rows are read by many CUs;
 // the second launch (one workgroup per sequence) finds the chunk that holds the border from the chunks' sums
 // and walks that chunk alone. Sums have a fixed order whatever the launch: a lane's four neighbours, the lanes of

@@ -489,6 +489,15 @@ def test_step_in_a_graph(dev):
         assert torch.equal(got.view(torch.int16), a.out.view(torch.int16))
 
 
+@pytest.mark.parametrize("n", [3, 60])
+def test_attention_without_own_positions(dev, n):
+    """A page table of no columns: the prefix is all there is."""
+    a = Attn(dev, [1] * n, [0] * n, 8, 4, 64, 32, 75, F16, seed=37, max_pages=0)
+    a.plan().run()
+    torch.cuda.synchronize()
+    a.check()
+
+
 def test_attention_most_sequences(dev):
     """The most sequences a call takes, with the largest tables in LDS beside the largest tiles."""
     n = 1024
