@@ -148,6 +148,37 @@ __device__ __forceinline__ int border_lane(double v, double run, double border, 
     return lane;
 }
 
+// The last token of a sequence: the first entry whose running sum exceeds the border, from the wave round that holds it
+// and the sum before that round. Every wave by itself, the same.
+template <class T>
+__device__ __forceinline__ int entry_in(const VerifyArgs &a, const Drawn<T> &r, bool rest, int c, int sub, double before,
+                                        double border) {
+    double m[4], after;
+    const int i = entry_of(c, sub);
+    masses(a, r, rest, i, m);
+    const int l = border_lane((m[0] + m[1]) + (m[2] + m[3]), before, border, before, after);
+    // the lane's own entry: the first over the border, else its last with mass (the sums' order can put the border past the
+    // last)
+    double cum = before;
+    int hit = -1, last = -1;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        cum += m[e];
+        if (m[e] > 0.0) {
+            if (hit < 0 && cum > border) hit = e;
+            last = e;
+        }
+    }
+    return __builtin_amdgcn_readlane(i + (hit >= 0 ? hit : last), l);
+}
+
+template <class T>
+__device__ __forceinline__ void write_tokens(const VerifyArgs &a, int b, int n, int token) {
+    for (int i = threadIdx.x; i <= a.max_drafts; i += kVerifyThreads)
+        a.out_tokens[(int64_t)b * (a.max_drafts + 1) + i] = i < n ? a.tokens[(int64_t)b * a.max_drafts + i] : i == n ? token : -1;
+    if (threadIdx.x == 0) a.accepted[b] = n;
+}
+
 template <class T>
 __global__ __launch_bounds__(kVerifyThreads) void verify_draw_kernel(VerifyArgs a) {
     __shared__ double subs[kSubs];
@@ -188,33 +219,48 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_draw_kernel(VerifyArgs 
         // in it the wave round, and in that the entry
         sub_sums(a, r, rest, chunk, subs);
         __syncthreads();
-        int l = border_lane(lane < kSubs ? subs[lane] : 0.0, base, border, before, after);
-        const int sub = l;
-        double m[4];
-        const int i = entry_of(chunk, sub);
-        masses(a, r, rest, i, m);
-        l = border_lane((m[0] + m[1]) + (m[2] + m[3]), before, border, before, after);
-        // the lane's own entry: the first over the border, else its last with mass (the sums' order can put the border
-        // past the last)
-        double cum = before;
-        int hit = -1, last = -1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            cum += m[e];
-            if (m[e] > 0.0) {
-                if (hit < 0 && cum > border) hit = e;
-                last = e;
-            }
-        }
-        token = __builtin_amdgcn_readlane(i + (hit >= 0 ? hit : last), l);
+        const int sub = border_lane(lane < kSubs ? subs[lane] : 0.0, base, border, before, after);
+        token = entry_in(a, r, rest, chunk, sub, before, border);
     }
-    for (int i = tid; i <= a.max_drafts; i += kVerifyThreads)
-        a.out_tokens[(int64_t)b * (a.max_drafts + 1) + i] = i < n ? a.tokens[(int64_t)b * a.max_drafts + i] : i == n ? token : -1;
-    if (tid == 0) a.accepted[b] = n;
+    write_tokens<T>(a, b, n, token);
+}
+
+// A small vocabulary: one workgroup to a sequence does it all in one launch.
+constexpr int kSmallChunks = 2;
+static_assert(kSmallChunks * kSubs <= 64, "a lane holds a wave round's sum");
+template <class T>
+__global__ __launch_bounds__(kVerifyThreads) void verify_small_kernel(VerifyArgs a) {
+    __shared__ double subs[kSmallChunks * kSubs];
+    const int b = blockIdx.x, lane = threadIdx.x & 63;
+    const Drawn<T> r = accept<T>(a, b);
+    bool rest = r.refused;
+    double total = 0.0;
+    while (true) {
+        for (int c = 0; c < a.chunks; ++c) sub_sums(a, r, rest, c, subs + c * kSubs);
+        __syncthreads();
+        total = wave_add(lane < a.chunks * kSubs ? subs[lane] : 0.0);
+        if (!rest || total > 0.0) break;
+        rest = false;  // nothing left after the draft's mass: the target's row itself
+        __syncthreads();
+    }
+    int token = -1;
+    if (total > 0.0) {
+        const double border = (double)a.sample_u[b] * total;
+        double before, after;
+        const int sub = border_lane(lane < a.chunks * kSubs ? subs[lane] : 0.0, 0.0, border, before, after);
+        token = entry_in(a, r, rest, sub / kSubs, sub % kSubs, before, border);
+    }
+    write_tokens<T>(a, b, r.n, token);
 }
 
 template <class T>
 static int run_verify(const VerifyArgs &a, hipStream_t s) {
+    // One launch or two, us a call: 1000 entries 4.6 and 8.4 (one sequence), 5.5 and 10.4 (64); 8000 entries 6.6 and 9.0,
+    // 7.4 and 10.1; 16384 entries 9.2 and 8.2, 14.7 and 12.9.
+    if (a.chunks <= kSmallChunks) {
+        verify_small_kernel<T><<<(unsigned)a.n_seqs, kVerifyThreads, 0, s>>>(a);
+        return (int)hipGetLastError();
+    }
     verify_sums_kernel<T><<<dim3((unsigned)a.chunks, (unsigned)a.n_seqs), kVerifyThreads, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
