@@ -1118,6 +1118,68 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_rows_kernel(AttnArgs a
     if (gr == 0) write_out<T>(a, p.t, hq, 4 * ln, acc, top, sum, rounded);
 }
 
+// Short contexts (prefix and page table together hold few positions): one launch. A workgroup of eight waves (four where
+// one needs more than half of its SIMD's registers) takes one
+// (sequence, key/value head, tile of 16 query rows), its waves equal runs of the prefix's and the sequence's steps,
+// and joins their parts through LDS. The prefix is read by each sequence; at these lengths it comes from the caches.
+template <int DP>
+constexpr int kShortWaves = DP == 256 ? 4 : 8;
+
+template <class T, int DP>
+__global__ __launch_bounds__(64 * kShortWaves<DP>) void attn_short_kernel(AttnArgs a, int tiles) {
+    constexpr int WAVES = kShortWaves<DP>;
+    __shared__ float part_o[WAVES][16][DP];
+    __shared__ float4 part_ml[WAVES][16];
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int bh = blockIdx.x / tiles, tile = blockIdx.x - bh * tiles, b = bh / a.kv_heads;
+    const int2 tok = seq_tokens(a, b);
+    AttnSpan s;
+    s.head = bh - b * a.kv_heads;
+    s.row0 = 16 * tile;
+    s.n_rows = tok.y * a.group;
+    if (s.row0 >= s.n_rows) return;
+    s.tok0 = tok.x;
+    s.n_tok = tok.y;
+    const int len = seq_len(a, b), steps_p = (a.prefix_len + kAttnStep - 1) / kAttnStep, steps_s = (len + kAttnStep - 1) / kAttnStep;
+    int run = max(1, (steps_p + steps_s + WAVES - 1) / WAVES);  // steps of a wave, all of one segment
+    while ((steps_p + run - 1) / run + (steps_s + run - 1) / run > WAVES) ++run;
+    const int waves_p = (steps_p + run - 1) / run;
+    const bool own = wave >= waves_p;
+    const int first = (own ? wave - waves_p : wave) * run;
+    s.pages = own ? a.table + (int64_t)b * a.table_stride : a.prefix_pages;
+    s.len = own ? len : a.prefix_len;
+    s.causal = own;
+    s.pos0 = first * kAttnStep;
+    s.pos1 = s.pos0 + run * kAttnStep;
+    s.po = &part_o[wave][0][0];
+    s.pml = part_ml[wave];
+    if (s.pos0 < s.len)
+        attend<T, 1, DP>(a, s);
+    else if ((tid & 63) < 16)
+        part_ml[wave][tid & 63] = make_float4(kNone, 0.0f, 0.0f, 0.0f);
+    __syncthreads();
+    for (int i = tid; i < 16 * (DP / 4); i += 64 * kShortWaves<DP>) {
+        const int row = i / (DP / 4), d = 4 * (i - row * (DP / 4));
+        if (s.row0 + row >= s.n_rows) break;
+        float top = kNone;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) top = fmaxf(top, part_ml[w][row].x);
+        float sum = 0.0f, rounded = 0.0f;
+        f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const float4 x = part_ml[w][row];
+            if (x.x == kNone) continue;  // (such a part's outputs may not be there)
+            const float f = __builtin_amdgcn_exp2f(x.x - top);
+            sum += f * x.y;
+            rounded += f * x.z;
+            acc += *reinterpret_cast<const f32x4 *>(&part_o[w][row][d]) * f;
+        }
+        const int j = (s.row0 + row) / a.group;
+        write_out<T>(a, tok.x + j, s.head * a.group + s.row0 + row - j * a.group, d, acc, top, sum, rounded);
+    }
+}
+
 template <class T, int DP, int MP, int MS>
 static int run_attn(const AttnArgs &a, hipStream_t st) {
     attn_split_kernel<T, DP, MP, MS><<<(unsigned)a.n_wgs, kAttnThreads, (size_t)(5 * (a.n_seqs + 1)) * 4, st>>>(a);
@@ -1136,6 +1198,11 @@ static int run_attn(const AttnArgs &a, hipStream_t st) {
 // against 79 with 256; with heads of 64, 40 rows: 26 against 23).
 template <class T, int DP>
 static int run_attn_tiles(const AttnArgs &a, int32_t mp, int32_t ms, hipStream_t st) {
+    if (mp == 0) {  // short contexts
+        const int tiles = (a.max_q * a.group + 15) / 16;
+        attn_short_kernel<T, DP><<<(unsigned)(a.n_seqs * a.kv_heads * tiles), 64 * kShortWaves<DP>, 0, st>>>(a, tiles);
+        return (int)hipGetLastError();
+    }
     if (ms == 16) {
         if (mp == 16) return run_attn<T, DP, 16, 16>(a, st);
         if (mp == 64) return run_attn<T, DP, 64, 16>(a, st);

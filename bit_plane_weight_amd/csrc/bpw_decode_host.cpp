@@ -231,6 +231,10 @@ struct AttnShape {
 // 8 x 96 rows of 64 over 1000 positions, 49 k: 16.6, 19.5; 8 x 32 rows of 128 over 2000, 129 k: 18.1, 15.7; 5 x 64 rows of
 // 128 over 1024, 82 k: 16.8, 15.1; 8 x 32 rows of 64 over 8000, 128 k: 17.9, 16.1.
 constexpr int64_t kNarrowWork = 65536;
+// Most positions (x padded head size) of a row of the page table for the one-launch kernel, those of a prefix twice, as every
+// sequence reads them. Measured, us a call (one launch, two): one sequence of 20 / 5 heads of 128, 128 positions 5.3, 9.3;
+// 256: 7.2, 9.1; 512: 9.0, 9.4; 704: 10.8, 9.6. 64 sequences of 256: 15.2, 17.0; with 256 of a prefix before them 23.6, 18.9.
+constexpr int64_t kShortWork = 65536;
 constexpr int64_t kPieceCost = 3;   // tiles that a piece of a wide prefix costs beyond its own (queries in, parts out)
 constexpr int64_t kBusyCost = 32;   // tiles that all workgroups being busy with pieces costs
 
@@ -396,9 +400,10 @@ bpw_status bpw_attn_shared_prefix(const bpw_attn_shared_prefix_args *a, void *d_
     k.part_ml = reinterpret_cast<float4 *>(ws + s.pml);
     k.part_s = s.pieces_p * s.mp * s.dp;
     k.ml_s = s.pieces_p * s.mp;
-    const int e = s.dp == 64    ? bpw::launch_attn_d64(k, c.dtype, s.mp, s.ms, stream)
-                  : s.dp == 128 ? bpw::launch_attn_d128(k, c.dtype, s.mp, s.ms, stream)
-                                : bpw::launch_attn_d256(k, c.dtype, s.mp, s.ms, stream);
+    const int32_t mp = (s.cap + 2 * a->prefix_len) * s.dp <= kShortWork ? 0 : s.mp;  // 0: one launch
+    const int e = s.dp == 64    ? bpw::launch_attn_d64(k, c.dtype, mp, s.ms, stream)
+                  : s.dp == 128 ? bpw::launch_attn_d128(k, c.dtype, mp, s.ms, stream)
+                                : bpw::launch_attn_d256(k, c.dtype, mp, s.ms, stream);
     return hip_status(e, "attention launch");
 }
 

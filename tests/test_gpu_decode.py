@@ -291,6 +291,22 @@ def test_attention(dev, n_q, lens, Hq, Hk, D, P, prefix, dt, layout):
     a.check()
 
 
+@pytest.mark.parametrize("n_q,lens,Hq,Hk,D,P,prefix,pages", [
+    # either side of the one-launch kernel's bound on table and prefix, the contents the same
+    ([1], [512], 20, 5, 128, 16, 0, 32),
+    ([1], [512], 20, 5, 128, 16, 0, 33),
+    ([3, 0, 2], [250, 9, 0], 24, 2, 128, 16, 100, 16),
+    ([2, 1], [300, 1024], 6, 3, 64, 64, 0, 16),
+    ([5, 9], [77, 128], 40, 2, 256, 16, 30, 8),
+    ([1, 1], [0, 16], 4, 2, 40, 16, 1, 1),
+])
+def test_attention_short(dev, n_q, lens, Hq, Hk, D, P, prefix, pages):
+    a = Attn(dev, n_q, lens, Hq, Hk, D, P, prefix, F16, seed=sum(lens), max_pages=pages)
+    a.plan().run()
+    torch.cuda.synchronize()
+    a.check()
+
+
 def test_attention_many_sequences(dev):
     """Sequence counts past one thread's four and past a wave's 256; most idle or one position long."""
     n_q = [i % 3 % 2 for i in range(700)]
