@@ -36,8 +36,10 @@ struct HeadsArgs {
 };
 
 constexpr int kHeadThreads = 256;
-// vec: every row is read and written 16 bytes at a time (alignment and divisibility checked by the host)
-int launch_heads(const HeadsArgs &a, int32_t dt_in, int32_t dt_out, bool vec, void *stream);
+// Paths: rows of any alignment; rows read and written 16 bytes at a time (alignment and divisibility checked by the
+// host), with pairs anywhere in them, or with pairs of whole chunks.
+constexpr int32_t kHeadsAny = 0, kHeadsMixed = 1, kHeadsVec = 2;
+int launch_heads(const HeadsArgs &a, int32_t dt_in, int32_t dt_out, int32_t path, void *stream);
 
 // ---------------------------------------------------------------- attention
 

@@ -101,12 +101,15 @@ bpw::HeadSet head_set(const bpw_heads &in, const bpw_heads &out, const float *ga
     return s;
 }
 
-// Lanes of a head, tokens of a workgroup, vector or element path.
+// Path, lanes of a head, tokens of a workgroup.
 bpw_status run_heads(bpw::HeadsArgs &a, int32_t dt_in, int32_t dt_out, bool vec, const char *who, void *stream) {
     const int D = a.head_dim, R = a.rot_dim;
     const int heads = a.q.heads + a.k.heads + a.v.heads;
-    vec = vec && D % 16 == 0 && R % 16 == 0 && aligned(a.q.gain, 16) && aligned(a.k.gain, 16);
-    a.lanes_log2 = vec ? log2_of(D / 16) : log2_of(D / 2);
+    vec = vec && aligned(a.q.gain, 16) && aligned(a.k.gain, 16);
+    // 8192 tokens of 32 + 8 heads of 128 in bf16, us: 34 with 128 or 80 elements turned (vec); with 66, 47-48 (mixed) or
+    // 136-142 (any). The mixed path holds a head in one wave, 8 elements to a lane, hence the 512.
+    const int32_t path = vec && D % 16 == 0 && R % 16 == 0 ? bpw::kHeadsVec : vec && D % 8 == 0 && D <= 512 ? bpw::kHeadsMixed : bpw::kHeadsAny;
+    a.lanes_log2 = log2_of(path == bpw::kHeadsVec ? D / 16 : path == bpw::kHeadsMixed ? D / 8 : D / 2);
     if (a.lanes_log2 > 6) a.lanes_log2 = 6;
     const int at_once = bpw::kHeadThreads >> a.lanes_log2;
     // Many tokens with few heads: as many to a workgroup as one sweep over its lanes holds. (More, so that a last sweep
@@ -114,7 +117,7 @@ bpw_status run_heads(bpw::HeadsArgs &a, int32_t dt_in, int32_t dt_out, bool vec,
     a.tokens_per_wg = a.n_tokens >= 2048 && heads < at_once ? at_once / heads : 1;
     bpw_status st = (bpw_status)bpw::host_check_device();
     if (st) return st;
-    return hip_status(bpw::launch_heads(a, dt_in, dt_out, vec, stream), who);
+    return hip_status(bpw::launch_heads(a, dt_in, dt_out, path, stream), who);
 }
 
 // q and k (and v) share the input type, their outputs the other.

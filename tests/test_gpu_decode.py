@@ -96,7 +96,7 @@ def run_rope(dev, T, Hq, Hk, D, R, adjacent, src, dst, gains, layout="fused", se
     (1, 1, 1, 2, 2, True, F32, F32, True),
     (3, 4, 2, 64, 64, True, BF16, BF16, True),
     (5, 3, 1, 80, 32, False, F16, F16, True),
-    (5, 3, 1, 80, 80, False, F16, F32, True),     # halves of 40: the element path
+    (5, 3, 1, 80, 80, False, F16, F32, True),
     (7, 5, 5, 96, 96, True, BF16, F32, False),
     (2, 2, 2, 10, 6, False, F32, F16, True),
     (4, 1, 0, 256, 64, False, F32, BF16, True),
@@ -105,6 +105,14 @@ def run_rope(dev, T, Hq, Hk, D, R, adjacent, src, dst, gains, layout="fused", se
     (2, 2, 1, 1022, 510, False, BF16, F16, True),
     (3, 2, 1, 128, 0, False, F32, BF16, True),    # no rotation
     (33, 40, 8, 128, 128, False, BF16, BF16, True),  # more heads than one sweep
+    (5, 3, 1, 80, 40, False, BF16, BF16, True),   # pairs that are not whole chunks
+    (5, 3, 1, 80, 54, True, F32, F16, True),
+    (9, 17, 3, 128, 66, False, F16, F32, True),
+    (3, 2, 2, 8, 6, False, BF16, BF16, True),
+    (3, 2, 2, 8, 2, True, F32, BF16, False),
+    (2, 5, 1, 512, 510, False, BF16, F16, True),
+    (2, 5, 1, 504, 130, True, BF16, BF16, True),
+    (2053, 2, 1, 72, 34, False, BF16, BF16, True),
     (2051, 3, 1, 64, 64, False, BF16, BF16, True),   # several tokens a workgroup, the last one short
 ])
 def test_norm_rope(dev, T, Hq, Hk, D, R, adjacent, src, dst, gains):
@@ -112,7 +120,7 @@ def test_norm_rope(dev, T, Hq, Hk, D, R, adjacent, src, dst, gains):
 
 
 @pytest.mark.parametrize("layout", ["odd", "in place"])
-@pytest.mark.parametrize("D,R,adjacent", [(128, 128, False), (128, 64, True), (36, 20, False)])
+@pytest.mark.parametrize("D,R,adjacent", [(128, 128, False), (128, 64, True), (36, 20, False), (88, 50, False), (88, 50, True)])
 def test_norm_rope_layouts(dev, layout, D, R, adjacent):
     run_rope(dev, 9, 4, 2, D, R, adjacent, BF16, BF16, True, layout)
 
