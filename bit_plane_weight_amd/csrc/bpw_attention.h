@@ -392,9 +392,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
-// Costs for the dealing, in steps of one suffix wave: a tile of the prefix, and what an item costs beyond its steps.
-constexpr float kWideCost64 = 0.5f, kWideCost128 = 0.6f, kItemCost = 4.0f;
-
 template <class T>
 __device__ __forceinline__ f32x16 mma32(u32v4 a, u32v4 b, f32x16 c);
 template <>
@@ -854,33 +851,12 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_ke
         if (b == a.n_seqs - 1) seqs.units[a.n_seqs] = eu, seqs.items[a.n_seqs] = ei;
     }
 
-    // The dealing. Narrow prefix: its units and the suffixes' in equal runs, one to a wave, wp and ws of them. Wide
-    // prefix: the waves of workgroups that had one piece less (`idle`) take more of the suffixes. qf, qb: units of a run
-    // of an idle and of a busy workgroup's wave; runs_f: runs of the idle ones, which come first.
-    int wp = 0, ws = 0, qf, qb, idle = 0;
+    // The dealing (deal_narrow, deal_wide).
     const int turns = WIDE ? (per_xcd + wgs_xcd - 1) / wgs_xcd : 0, busy_xcd = per_xcd - (turns - 1) * wgs_xcd;
-    if constexpr (WIDE) {
-        idle = 8 * (wgs_xcd - busy_xcd);
-        const float cost_s = total_s > 0 ? 1.0f + kItemCost * (float)items_s / (float)total_s : 1.0f;
-        const int more = (int)((float)a.split_units * (MP == 64 ? kWideCost64 : kWideCost128) / cost_s);
-        const int64_t first = (int64_t)4 * idle * more;  // units that the idle ones take meanwhile
-        if (idle > 0 && total_s <= first) {
-            qf = max(1, (total_s + 4 * idle - 1) / (4 * idle));
-            qb = 1;
-        } else {
-            qb = (total_s - (int)first + 4 * (int)gridDim.x - 1) / (4 * (int)gridDim.x);
-            qf = qb + more;
-        }
-    } else {
-        qf = qb = max(1, (total_p + total_s + 4 * (int)gridDim.x - 1) / (4 * (int)gridDim.x));
-        while (true) {
-            wp = (total_p + qb - 1) / qb;
-            ws = (total_s + qb - 1) / qb;
-            if (wp + ws <= 4 * (int)gridDim.x) break;
-            qf = ++qb;
-        }
-    }
-    const int runs_f = 4 * idle;
+    const int idle = WIDE ? 8 * (wgs_xcd - busy_xcd) : 0;
+    const AttnDeal deal = WIDE ? deal_wide(total_s, items_s, idle, a.split_units, MP == 64, gridDim.x)
+                               : deal_narrow(total_p, total_s, gridDim.x);
+    const int qf = deal.qf, qb = deal.qb, wp = deal.wp, runs_f = deal.runs_f;
     __syncthreads();
     if (blockIdx.x == 0) {  // what the join needs
         if (tid == 0) a.sched[0] = up, a.sched[1] = qf, a.sched[2] = qb, a.sched[3] = runs_f;
@@ -925,8 +901,7 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_split_ke
         }
     };
     if constexpr (WIDE) {
-        const bool busy = at < busy_xcd;
-        const int w = busy ? runs_f + wave * 8 * busy_xcd + xcd + 8 * at : wave * idle + xcd + 8 * (at - busy_xcd);
+        const int w = wide_run(blockIdx.x, wave, busy_xcd, idle);
         const int u = w < runs_f ? w * qf : runs_f * qf + (w - runs_f) * qb;
         suffixes(w, u, min(total_s, u + (w < runs_f ? qf : qb)));
     } else {
@@ -961,7 +936,8 @@ struct AttnParts {
 
     __device__ __forceinline__ AttnParts(const AttnArgs &a, int mp, int ms_, int b, int j, int hq) : step_p(0), ms(ms_) {
         const int2 tok = seq_tokens(a, b);
-        const int up = a.sched[0], qf = a.sched[1], qb = a.sched[2], runs_f = a.sched[3];
+        const int up = a.sched[0], qb = a.sched[2];
+        const AttnDeal deal{a.sched[1], qb, 0, a.sched[3]};
         const int before_u = a.sched[kSchedHead + b], before_i = a.sched[kSchedHead + a.n_seqs + 1 + b];
         const int ub = (seq_len(a, b) + kAttnStep - 1) / kAttnStep;
         const int head = hq / a.group, gi = hq - head * a.group;
@@ -984,9 +960,8 @@ struct AttnParts {
         }
         if (ub > 0) {
             const int row = j * a.group + gi, tile = row / ms, item = head * ((tok.y * a.group + ms - 1) / ms) + tile;
-            const auto run_of = [&](int u) { return u < runs_f * qf ? u / qf : runs_f + (u - runs_f * qf) / qb; };
-            const int u0 = before_u + item * ub, w0 = run_of(u0);
-            ns = run_of(u0 + ub - 1) - w0 + 1;
+            const int u0 = before_u + item * ub, w0 = deal.run_of(u0);
+            ns = deal.run_of(u0 + ub - 1) - w0 + 1;
             row_s = (int64_t)(before_i + item + w0) * ms + row - tile * ms;
         }
     }
@@ -1018,7 +993,7 @@ constexpr int kJoinRows = 1024;
 template <class T, int DP>
 __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int mp, int ms) {
     constexpr int LANES = DP / 4, GROUPS = kAttnThreads / LANES;
-    __shared__ float weight[kAttnWaves * kAttnWgs + 2];
+    __shared__ float weight[kAttnParts];
     __shared__ f32x4 sums[GROUPS][LANES];
     __shared__ float red[3][kAttnWaves];
     const int tid = threadIdx.x;

@@ -49,6 +49,9 @@ constexpr int kAttnStep = 32;                      // positions a wave takes at 
 constexpr int kWideTile = 64;                      // positions a workgroup takes at a time of a prefix that many rows share
 constexpr int kAttnMaxSeqs = 1024;
 constexpr int kAttnWgs = 512;                      // most workgroups of a launch: two to each of 256 CUs
+constexpr int kAttnPieces = 64;                    // most pieces that the host cuts an item of a wide prefix into
+// Most parts of a query row: one from each wave's run, and beside those a wide prefix's pieces.
+constexpr int kAttnParts = kAttnWaves * kAttnWgs + kAttnPieces;
 
 struct AttnArgs {
     const void *q;
@@ -76,6 +79,51 @@ struct AttnArgs {
     int64_t ml_s;            // and in part_ml
 };
 constexpr int kSchedHead = 8;  // units of a prefix item, units of the two lengths of runs, runs of the first
+
+// Costs for the dealing, in steps of one suffix wave: a tile of a wide prefix, and what an item costs beyond its steps.
+constexpr float kWideCost64 = 0.5f, kWideCost128 = 0.6f, kItemCost = 4.0f;
+
+// The dealing of units (kAttnStep positions of an item) to the runs of the 4 n_wgs waves. The first runs_f runs hold qf
+// units, the others qb. Narrow prefix: its units and the suffixes' in equal runs, wp of them the prefix's. Wide prefix:
+// the waves of the `idle` workgroups, which had one piece less, take more of the suffixes and come first.
+struct AttnDeal {
+    int32_t qf, qb, wp, runs_f;
+    // run of unit u of the suffixes
+    __host__ __device__ int32_t run_of(int32_t u) const { return u < runs_f * qf ? u / qf : runs_f + (u - runs_f * qf) / qb; }
+};
+
+inline __host__ __device__ AttnDeal deal_narrow(int32_t total_p, int32_t total_s, int32_t n_wgs) {
+    AttnDeal d{0, 1, 0, 0};
+    const int32_t even = (total_p + total_s + kAttnWaves * n_wgs - 1) / (kAttnWaves * n_wgs);
+    for (d.qb = even > 1 ? even : 1;; ++d.qb) {
+        d.wp = (total_p + d.qb - 1) / d.qb;
+        if (d.wp + (total_s + d.qb - 1) / d.qb <= kAttnWaves * n_wgs) break;
+    }
+    d.qf = d.qb;
+    return d;
+}
+
+inline __host__ __device__ AttnDeal deal_wide(int32_t total_s, int32_t items_s, int32_t idle, int32_t split_units, bool tile64,
+                                              int32_t n_wgs) {
+    AttnDeal d{0, 1, 0, kAttnWaves * idle};
+    const float cost_s = total_s > 0 ? 1.0f + kItemCost * (float)items_s / (float)total_s : 1.0f;
+    const int32_t more = (int32_t)((float)split_units * (tile64 ? kWideCost64 : kWideCost128) / cost_s);
+    const int64_t first = (int64_t)d.runs_f * more;  // units that the idle ones take meanwhile
+    if (idle > 0 && total_s <= first) {
+        const int32_t even = (total_s + d.runs_f - 1) / d.runs_f;
+        d.qf = even > 1 ? even : 1;
+    } else {
+        d.qb = (total_s - (int32_t)first + kAttnWaves * n_wgs - 1) / (kAttnWaves * n_wgs);
+        d.qf = d.qb + more;
+    }
+    return d;
+}
+
+// Wide prefix: the run of a wave. `busy` workgroups of each XCD had all the pieces of a turn; workgroup b runs on XCD b % 8.
+inline __host__ __device__ int32_t wide_run(int32_t block, int32_t wave, int32_t busy, int32_t idle) {
+    const int32_t xcd = block & 7, at = block >> 3;
+    return at < busy ? kAttnWaves * idle + wave * 8 * busy + xcd + 8 * at : wave * idle + xcd + 8 * (at - busy);
+}
 
 int launch_attn_d64(const AttnArgs &a, int32_t dtype, int32_t mp, int32_t ms, void *stream);
 int launch_attn_d128(const AttnArgs &a, int32_t dtype, int32_t mp, int32_t ms, void *stream);

@@ -300,7 +300,7 @@ bpw_status attn_shape(const bpw_attn_shared_prefix_args *a, AttnShape *s) {
         s->n_wgs = (s->n_wgs + 7) / 8 * 8;
         const int64_t tiles = (a->prefix_len + bpw::kWideTile - 1) / bpw::kWideTile;
         int64_t best = INT64_MAX;
-        for (int64_t n = 1; n <= tiles && n <= 64; ++n) {
+        for (int64_t n = 1; n <= tiles && n <= bpw::kAttnPieces; ++n) {
             const int64_t turns = (items_p * n + s->n_wgs - 1) / s->n_wgs, len = (tiles + n - 1) / n;
             const int64_t cost = turns * (len + kPieceCost) * s->n_wgs + kBusyCost * items_p * n;
             if (cost < best) {

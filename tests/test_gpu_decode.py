@@ -333,6 +333,14 @@ def test_attention_long_splits(dev):
     a.check()
 
 
+def test_attention_most_parts_of_a_row(dev):
+    """A wide prefix in the most pieces beside one suffix that every wave takes a part of: 2112 parts to a row."""
+    a = Attn(dev, [1, 1], [122880, 0], 16, 1, 128, 16, 16384, BF16, seed=41)
+    a.plan().run()
+    torch.cuda.synchronize()
+    a.check()
+
+
 def test_attention_runtime_values_out_of_range(dev):
     """Pages that do not exist are hidden, lengths past the table cut, query tokens past the starts or max_q left out."""
     a = Attn(dev, [1, 1, 3, 2], [100, 64, 40, 208], 4, 2, 64, 16, 50, BF16, seed=9)

@@ -276,3 +276,63 @@ def test_packers_under_sanitizers(driver, tmp_path):
     lines = run_cases(driver, tmp_path, recs)
     for k, (w, line) in enumerate(zip(ws, lines)):
         assert line == trits_expected(w), (k, w.shape, line)
+
+
+# ---------------------------------------------------------------- the attention's shapes and dealing
+
+
+@pytest.fixture(scope="module")
+def dealing(tmp_path_factory):
+    cxx = _clang()
+    if cxx is None:
+        pytest.skip("clang++ not found")
+    exe = str(tmp_path_factory.mktemp("dealing") / "attn_dealing_driver")
+    src = os.path.join(ROOT, "tests", "sanitize", "attn_dealing_driver.cpp")
+    r = subprocess.run([cxx, "-std=c++17", "-O1", "-g", *SAN, "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", src, "-o", exe],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+    def run(calls):
+        """calls: (n_tokens, n_seqs, max_q, q_heads, kv_heads, head_dim, prefix, page, max_pages, [(length, tokens)]) ->
+        (status, mp, ms, workgroups, most parts of a row, most that a row may have) of each."""
+        lines = []
+        for i in range(0, len(calls), 200):
+            args = [",".join(map(str, c[:9])) + ":" + ",".join(f"{n}x{t}" for n, t in c[9]) for c in calls[i:i + 200]]
+            r = subprocess.run([exe, *args], capture_output=True, text=True, timeout=120)
+            assert r.returncode == 0 and not r.stderr, (r.stderr[-2000:], args)
+            lines += r.stdout.splitlines()
+        assert len(lines) == len(calls)
+        return [tuple(map(int, x.split())) for x in lines]
+
+    return run
+
+
+def test_attention_dealing_wide_prefix_and_one_long_suffix(dealing):
+    """A row's parts are those of a wide prefix's pieces and those of every wave that took a piece of its sequence:
+    the join's LDS holds them all."""
+    calls = [(2, 2, 1, 16, 1, 128, 16384, 16, max(n, m) // 16 + 1, [(n, 1), (m, 1)])
+             for m in (0, 40) for n in range(64, 1000000, 4096)]
+    got = dealing(calls)
+    assert all(g[0] == 0 and g[1] == 64 for g in got)
+    assert max(g[4] for g in got) > 4 * 512  # beyond one for each wave
+    assert all(g[4] <= g[5] for g in got)
+
+
+def test_attention_dealing_over_drawn_calls(dealing):
+    """Ragged calls of every kind: all units dealt, a part of its own for each item and run, no row with more parts than
+    the join holds."""
+    rng = np.random.default_rng(7)
+    log = lambda hi: int(np.exp(rng.uniform(0, np.log(hi))))  # noqa: E731
+    calls = []
+    for _ in range(600):
+        kv, seqs, most = int(rng.integers(1, 9)), log(200), log(9)
+        seq = [(int(rng.integers(0, log(200000) + 1)), int(rng.integers(0, most + 1))) for _ in range(seqs)]
+        tokens = sum(t for _, t in seq)
+        if tokens == 0:
+            continue
+        page = int(2 ** rng.integers(4, 8))
+        calls.append((tokens, seqs, most, kv * int(rng.integers(1, 41)), kv, int(rng.choice([64, 80, 128, 256])),
+                      int(rng.choice([0, log(300000)])), page, max(n for n, _ in seq) // page + 1, seq))
+    got = dealing(calls)
+    assert {g[1] for g in got if g[0] == 0} == {16, 32, 64, 128}
+    assert all(g[0] in (0, E_UNSUPPORTED) and g[4] <= g[5] for g in got)
