@@ -80,11 +80,15 @@ struct AttnSpan {
     int32_t n_rows;    // rows of all tiles
     int32_t pos0, pos1;
     float *po;         // results of the tile: [rows][DP]
-    float4 *pml;       // [rows]: shift (log2 units), sum of the weights, sum of the rounded weights
+    float4 *pml;       // [rows]: shift (log2 units; -inf: nothing seen), sum of the weights, sum of the rounded weights
 };
 
 constexpr float kNone = -__builtin_inff();
 constexpr float kShiftLimit = 1024.0f;  // float16 weights reach 65504
+
+// The shift that a part is stored with. Maxima pass over NaN, so a row whose scores are all NaN has a sum of NaN at a shift
+// that is still kNone; any finite shift tells it from a row that saw nothing.
+__device__ __forceinline__ float stored_shift(float m, float l) { return m == kNone && l != 0.0f ? 0.0f : m; }
 
 // Pages of the positions to come, one granule of 16 positions a lane (pages hold a multiple of 16, so a granule
 // never straddles two): two runs of 64 granules, the second loaded while the first is in use, so that
@@ -356,7 +360,7 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s) {
         lr[i] += __shfl_xor(lr[i], 32);
         const int row = 16 * i + n;
         if (s.row0 + row >= s.n_rows) continue;
-        if (g == 0) s.pml[row] = make_float4(m[i], l[i], lr[i], 0.0f);
+        if (g == 0) s.pml[row] = make_float4(stored_shift(m[i], l[i]), l[i], lr[i], 0.0f);
         float *po = s.po + row * DP;
 #pragma unroll
         for (int h = 0; h < NH; ++h)
@@ -699,6 +703,7 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
 
     l += __shfl_xor(l, 32);
     lr += __shfl_xor(lr, 32);
+    m = stored_shift(m, l);
     if constexpr (PARTS == 2) {  // the second wave of the same rows hands over through LDS
         constexpr int PAD = DP + 4;
         float *box = reinterpret_cast<float *>(&lds) + (wave % WQ) * (32 * PAD);

@@ -414,6 +414,68 @@ def test_attention_nan_and_infinity_where_seen(dev):
     assert torch.isnan(got[0, :2]).all() and not torch.isnan(got[0, 2:]).any() and not torch.isnan(got[1]).any()
 
 
+# Calls by the path they take: one launch; two, joined by a workgroup or by a wave to a row; a prefix of 64 and of 128 rows
+# through LDS. (n_q, lens, Hq, Hk, D, P, prefix, max_pages)
+ATTENTION_PATHS = {
+    "short": ([1, 2, 1], [40, 1, 77], 4, 2, 64, 16, 20, 8),
+    "narrow": ([1, 2, 1], [900, 1, 77], 4, 2, 64, 16, 20, 64),
+    "narrow 256": ([1, 2, 1], [300, 1, 77], 4, 2, 256, 16, 40, 64),
+    "narrow rows": ([3] * 30, [40 + i for i in range(30)], 12, 2, 128, 64, 65, 8),
+    "wide 64": ([1] * 12, [40] * 11 + [1], 8, 2, 128, 16, 3333, 4),
+    "wide 128": ([3] * 13, [40 + i for i in range(12)] + [3], 12, 2, 128, 64, 3333, 1),
+    "wide 128, padded": ([3] * 13, [40 + i for i in range(12)] + [3], 12, 2, 80, 32, 3333, 2),
+    "wide 64, small": ([1] * 30, [40] * 29 + [1], 4, 2, 48, 16, 9000, 4),
+    "wide 64, large": ([2] * 10, [70] * 9 + [2], 6, 2, 256, 16, 3333, 5),
+    "wide 128, large": ([5] * 9, [70] * 8 + [5], 12, 2, 200, 128, 3333, 1),
+}
+
+
+def check_with_nan(a, what):
+    """As Attn.check, where every token belongs to a sequence: NaN has to be where the reference has it, in out and lse."""
+    out, lse, mag = a.reference()
+    D, L = a.q.shape[-1], a.prefix + max(a.lens)
+    q, k, v = f64(a.q), f64(a.k), f64(a.v)
+    tol, tol_lse = attn_tol(out, mag, q, k[np.isfinite(k).all(-1)], v[np.isfinite(v)], D, L, a.scale or D ** -0.5, a.dt)
+    within(a.out, out, tol, f"{what} out")
+    within(a.lse, lse, tol_lse + 4 * U * np.abs(lse), f"{what} lse")
+
+
+@pytest.mark.parametrize("path", ATTENTION_PATHS)
+def test_attention_nan_scores_are_not_nothing_seen(dev, path):
+    """Rows whose scores are all NaN in a part of their positions, or in all: a query of NaN, the one key a sequence has of its
+    own, all keys of a sequence or of the prefix, a wave's step of them. out and lse are NaN, and no other row's."""
+    n_q, lens, Hq, Hk, D, P, prefix, pages = ATTENTION_PATHS[path]
+    a = Attn(dev, n_q, lens, Hq, Hk, D, P, prefix, BF16, seed=43, max_pages=pages)
+    clean_q, clean_k = a.q.clone(), a.k.clone()
+
+    def row(b, pos):  # a position of sequence b (None: of the prefix), of key/value head 0
+        page = (a.prefix_pages if b is None else a.table[b])[pos // P].long()
+        return page, 0, pos % P
+
+    def run(what):
+        a.plan().run()
+        torch.cuda.synchronize()
+        assert np.isnan(f64(a.lse)).any()
+        check_with_nan(a, what)
+        a.q.copy_(clean_q), a.k.copy_(clean_k)
+
+    a.q[0, 1] = float("nan")
+    run("query")
+    one = int(np.argmin(lens))
+    for pos in range(lens[one]):
+        a.k[row(one, pos)] = float("nan")
+    run("the sequence of the fewest positions")
+    for pos in range(lens[0]):
+        a.k[row(0, pos)] = float("nan")
+    run("a sequence")
+    for pos in range(prefix):
+        a.k[row(None, pos)] = float("nan")
+    run("the prefix")
+    for pos in range(min(32, prefix)):
+        a.k[row(None, pos)] = float("nan")
+    run("a step of the prefix")
+
+
 @pytest.mark.parametrize("Hq,Hk,D,n,dt", [(3, 1, 64, 5, BF16), (8, 2, 128, 3, F16), (12, 2, 80, 7, BF16), (4, 4, 256, 9, F16)])
 def test_attention_values_that_are_not_finite_in_later_drafts(dev, Hq, Hk, D, n, dt):
     """NaN and infinities in the values of drafts: the tokens before them are as without, the others show them.

@@ -318,6 +318,15 @@ def test_attention_dealing_wide_prefix_and_one_long_suffix(dealing):
     assert all(g[4] <= g[5] for g in got)
 
 
+def test_attention_paths_of_the_gpu_tests(dealing):
+    """The GPU tests' calls by path take the paths they are named after."""
+    from test_gpu_decode import ATTENTION_PATHS as paths
+    got = dealing([(sum(n_q), len(n_q), max(n_q), Hq, Hk, D, prefix, P, pages, list(zip(lens, n_q)))
+                   for n_q, lens, Hq, Hk, D, P, prefix, pages in paths.values()])
+    for name, (status, mp, *_) in zip(paths, got):
+        assert status == 0 and (mp == int(name.split()[1].strip(",")) if "wide" in name else mp <= 32), name
+
+
 def test_attention_dealing_over_drawn_calls(dealing):
     """Ragged calls of every kind: all units dealt, a part of its own for each item and run, no row with more parts than
     the join holds."""
