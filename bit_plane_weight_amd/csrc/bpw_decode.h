@@ -8,6 +8,10 @@
 
 namespace bpw {
 
+// Most workgroups of a launch: a grid of 2^32 threads or more is not run as asked, and no error says so. What needs more
+// workgroups (of up to 512 threads) goes in several launches.
+constexpr int32_t kMaxWgs = 1 << 22;
+
 // ---------------------------------------------------------------- heads (norm, rotation, append)
 
 // One set of heads: inputs and outputs by element strides. With slots, out_ts is the stride of a cache
@@ -32,6 +36,7 @@ struct HeadsArgs {
     int32_t page_log2;
     int32_t lanes_log2;      // lanes of one head
     int32_t tokens_per_wg;
+    int32_t first_wg;        // of this launch
     float eps;
 };
 

@@ -92,7 +92,7 @@ template <class TI, class TO>
 __global__ __launch_bounds__(kHeadThreads) void heads_vec_kernel(HeadsArgs a) {
     extern __shared__ float2 cs[];
     const int heads = a.q.heads + a.k.heads + a.v.heads;
-    const int t0 = blockIdx.x * a.tokens_per_wg;
+    const int t0 = (a.first_wg + (int)blockIdx.x) * a.tokens_per_wg;
     const int nt = min(a.tokens_per_wg, a.n_tokens - t0);
     const int c = threadIdx.x & ((1 << a.lanes_log2) - 1);
     const int step = kHeadThreads >> a.lanes_log2, total = nt * heads;
@@ -171,7 +171,7 @@ template <class TI, class TO>
 __global__ __launch_bounds__(kHeadThreads) void heads_mixed_kernel(HeadsArgs a) {
     extern __shared__ float2 cs[];
     const int heads = a.q.heads + a.k.heads + a.v.heads, half = a.rot_dim >> 1;
-    const int t0 = blockIdx.x * a.tokens_per_wg;
+    const int t0 = (a.first_wg + (int)blockIdx.x) * a.tokens_per_wg;
     const int nt = min(a.tokens_per_wg, a.n_tokens - t0);
     const int c = threadIdx.x & ((1 << a.lanes_log2) - 1), i0 = 8 * c;
     const int step = kHeadThreads >> a.lanes_log2, total = nt * heads;
@@ -217,7 +217,7 @@ template <class TI, class TO>
 __global__ __launch_bounds__(kHeadThreads) void heads_any_kernel(HeadsArgs a) {
     extern __shared__ float2 cs[];
     const int heads = a.q.heads + a.k.heads + a.v.heads;
-    const int t0 = blockIdx.x * a.tokens_per_wg;
+    const int t0 = (a.first_wg + (int)blockIdx.x) * a.tokens_per_wg;
     const int nt = min(a.tokens_per_wg, a.n_tokens - t0);
     const int lanes = 1 << a.lanes_log2, c = threadIdx.x & (lanes - 1);
     const int step = kHeadThreads >> a.lanes_log2, total = nt * heads, pairs = a.head_dim >> 1, half = a.rot_dim >> 1;
@@ -258,18 +258,23 @@ __global__ __launch_bounds__(kHeadThreads) void heads_any_kernel(HeadsArgs a) {
 }
 
 template <class TI, class TO>
-static int launch_typed(const HeadsArgs &a, int32_t path, hipStream_t s) {
-    const unsigned grid = (unsigned)((a.n_tokens + a.tokens_per_wg - 1) / a.tokens_per_wg);
-    const size_t lds = (size_t)a.tokens_per_wg * (size_t)(a.rot_dim / 2) * sizeof(float2);
-    if (path == kHeadsVec)
-        heads_vec_kernel<TI, TO><<<grid, kHeadThreads, lds, s>>>(a);
-    else if (path == kHeadsMixed)
-        heads_mixed_kernel<TI, TO><<<grid, kHeadThreads,
-                                    (size_t)mixed_turns(a) * sizeof(float2) + (size_t)(kHeadThreads >> a.lanes_log2) * mixed_pitch(a) * sizeof(float),
-                                    s>>>(a);
-    else
-        heads_any_kernel<TI, TO><<<grid, kHeadThreads, lds, s>>>(a);
-    return (int)hipGetLastError();
+static int launch_typed(HeadsArgs a, int32_t path, hipStream_t s) {
+    const int32_t wgs = (a.n_tokens - 1) / a.tokens_per_wg + 1;
+    const size_t turns = (size_t)a.tokens_per_wg * (size_t)(a.rot_dim / 2) * sizeof(float2);
+    const size_t mixed = (size_t)mixed_turns(a) * sizeof(float2) + (size_t)(kHeadThreads >> a.lanes_log2) * mixed_pitch(a) * sizeof(float);
+    for (; a.first_wg < wgs; a.first_wg += kMaxWgs) {
+        const unsigned grid = (unsigned)(wgs - a.first_wg < kMaxWgs ? wgs - a.first_wg : kMaxWgs);
+        if (path == kHeadsVec)
+            heads_vec_kernel<TI, TO><<<grid, kHeadThreads, turns, s>>>(a);
+        else if (path == kHeadsMixed)
+            heads_mixed_kernel<TI, TO><<<grid, kHeadThreads, mixed, s>>>(a);
+        else
+            heads_any_kernel<TI, TO><<<grid, kHeadThreads, turns, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return (int)e;
+        if (wgs - a.first_wg <= kMaxWgs) break;  // (before first_wg can pass 2^31)
+    }
+    return (int)hipSuccess;
 }
 
 template <class TI>

@@ -125,6 +125,22 @@ def test_norm_rope_layouts(dev, layout, D, R, adjacent):
     run_rope(dev, 9, 4, 2, D, R, adjacent, BF16, BF16, True, layout)
 
 
+def test_norm_rope_more_tokens_than_one_launch(dev):
+    """A workgroup to a token and more tokens than a launch has workgroups: those about the border and the last are right, and
+    every token is written. All tokens read one row; their positions differ."""
+    T, H, far = 2 ** 24 + 3, 256, 1 << 20
+    q = torch.randn(1, H, 2, device=dev).expand(T, H, 2)
+    out = torch.full((T, H, 2), float("nan"), dtype=BF16, device=dev)
+    pos = (torch.arange(T, device=dev) % far).int()
+    freq = torch.tensor([0.7], dtype=torch.float64, device=dev)
+    bpw.bpw_qk_norm_rope(q, None, out, None, pos, freq, q_gain=torch.ones(2, device=dev))
+    torch.cuda.synchronize()
+    assert all(not torch.isnan(x).any() for x in out.split(1 << 19))
+    at = [0, 1, 2 ** 22 - 1, 2 ** 22, 2 ** 24, T - 1]
+    want, mag = decode_ops.norm_rope(f64(q[at]), np.ones(2), pos[at].tolist(), freq.tolist(), 1e-6, False)
+    within(out[at], want, heads_tol(want, mag, BF16), "tokens")
+
+
 def test_norm_rope_zero_head_and_far_position(dev):
     """A head of zeros stays zero under eps; the farthest position's angle keeps its digits."""
     q = torch.zeros(1, 2, 64, device=dev)
