@@ -1047,12 +1047,12 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int
     write_out<T>(a, p.t, hq, 4 * ln, acc, top, sum, rounded);
 }
 
-// Many rows, which have few parts each: one wave to a row, no barriers.
+// Many rows, which have few parts each: one wave to a row, no barriers. Row r0 is the launch's first.
 template <class T, int DP>
-__global__ __launch_bounds__(kAttnThreads) void attn_join_rows_kernel(AttnArgs a, int mp, int ms, int rows) {
+__global__ __launch_bounds__(kAttnThreads) void attn_join_rows_kernel(AttnArgs a, int mp, int ms, int r0, int rows) {
     constexpr int LANES = DP / 4, GROUPS = 64 / LANES;
     const int lane = threadIdx.x & 63;
-    const int r = __builtin_amdgcn_readfirstlane(blockIdx.x * kAttnWaves + (threadIdx.x >> 6));
+    const int r = __builtin_amdgcn_readfirstlane(r0 + blockIdx.x * kAttnWaves + (threadIdx.x >> 6));
     if (r >= rows) return;
     const int hq = r % a.q_heads, bj = r / a.q_heads;
     const AttnParts p(a, mp, ms, bj / a.max_q, bj % a.max_q, hq);
@@ -1106,12 +1106,12 @@ template <int DP>
 constexpr int kShortWaves = DP == 256 ? 4 : 8;
 
 template <class T, int DP>
-__global__ __launch_bounds__(64 * kShortWaves<DP>) void attn_short_kernel(AttnArgs a, int tiles) {
+__global__ __launch_bounds__(64 * kShortWaves<DP>) void attn_short_kernel(AttnArgs a, int tiles, int wg0) {
     constexpr int WAVES = kShortWaves<DP>;
     __shared__ float part_o[WAVES][16][DP];
     __shared__ float4 part_ml[WAVES][16];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int bh = blockIdx.x / tiles, tile = blockIdx.x - bh * tiles, b = bh / a.kv_heads;
+    const int wg = wg0 + blockIdx.x, bh = wg / tiles, tile = wg - bh * tiles, b = bh / a.kv_heads;
     const int2 tok = seq_tokens(a, b);
     AttnSpan s;
     s.head = bh - b * a.kv_heads;
@@ -1166,11 +1166,16 @@ static int run_attn(const AttnArgs &a, hipStream_t st) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
     const int rows = a.n_seqs * a.max_q * a.q_heads;
-    if (rows >= kJoinRows)
-        attn_join_rows_kernel<T, DP><<<(unsigned)((rows + kAttnWaves - 1) / kAttnWaves), kAttnThreads, 0, st>>>(a, MP, MS, rows);
-    else
+    if (rows < kJoinRows) {
         attn_join_kernel<T, DP><<<(unsigned)rows, kAttnThreads, 0, st>>>(a, MP, MS);
-    return (int)hipGetLastError();
+        return (int)hipGetLastError();
+    }
+    const int wgs = (rows + kAttnWaves - 1) / kAttnWaves;
+    for (int first = 0; first < wgs && e == hipSuccess; first += kMaxWgs) {
+        attn_join_rows_kernel<T, DP><<<(unsigned)min(wgs - first, kMaxWgs), kAttnThreads, 0, st>>>(a, MP, MS, first * kAttnWaves, rows);
+        e = hipGetLastError();
+    }
+    return (int)e;
 }
 
 // Heads beyond 64 take tiles of 16 rows only from registers: with 32 the outputs spill, and reading the keys twice costs
@@ -1180,8 +1185,13 @@ template <class T, int DP>
 static int run_attn_tiles(const AttnArgs &a, int32_t mp, int32_t ms, hipStream_t st) {
     if (mp == 0) {  // short contexts
         const int tiles = (a.max_q * a.group + 15) / 16;
-        attn_short_kernel<T, DP><<<(unsigned)(a.n_seqs * a.kv_heads * tiles), 64 * kShortWaves<DP>, 0, st>>>(a, tiles);
-        return (int)hipGetLastError();
+        const int wgs = a.n_seqs * a.kv_heads * tiles;
+        hipError_t e = hipSuccess;
+        for (int first = 0; first < wgs && e == hipSuccess; first += kMaxWgs) {
+            attn_short_kernel<T, DP><<<(unsigned)min(wgs - first, kMaxWgs), 64 * kShortWaves<DP>, 0, st>>>(a, tiles, first);
+            e = hipGetLastError();
+        }
+        return (int)e;
     }
     if (ms == 16) {
         if (mp == 16) return run_attn<T, DP, 16, 16>(a, st);

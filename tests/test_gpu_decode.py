@@ -617,6 +617,19 @@ def test_attention_most_sequences(dev):
     a.check()
 
 
+@pytest.mark.parametrize("tokens,lens,Hq,Hk,prefix,pages", [
+    (2049, 0, 32, 2, 600, 0),     # the join: 2^26 query rows, idle sequences' among them
+    (4097, 9, 32, 32, 5, 1),      # the one-launch kernel: 2^23 tiles
+])
+def test_attention_more_rows_than_one_launch(dev, tokens, lens, Hq, Hk, prefix, pages):
+    """The last of the most sequences holds all tokens, so that its rows lie past the first launch's."""
+    n = 1024
+    a = Attn(dev, [0] * (n - 1) + [tokens], [0] * (n - 1) + [lens], Hq, Hk, 8, 16, prefix, F16, seed=47, max_pages=pages)
+    a.plan().run()
+    torch.cuda.synchronize()
+    a.check()
+
+
 def test_speculative_step_example(dev):
     """The operators together, from ternary projections to accepted tokens."""
     import importlib.util
