@@ -84,7 +84,14 @@ struct AttnSpan {
 };
 
 constexpr float kNone = -__builtin_inff();
-constexpr float kShiftLimit = 1024.0f;  // float16 weights reach 65504
+
+// A raised shift makes the largest weight 2^kLift, and a lane's sum of a step stays below kShiftLimit: about 1000 times that.
+// float16 holds weights from half of 2^-24 to 65504, so they begin at 2^6: one is lost only below 2^-31 of the largest
+// (at 2^0, a thousand positions at 2^-25 were all lost); bfloat16 has the exponents of float32.
+template <class T>
+constexpr float kLift = __is_same(T, __bf16) ? 0.0f : 6.0f;
+template <class T>
+constexpr float kShiftLimit = __is_same(T, __bf16) ? 1024.0f : 61440.0f;
 
 // The shift that a part is stored with. Maxima pass over NaN, so a row whose scores are all NaN has a sum of NaN at a shift
 // that is still kNone; any finite shift tells it from a row that saw nothing.
@@ -273,7 +280,7 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s) {
         for (int i = 0; i < NQ; ++i) {
             // The weights are taken against a shift, not the exact maximum: while a lane's sum of a step stays
             // below kShiftLimit no weight has lost anything, in float32 or in 16 bits, and no maximum is formed.
-            // Otherwise (the first step, a score far above all before it, NaN) the shift becomes the maximum.
+            // Otherwise (the first step, a score far above all before it, NaN) the shift becomes the maximum less kLift.
             f32x8 w;
             float sum = 0.0f;
             const auto weigh = [&](float shift) {
@@ -285,13 +292,13 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const AttnSpan &s) {
                 }
             };
             weigh(m[i]);  // (a shift of minus infinity gives infinities or NaN, which take the branch)
-            if (__any(!(sum < kShiftLimit))) {
+            if (__any(!(sum < kShiftLimit<T>))) {
                 float top = kNone;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) top = fmaxf(top, fmaxf(sc[i][0][r], sc[i][1][r]));
                 top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
-                const float up = fmaxf(m[i], top);
+                const float up = fmaxf(m[i], top - kLift<T>);
                 const float f = up == m[i] ? 1.0f : __builtin_amdgcn_exp2f(m[i] - up);
                 m[i] = up;
                 l[i] *= f;
@@ -635,12 +642,12 @@ __device__ __forceinline__ void attend_wide(const AttnArgs &a, const AttnSpan &s
             sum = part_sum[0] + part_sum[1];
         };
         const auto settle = [&](int b) {  // the shift raised where it has to be, as in the narrow path; weights in 16 bits
-            if (__any(!(sum < kShiftLimit))) {
+            if (__any(!(sum < kShiftLimit<T>))) {
                 float top = kNone;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[b][r]);
                 top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
-                const float up = fmaxf(m, top);
+                const float up = fmaxf(m, top - kLift<T>);
                 const float f = up == m ? 1.0f : __builtin_amdgcn_exp2f(m - up);
                 m = up;
                 l *= f;

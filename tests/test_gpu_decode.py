@@ -492,6 +492,34 @@ def test_attention_nan_scores_are_not_nothing_seen(dev, path):
     run("a step of the prefix")
 
 
+@pytest.mark.parametrize("path", ATTENTION_PATHS)
+def test_attention_float16_weights_far_below_the_largest(dev, path):
+    """One position of 32 has all but 2^-25 of the weight and values of zero: the output is what the others add. Weights are
+    rounded to float16 from 2^6 at the largest, so a step of its subnormals is 2^-30 of it, and half of one the error."""
+    n_q, lens, Hq, Hk, D, P, prefix, pages = ATTENTION_PATHS[path]
+    a = Attn(dev, n_q, lens, Hq, Hk, D, P, prefix, F16, seed=53, max_pages=pages)
+    a.scale = 1.0
+    a.q.zero_()
+    a.q[..., 0] = 1.0
+    a.k.copy_(torch.where(torch.isnan(a.k), a.k, 0.0))
+    a.v.copy_(a.v.abs() + 500.0)
+    for pages_of, n in [(a.prefix_pages, prefix)] + [(a.table[b], n) for b, n in enumerate(lens)]:
+        for pos in range(0, n, 32):
+            a.k[pages_of[pos // P].long(), :, pos % P, 0] = 17.5  # exp(-17.5) = 2^-25.2
+            a.v[pages_of[pos // P].long(), :, pos % P] = 0.0
+    a.plan().run()
+    torch.cuda.synchronize()
+    out, lse, mag = a.reference()
+    assert (out > 1e-4).all()
+    k, v = f64(a.k), f64(a.v)
+    v = v[np.isfinite(v)]
+    _, tol_lse = attn_tol(out, mag, f64(a.q), k[np.isfinite(k).all(-1)], v, D, prefix + max(lens), 1.0, F16)
+    # float32 errors as of lse, twice; the weights above and at the subnormals (32 to one of 2^6); the output
+    tol = mag * (2 * tol_lse[..., None] + half_step(F16)) + 32 * 2.0 ** -31 * v.max() + half_step(F16) * out + smallest(F16)
+    within(a.out, out, tol, "out")
+    within(a.lse, lse, tol_lse + 4 * U * np.abs(lse), "lse")
+
+
 @pytest.mark.parametrize("Hq,Hk,D,n,dt", [(3, 1, 64, 5, BF16), (8, 2, 128, 3, F16), (12, 2, 80, 7, BF16), (4, 4, 256, 9, F16)])
 def test_attention_values_that_are_not_finite_in_later_drafts(dev, Hq, Hk, D, n, dt):
     """NaN and infinities in the values of drafts: the tokens before them are as without, the others show them.
