@@ -1105,7 +1105,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_rows_kernel(AttnArgs a
     if (gr == 0) write_out<T>(a, p.t, hq, 4 * ln, acc, top, sum, rounded);
 }
 
-// Short contexts (prefix and page table together hold few positions): one launch. A workgroup of eight waves (four where
+// Short contexts (prefix and page table together hold few positions, and not many rows read them): one launch. A workgroup of eight waves (four where
 // one needs more than half of its SIMD's registers) takes one
 // (sequence, key/value head, tile of 16 query rows), its waves equal runs of the prefix's and the sequence's steps,
 // and joins their parts through LDS. The prefix is read by each sequence; at these lengths it comes from the caches.
@@ -1113,12 +1113,12 @@ template <int DP>
 constexpr int kShortWaves = DP == 256 ? 4 : 8;
 
 template <class T, int DP>
-__global__ __launch_bounds__(64 * kShortWaves<DP>) void attn_short_kernel(AttnArgs a, int tiles, int wg0) {
+__global__ __launch_bounds__(64 * kShortWaves<DP>) void attn_short_kernel(AttnArgs a, int tiles) {
     constexpr int WAVES = kShortWaves<DP>;
     __shared__ float part_o[WAVES][16][DP];
     __shared__ float4 part_ml[WAVES][16];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wg = wg0 + blockIdx.x, bh = wg / tiles, tile = wg - bh * tiles, b = bh / a.kv_heads;
+    const int bh = blockIdx.x / tiles, tile = blockIdx.x - bh * tiles, b = bh / a.kv_heads;
     const int2 tok = seq_tokens(a, b);
     AttnSpan s;
     s.head = bh - b * a.kv_heads;
@@ -1192,13 +1192,8 @@ template <class T, int DP>
 static int run_attn_tiles(const AttnArgs &a, int32_t mp, int32_t ms, hipStream_t st) {
     if (mp == 0) {  // short contexts
         const int tiles = (a.max_q * a.group + 15) / 16;
-        const int wgs = a.n_seqs * a.kv_heads * tiles;
-        hipError_t e = hipSuccess;
-        for (int first = 0; first < wgs && e == hipSuccess; first += kMaxWgs) {
-            attn_short_kernel<T, DP><<<(unsigned)min(wgs - first, kMaxWgs), 64 * kShortWaves<DP>, 0, st>>>(a, tiles, first);
-            e = hipGetLastError();
-        }
-        return (int)e;
+        attn_short_kernel<T, DP><<<(unsigned)(a.n_seqs * a.kv_heads * tiles), 64 * kShortWaves<DP>, 0, st>>>(a, tiles);
+        return (int)hipGetLastError();
     }
     if (ms == 16) {
         if (mp == 16) return run_attn<T, DP, 16, 16>(a, st);

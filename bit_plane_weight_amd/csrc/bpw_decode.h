@@ -9,7 +9,7 @@
 namespace bpw {
 
 // Most workgroups of a launch: a grid of 2^32 threads or more is not run as asked, and no error says so. What needs more
-// workgroups (of up to 512 threads) goes in several launches.
+// workgroups (of 256 threads) goes in several launches.
 constexpr int32_t kMaxWgs = 1 << 22;
 
 // ---------------------------------------------------------------- heads (norm, rotation, append)

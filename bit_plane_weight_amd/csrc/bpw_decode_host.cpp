@@ -224,6 +224,7 @@ namespace {
 struct AttnShape {
     int32_t dp, mp, ms;
     int32_t group, tiles_p, splits, split_units;
+    bool one_launch;
     int64_t cap, pieces_p, pieces_s;
     int32_t n_wgs;
     size_t sched, po, pml, total;  // workspace: bytes of the schedule, offsets of the parts, all
@@ -238,6 +239,12 @@ constexpr int64_t kNarrowWork = 65536;
 // sequence reads them. Measured, us a call (one launch, two): one sequence of 20 / 5 heads of 128, 128 positions 5.3, 9.3;
 // 256: 7.2, 9.1; 512: 9.0, 9.4; 704: 10.8, 9.6. 64 sequences of 256: 15.2, 17.0; with 256 of a prefix before them 23.6, 18.9.
 constexpr int64_t kShortWork = 65536;
+// Most of all its workgroups' steps (x padded head size), as each of them reads the sequence and the prefix for its 16 rows.
+// Measured over 582 calls within the bound above (heads of 64, 128, 256; 1 to 256 sequences of 1 to 128 tokens; with and
+// without a prefix): one launch takes 0.36 to 1.2 of two's time below 2^20 steps, 0.6 to 1.5 up to 2^21, 0.7 to 2.4 beyond.
+// 256 sequences of 8 heads of 128 over 240 shared and 32 own positions: 50.8, two launches 21.4. With both bounds the calls
+// take 1.7 % more than the better of the two on average (3.1 % without this one).
+constexpr int64_t kShortSteps = 1 << 21;
 constexpr int64_t kPieceCost = 3;   // tiles that a piece of a wide prefix costs beyond its own (queries in, parts out)
 constexpr int64_t kBusyCost = 32;   // tiles that all workgroups being busy with pieces costs
 
@@ -311,6 +318,8 @@ bpw_status attn_shape(const bpw_attn_shared_prefix_args *a, AttnShape *s) {
         }
         s->splits = (int32_t)((tiles + s->split_units - 1) / s->split_units);
     }
+    const int64_t steps = (int64_t)a->n_seqs * c.kv_heads * ((rows_s + 15) / 16) * (up + us) * s->dp;
+    s->one_launch = (s->cap + 2 * a->prefix_len) * s->dp <= kShortWork && steps <= kShortSteps;
     // one part per item and per run, or per piece of a wide prefix
     const int64_t waves = (int64_t)bpw::kAttnWaves * s->n_wgs;
     s->pieces_p = mp > 32 ? items_p * s->splits : up > 0 ? items_p + waves : 0;
@@ -403,7 +412,7 @@ bpw_status bpw_attn_shared_prefix(const bpw_attn_shared_prefix_args *a, void *d_
     k.part_ml = reinterpret_cast<float4 *>(ws + s.pml);
     k.part_s = s.pieces_p * s.mp * s.dp;
     k.ml_s = s.pieces_p * s.mp;
-    const int32_t mp = (s.cap + 2 * a->prefix_len) * s.dp <= kShortWork ? 0 : s.mp;  // 0: one launch
+    const int32_t mp = s.one_launch ? 0 : s.mp;
     const int e = s.dp == 64    ? bpw::launch_attn_d64(k, c.dtype, mp, s.ms, stream)
                   : s.dp == 128 ? bpw::launch_attn_d128(k, c.dtype, mp, s.ms, stream)
                                 : bpw::launch_attn_d256(k, c.dtype, mp, s.ms, stream);

@@ -5,7 +5,7 @@
 //
 // Each argument is one call, "n_tokens,n_seqs,max_q,q_heads,kv_heads,head_dim,prefix_len,page_size,max_pages:len x tokens,..."
 // with the sequences' lengths and query tokens ("122880x1,0x1"). Output, one line per argument:
-//   "<status> <mp> <ms> <workgroups> <most parts of a query row> <most parts a row may have>"
+//   "<status> <mp> <ms> <workgroups> <most parts of a query row> <most parts a row may have> <one launch>"
 // after checking that every run is one wave's, that the runs hold all units, and that every (item, run) has a part of
 // its own inside the workspace.
 #include "../../bit_plane_weight_amd/csrc/bpw_decode_host.cpp"
@@ -60,7 +60,7 @@ int main(int argc, char **argv) {
         AttnShape s{};
         const bpw_status st = attn_shape(&a, &s);
         if (st) {
-            std::printf("%d 0 0 0 0 %d\n", st, bpw::kAttnParts);
+            std::printf("%d 0 0 0 0 %d 0\n", st, bpw::kAttnParts);
             continue;
         }
         require((int)lens.size() == v[1], "sequences");
@@ -110,7 +110,7 @@ int main(int argc, char **argv) {
                 most_s = w1 - w0 + 1 > most_s ? w1 - w0 + 1 : most_s;
             }
         }
-        std::printf("%d %d %d %d %d %d\n", st, s.mp, s.ms, s.n_wgs, most_p + most_s, bpw::kAttnParts);
+        std::printf("%d %d %d %d %d %d %d\n", st, s.mp, s.ms, s.n_wgs, most_p + most_s, bpw::kAttnParts, s.one_launch);
     }
     return 0;
 }

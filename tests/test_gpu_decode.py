@@ -647,7 +647,7 @@ def test_attention_most_sequences(dev):
 
 @pytest.mark.parametrize("tokens,lens,Hq,Hk,prefix,pages", [
     (2049, 0, 32, 2, 600, 0),     # the join: 2^26 query rows, idle sequences' among them
-    (4097, 9, 32, 32, 5, 1),      # the one-launch kernel: 2^23 tiles
+    (4097, 9, 32, 32, 5, 1),      # few positions, 2^23 tiles
 ])
 def test_attention_more_rows_than_one_launch(dev, tokens, lens, Hq, Hk, prefix, pages):
     """The last of the most sequences holds all tokens, so that its rows lie past the first launch's."""

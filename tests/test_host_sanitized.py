@@ -294,7 +294,7 @@ def dealing(tmp_path_factory):
 
     def run(calls):
         """calls: (n_tokens, n_seqs, max_q, q_heads, kv_heads, head_dim, prefix, page, max_pages, [(length, tokens)]) ->
-        (status, mp, ms, workgroups, most parts of a row, most that a row may have) of each."""
+        (status, mp, ms, workgroups, most parts of a row, most that a row may have, one launch) of each."""
         lines = []
         for i in range(0, len(calls), 200):
             args = [",".join(map(str, c[:9])) + ":" + ",".join(f"{n}x{t}" for n, t in c[9]) for c in calls[i:i + 200]]
@@ -323,8 +323,18 @@ def test_attention_paths_of_the_gpu_tests(dealing):
     from test_gpu_decode import ATTENTION_PATHS as paths
     got = dealing([(sum(n_q), len(n_q), max(n_q), Hq, Hk, D, prefix, P, pages, list(zip(lens, n_q)))
                    for n_q, lens, Hq, Hk, D, P, prefix, pages in paths.values()])
-    for name, (status, mp, *_) in zip(paths, got):
-        assert status == 0 and (mp == int(name.split()[1].strip(",")) if "wide" in name else mp <= 32), name
+    for name, (status, mp, *_, one) in zip(paths, got):
+        assert status == 0 and one == (name == "short"), name
+        assert mp == int(name.split()[1].strip(",")) if "wide" in name else mp <= 32, name
+
+
+def test_attention_one_launch_by_positions_and_rows(dealing):
+    """Few positions go in one launch, unless many query rows would each read them: then the prefix is shared."""
+    call = lambda seqs, most, kv, G, D, prefix, pages: (seqs * most, seqs, most, kv * G, kv, D, prefix, 16, pages, [(16, most)] * seqs)  # noqa: E731
+    few = [call(1, 1, 5, 4, 128, 0, 32), call(64, 1, 8, 4, 128, 100, 16), call(16, 8, 2, 16, 256, 30, 8), call(64, 1, 8, 8, 64, 500, 1)]
+    many = [call(64, 8, 8, 8, 64, 500, 1), call(256, 1, 8, 1, 128, 240, 2), call(1024, 1, 8, 4, 64, 0, 32)]
+    longer = [call(1, 1, 5, 4, 128, 0, 33), call(1, 1, 5, 4, 128, 257, 1)]
+    assert [g[6] for g in dealing(few + many + longer)] == [1] * 4 + [0] * 5
 
 
 def test_attention_dealing_over_drawn_calls(dealing):
