@@ -138,11 +138,13 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_sums_kernel(VerifyArgs 
 }
 
 // Running sums over up to 64 lanes, and the first lane whose running sum exceeds the border (or, if none does, the last
-// with a positive value): that lane, or -1 if none is positive, and the sum before it.
-__device__ __forceinline__ int border_lane(double v, double run, double border, double &before, double &after) {
+// with a positive value): that lane, or -1 if none is positive, the sum before it and whether it exceeds. (before + its v may
+// not, as floating point sums.)
+__device__ __forceinline__ int border_lane(double v, double run, double border, double &before, double &after, bool &exceeds) {
     const double inc = scan_add(v);
     after = run + read_lane(inc, 63);
     const uint64_t some = __ballot(v > 0.0), over = __ballot(v > 0.0 && run + inc > border);
+    exceeds = over != 0;
     const int lane = over ? __builtin_ctzll(over) : some ? 63 - __builtin_clzll(some) : -1;
     before = lane < 0 ? run : run + read_lane(inc - v, lane < 0 ? 0 : lane);
     return lane;
@@ -154,9 +156,10 @@ template <class T>
 __device__ __forceinline__ int entry_in(const VerifyArgs &a, const Drawn<T> &r, bool rest, int c, int sub, double before,
                                         double border) {
     double m[4], after;
+    bool exceeds;
     const int i = entry_of(c, sub);
     masses(a, r, rest, i, m);
-    const int l = border_lane((m[0] + m[1]) + (m[2] + m[3]), before, border, before, after);
+    const int l = border_lane((m[0] + m[1]) + (m[2] + m[3]), before, border, before, after, exceeds);
     // the lane's own entry: the first over the border, else its last with mass (the sums' order can put the border past the
     // last)
     double cum = before;
@@ -206,20 +209,21 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_draw_kernel(VerifyArgs 
         const double border = (double)a.sample_u[b] * total;
         // the first chunk whose running sum exceeds the border, else the last with mass
         double run = 0.0, base = 0.0, before, after;
+        bool exceeds;
         int chunk = -1;
         for (int c0 = 0; c0 < a.chunks; c0 += 64) {
-            const int l = border_lane(c0 + lane < a.chunks ? sums[c0 + lane] : 0.0, run, border, before, after);
+            const int l = border_lane(c0 + lane < a.chunks ? sums[c0 + lane] : 0.0, run, border, before, after, exceeds);
             if (l >= 0) {
                 chunk = c0 + l;
                 base = before;
-                if (before + sums[chunk] > border) break;
+                if (exceeds) break;
             }
             run = after;
         }
         // in it the wave round, and in that the entry
         sub_sums(a, r, rest, chunk, subs);
         __syncthreads();
-        const int sub = border_lane(lane < kSubs ? subs[lane] : 0.0, base, border, before, after);
+        const int sub = border_lane(lane < kSubs ? subs[lane] : 0.0, base, border, before, after, exceeds);
         token = entry_in(a, r, rest, chunk, sub, before, border);
     }
     write_tokens<T>(a, b, n, token);
@@ -247,7 +251,8 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_small_kernel(VerifyArgs
     if (total > 0.0) {
         const double border = (double)a.sample_u[b] * total;
         double before, after;
-        const int sub = border_lane(lane < a.chunks * kSubs ? subs[lane] : 0.0, 0.0, border, before, after);
+        bool exceeds;
+        const int sub = border_lane(lane < a.chunks * kSubs ? subs[lane] : 0.0, 0.0, border, before, after, exceeds);
         token = entry_in(a, r, rest, sub / kSubs, sub % kSubs, before, border);
     }
     write_tokens<T>(a, b, r.n, token);

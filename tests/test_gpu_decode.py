@@ -735,6 +735,34 @@ def test_verify_borders(dev, V):
             run_verify(dev, base, None, tokens, torch.full((8, K), u), torch.full((8,), r))
 
 
+@pytest.mark.parametrize("V", [262145, 300001, 600000])
+def test_verify_more_than_a_wave_of_chunks(dev, V):
+    """Vocabularies of more than 64 chunks of 4096, the border in each 64 of them; mass only past the first 64; a draft that
+    takes all of it."""
+    target, draft, tokens, u, r = verify_case(5, 2, V, F32, V)
+    target[2, :, :262144] = 0.0
+    draft[3] = target[3, :2]
+    for x in (r, r * 0, r * 0 + 0.999, r * 0 + (1.0 - 2.0 ** -24), r * 0 + 1.0):
+        run_verify(dev, target, draft, tokens, u, x)
+    run_verify(dev, target, None, tokens, u, r)
+
+
+def test_verify_border_within_a_rounding_of_a_chunk(dev):
+    """Masses 1, 2^-53 and 2^-53 in the chunks 0, 2 and 3, halves in 10 and 70, r = 1/2: the border 1 + 2^-53 is passed in chunk 3,
+    by less than float64 tells from chunk 2's end, and not 60 chunks later."""
+    V, at = 71 * 4096, {0: 1.0, 2: 2.0 ** -53, 3: 2.0 ** -53, 10: 0.5, 70: 0.5}
+    target = torch.zeros(1, 2, V, device=dev)
+    for chunk, mass in at.items():
+        target[:, 1, chunk * 4096 + 7] = mass
+    target[0, 0, 5] = 1.0
+    out, acc = torch.zeros(1, 2, dtype=torch.int32, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    ws = torch.empty(bpw.bpw_verify_draft_workspace_bytes(1, V), dtype=torch.uint8, device=dev)
+    bpw.bpw_verify_draft(target, None, torch.full((1, 1), 5, dtype=torch.int32, device=dev), torch.zeros(1, 1, device=dev),
+                         torch.full((1,), 0.5, device=dev), out, acc, ws)
+    torch.cuda.synchronize()
+    assert acc.tolist() == [1] and out.tolist() == [[5, 3 * 4096 + 7]]
+
+
 def test_verify_strided_rows(dev):
     """Rows inside wider ones, steps out of order in memory, at an address no vector is aligned to."""
     target, draft, tokens, u, r = verify_case(3, 2, 5001, F32, 77)
