@@ -8,6 +8,7 @@ arrays.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import numpy as np
 
@@ -606,6 +607,15 @@ def _dtype_code(t, what: str, cache: bool = False) -> int:
     return code
 
 
+def _shaped(t, dtype: str, shape: tuple, what: str) -> int | None:
+    """As _checked, and refuses a larger tensor of several dimensions whose rows have another length than those of `shape`: the
+    kernels would take them from other places."""
+    n = math.prod(shape)
+    if t is not None and t.dim() > 1 and t.numel() > n and math.prod(t.shape[1:]) != math.prod(shape[1:]):
+        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+    return _checked(t, dtype, n, what)
+
+
 def _gpu(t, what: str) -> int:
     """Device address of a strided GPU tensor."""
     if not getattr(t, "is_cuda", False):
@@ -819,7 +829,7 @@ class SharedPrefixAttnPlan(_Bound):
         a.d_table = _gpu(table, "table")
         a.table_stride = max(table.stride(0), table.shape[1]) if n_seqs == 1 else table.stride(0)
         a.scale = kv.c.head_dim ** -0.5 if scale is None else float(scale)
-        a.d_lse = _checked(lse, "float32", q.shape[0] * q.shape[1], "lse")
+        a.d_lse = _shaped(lse, "float32", (q.shape[0], q.shape[1]), "lse")
         if d_ws is None:
             raise ValueError("a workspace is required")
         self._bind("bpw_attn_shared_prefix", a, (kv, q, out, prefix_pages, table, lens, q_starts, lse), d_ws)
@@ -861,11 +871,11 @@ class DraftVerifyPlan(_Bound):
                         (accepted, "accepted")):
             if t is None:
                 raise ValueError(f"{what} is required")
-        a.d_tokens = _checked(tokens, "int32", B * K, "tokens")
+        a.d_tokens = _shaped(tokens, "int32", (B, K), "tokens")
         a.d_n_draft = _checked(n_draft, "int32", B, "n_draft")
-        a.d_accept_u = _checked(accept_u, "float32", B * K, "accept_u")
+        a.d_accept_u = _shaped(accept_u, "float32", (B, K), "accept_u")
         a.d_sample_u = _checked(sample_u, "float32", B, "sample_u")
-        a.d_out_tokens = _checked(out_tokens, "int32", B * (K + 1), "out_tokens")
+        a.d_out_tokens = _shaped(out_tokens, "int32", (B, K + 1), "out_tokens")
         a.d_accepted = _checked(accepted, "int32", B, "accepted")
         if d_ws is None:
             raise ValueError("a workspace is required")

@@ -129,6 +129,29 @@ def test_binding_refuses_what_the_abi_cannot_see():
         verify_plan(out_tokens=fake(2, 3, dtype=torch.int32))
 
 
+def test_binding_refuses_rows_of_another_length():
+    """Enough elements, but in rows that the kernels would not find; flat tensors and more rows are taken."""
+    f32, i32 = torch.float32, torch.int32
+    for shape in ((5, 3), (3, 5), (3, 4, 2)):
+        with pytest.raises(ValueError, match=r"lse must be \[3, 4\]"):
+            attn_plan(lse=fake(*shape, dtype=f32))
+    with pytest.raises(ValueError, match=r"out_tokens must be \[2, 4\]"):
+        verify_plan(out_tokens=fake(2, 9, dtype=i32))
+    args = lambda **k: {"tokens": fake(2, 3, dtype=i32), "accept_u": fake(2, 3, dtype=f32), **k}  # noqa: E731
+    plan = lambda a: bpw.DraftVerifyPlan(fake(2, 4, 100, dtype=f32), None, a["tokens"], a["accept_u"], fake(2, dtype=f32),  # noqa: E731
+                                         fake(2, 4, dtype=i32), fake(2, dtype=i32), fake(4096, dtype=torch.uint8))
+    plan(args())
+    plan(args(tokens=fake(7, dtype=i32), accept_u=fake(5, 3, dtype=f32)))
+    plan(args(tokens=fake(1, 2, 3, dtype=i32)))
+    with pytest.raises(ValueError, match=r"tokens must be \[2, 3\]"):
+        plan(args(tokens=fake(2, 8, dtype=i32)))
+    with pytest.raises(ValueError, match=r"accept_u must be \[2, 3\]"):
+        plan(args(accept_u=fake(2, 4, dtype=f32)))
+    for shape in ((12,), (3, 2, 2), (9, 4)):
+        assert status_of(lambda: attn_plan(lse=fake(*shape, dtype=f32)).run(0)) is None
+    assert status_of(lambda: attn_plan(T=0, lse=fake(3, 4, dtype=f32)).run(0)) is None
+
+
 def append_plan(kv=None, T=3, Hk=2, D=64, R=64, src=torch.float32, **kw):
     return bpw.KvAppendPlan(kv or cache(), fake(T, Hk, D, dtype=src), fake(T, Hk, D, dtype=src), fake(T, dtype=torch.int64),
                             fake(T, dtype=torch.int32), fake(R // 2, dtype=torch.float64), **kw)
