@@ -456,6 +456,37 @@ def check_with_nan(a, what):
     within(a.lse, lse, tol_lse + 4 * U * np.abs(lse), f"{what} lse")
 
 
+@pytest.mark.parametrize("layout,dt", [("hnd", BF16), ("nhd", F16)])
+@pytest.mark.parametrize("path", ATTENTION_PATHS)
+def test_attention_paths(dev, path, layout, dt):
+    """Every path: as it is, with scores that rise along the pages and with nearly equal weights, and with pages missing: the first,
+    some in the middle and the last of the prefix, one of a sequence's, all of them."""
+    n_q, lens, Hq, Hk, D, P, prefix, pages = ATTENTION_PATHS[path]
+    a = Attn(dev, n_q, lens, Hq, Hk, D, P, prefix, dt, seed=59, layout=layout, max_pages=pages)
+
+    def run(what):
+        a.out.fill_(77.0), a.lse.fill_(77.0)
+        a.plan().run()
+        torch.cuda.synchronize()
+        a.check(what)
+
+    run("as it is")
+    flat_k = a.k.clone()
+    a.k *= torch.linspace(0.1, 6, a.k.shape[0], device=dev).to(dt)[:, None, None, None]
+    for a.scale in (2.0, 1e-30):
+        run(f"scale {a.scale}")
+    a.k, a.scale = flat_k, None
+    last = a.prefix_pages.numel() - 1
+    for i, bad in ((0, -1), (last // 2, 2 ** 31 - 1), (last // 2 + 1, -2 ** 31), (last, a.k.shape[0])):
+        a.prefix_pages[min(i, last)] = bad
+    a.table[0, 0] = -1
+    run("missing pages")
+    a.prefix_pages.fill_(-1)
+    run("no prefix page")
+    a.table.fill_(a.k.shape[0])
+    run("no page")
+
+
 @pytest.mark.parametrize("path", ATTENTION_PATHS)
 def test_attention_nan_scores_are_not_nothing_seen(dev, path):
     """Rows whose scores are all NaN in a part of their positions, or in all: a query of NaN, the one key a sequence has of its
