@@ -120,7 +120,6 @@ bpw_status run_heads(bpw::HeadsArgs &a, int32_t dt_in, int32_t dt_out, bool vec,
     return hip_status(bpw::launch_heads(a, dt_in, dt_out, path, stream), who);
 }
 
-// q and k (and v) share the input type, their outputs the other.
 bpw_status check_eps(float eps, const char *who) {
     if (!(std::isfinite(eps) && eps >= 0.0f)) return fail(BPW_E_INVAL, "%s: eps is negative or not finite", who);
     return BPW_OK;

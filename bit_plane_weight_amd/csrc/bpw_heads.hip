@@ -8,7 +8,8 @@
 // is already wrong in its third decimal; sine and cosine of the reduced turn are float32.
 //
 // Bound: HBM for prompts (each element read once and written once: 16384 tokens of 40 heads of 128 in bf16, 336 MB,
-// 66.4 us = 5.06 TB/s, a torch copy of 4 GiB 4.81), the launch for a decode step (one token 2.8 us). A
+// 66.3 us = 5.06 TB/s, where a copy of as many bytes with non-temporal loads and stores reaches 6.33), the launch for a
+// decode step (one token 2.8 us). A
 // workgroup takes whole tokens, so that the rot_dim / 2 sines and cosines are formed once per token
 // (by as many threads) and shared by its heads through LDS. In the vector path 2^lanes_log2 lanes hold one
 // head, each both partners of its pairs (8 elements of the first half and the 8 opposite ones, or 16

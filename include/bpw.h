@@ -569,22 +569,27 @@ bpw_status bpw_kv_append(const bpw_kv_append_args *a, void *stream);
  * Query token j of n_b sees the prefix and the first d_lens[b] - (n_b - 1 - j) own positions. Query head h
  * reads key/value head h / (q.heads / kv_heads):
  *   out = sum_i softmax_i(scale * <q, K_i>) V_i,   lse = log sum_i exp(scale * <q, K_i>)  (natural log).
- * A token that sees nothing gets out = 0 and lse = -inf. Scores, maxima, sums and outputs are held in
- * float32; the softmax weights are rounded to the cache's type for the matrix cores, and out is divided by
- * the sum of the rounded weights.
+ * A token that sees nothing gets out = 0 and lse = -inf; a NaN among the scores that it sees makes both NaN.
+ * Scores, maxima, sums and outputs are held in float32; the softmax weights are rounded to the cache's type for
+ * the matrix cores (float16: to 2^-30 of the largest at the finest), and out is divided by the sum of the rounded
+ * weights.
  * Device values out of range read no memory: a page outside [0, n_pages) has its positions hidden, lengths
  * are cut to [0, max_pages * page_size], query tokens past q's n_tokens or past max_q are left out.
  * Cache contents that a token does not see do not reach its results, whatever they are (NaN in an unused
  * row of a page, or in the value of a later draft). Tokens of no sequence are not written.
- * The prefix is read once for all sequences (once per 128 query rows of a key/value head), long prefixes
- * and sequences are split over the GPU, and the parts joined by a second launch, in a fixed order: the same
- * arguments give the same bits.
+ * The prefix is read once for all sequences (once per 128 query rows of a key/value head; a prefix of little work or
+ * few rows once per 16 or 32), long prefixes and sequences are split over the GPU, and the parts joined by a second
+ * launch. Where prefix and table hold few positions ((max_pages * page_size + 2 * prefix_len) * head_dim up to 2^16,
+ * head_dim as padded to 64, 128 or 256) and not many rows read them, one launch does it all, each 16 rows of a
+ * sequence reading the prefix by themselves. That goes by the table's columns, not by the lengths in it: a table
+ * cut to the columns in use is faster for short sequences. The joins have a fixed order: the same arguments give the
+ * same bits.
  * q and out have the cache's type; head_dim is a multiple of 8, 8 .. 256; pointers are 16-byte aligned and
  * strides multiples of 8 elements, a cache row's at least head_dim; q.heads is a multiple of kv_heads.
  * 1 <= n_seqs <= 1024. */
 typedef struct bpw_attn_shared_prefix_args {
     int32_t n_tokens, n_seqs, max_q;
-    float scale;                      /* finite, usually 1 / sqrt(head_dim) */
+    float scale;                      /* finite and above 0, usually 1 / sqrt(head_dim) */
     bpw_heads q, out;
     float *d_lse;                     /* device float [n_tokens][q.heads] or NULL */
     const int32_t *d_prefix_pages;    /* device int32 [ceil(prefix_len / page_size)] (NULL if prefix_len is 0) */
