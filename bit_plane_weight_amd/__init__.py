@@ -30,6 +30,9 @@ __all__ = [
     "PagedKv", "QkNormRopePlan", "bpw_qk_norm_rope", "KvAppendPlan", "bpw_kv_append",
     "bpw_attn_shared_prefix_workspace_bytes", "SharedPrefixAttnPlan", "bpw_attn_shared_prefix",
     "bpw_verify_draft_workspace_bytes", "DraftVerifyPlan", "bpw_verify_draft",
+    "PromptAttnPlan", "bpw_prompt_attn", "PagedKv4", "Kv4AppendPlan", "bpw_kv4_append",
+    "bpw_kv4_attn_workspace_bytes", "Kv4AttnPlan", "bpw_kv4_attn",
+    "bpw_token_logprobs_workspace_bytes", "TokenLogprobsPlan", "bpw_token_logprobs",
 ]
 
 
@@ -886,6 +889,211 @@ def bpw_verify_draft(target, draft, tokens, accept_u, sample_u, out_tokens, acce
                      stream=None) -> None:
     """One run of a DraftVerifyPlan."""
     DraftVerifyPlan(target, draft, tokens, accept_u, sample_u, out_tokens, accepted, d_ws, n_draft).run(stream)
+
+
+# ------------------------------------------------------------------------------ whole prompts, a cache in 4 bits, log probabilities
+
+
+def _one_device(*tensors) -> None:
+    """Refuses tensors of several GPUs: a launch runs on one."""
+    devices = {str(t.device) for t in tensors if t is not None}
+    if len(devices) > 1:
+        raise ValueError(f"tensors on several devices: {', '.join(sorted(devices))}")
+
+
+class PromptAttnPlan(_Bound):
+    """bpw_prompt_attn: causal attention over whole prompts, packed. q and out [tokens, q_heads, head_dim], k and v [tokens,
+    kv_heads, head_dim], all bfloat16 or all float16, any strides with contiguous elements; starts int32 [sequences + 1]
+    the first token of each and the end of the last; lse float32 [tokens, q_heads] or None; scale None: 1 /
+    sqrt(head_dim). Tokens of no sequence are not written."""
+
+    def __init__(self, q, k, v, out, starts, scale: float | None = None, lse=None):
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens, q_heads, head_dim]")
+        T, D = q.shape[0], q.shape[2]
+        if starts is None or starts.numel() < 2:
+            raise ValueError("starts must hold the first token of each sequence and the end of the last")
+        _one_device(q, k, v, out, starts, lse)
+        a = _lib.BpwPromptAttnArgs()
+        a.n_tokens, a.n_seqs, a.head_dim = T, starts.numel() - 1, D
+        a.scale = D ** -0.5 if scale is None else float(scale)
+        a.q, a.k, a.v, a.out = (_heads(t, T, D, n) for t, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out")))
+        _written(a.out, out, "out")
+        a.d_lse = _shaped(lse, "float32", (T, q.shape[1]), "lse")
+        a.d_starts = _checked(starts, "int32", 2, "starts")
+        self._bind("bpw_prompt_attn", a, (q, k, v, out, starts, lse))
+
+
+def bpw_prompt_attn(q, k, v, out, starts, scale: float | None = None, lse=None, stream=None) -> None:
+    """One run of a PromptAttnPlan."""
+    PromptAttnPlan(q, k, v, out, starts, scale, lse).run(stream)
+
+
+class PagedKv4:
+    """A paged key/value cache held in 4 bits (bpw_paged_kv4): k_codes and v_codes are uint8 GPU tensors [pages, kv_heads,
+    page_size, head_dim / 2], k_scales and v_scales [pages, kv_heads, page_size, head_dim / 32], any strides with
+    contiguous rows (those of the codes multiples of 16)."""
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales):
+        tensors = {"k_codes": k_codes, "v_codes": v_codes, "k_scales": k_scales, "v_scales": v_scales}
+        _one_device(*tensors.values())
+        c = _lib.BpwPagedKv4()
+        if k_codes.dim() != 4 or k_codes.shape[3] % 16:
+            raise ValueError("k_codes must be [pages, kv_heads, page_size, head_dim / 2], head_dim a multiple of 32")
+        c.n_pages, c.kv_heads, c.page_size = k_codes.shape[:3]
+        c.head_dim = 2 * k_codes.shape[3]
+        for (what, t), (x, d) in zip(tensors.items(), (("k", "d_k"), ("v", "d_v"), ("ks", "d_k_scale"), ("vs", "d_v_scale"))):
+            row = c.head_dim // (2 if "codes" in what else 32)
+            if str(t.dtype) != "torch.uint8":
+                raise TypeError(f"{what} must be torch.uint8, got {t.dtype}")
+            if tuple(t.shape) != (*k_codes.shape[:3], row):
+                raise ValueError(f"{what} must be {[*k_codes.shape[:3], row]}, got {list(t.shape)}")
+            if row > 1 and t.stride(3) != 1:
+                raise ValueError(f"{what}: a row must be contiguous")
+            if any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride())):
+                raise ValueError(f"{what} is an expanded view: its rows share memory")
+            setattr(c, d, _gpu(t, what))
+            # the stride of a dimension of one is free: 0, as nothing is reached by it
+            for n, st, y in zip(t.shape, t.stride(), ("page", "head", "row")):
+                setattr(c, f"{x}_{y}_stride", st if n > 1 else 0)
+        self.c, self.k_codes, self.v_codes, self.k_scales, self.v_scales = c, k_codes, v_codes, k_scales, v_scales
+
+    @property
+    def page_size(self) -> int:
+        return self.c.page_size
+
+    @property
+    def head_dim(self) -> int:
+        return self.c.head_dim
+
+
+class Kv4AppendPlan(_Bound):
+    """bpw_kv4_append: k and v [tokens, kv_heads, head_dim] written to the cache at slots (int64 [tokens]: page * page_size
+    + offset; outside the cache: not written), k normed and rotated on the way; q, if given, normed and rotated into q_out
+    in the same launch; k_values and v_values, if given, get what the codes stand for, as a prompt's attention reads it."""
+
+    def __init__(self, kv: PagedKv4, k, v, slots, positions=None, inv_freq=None, k_gain=None, q=None, q_out=None,
+                 q_gain=None, eps: float = 1e-6, interleaved: bool = False, k_values=None, v_values=None):
+        if k.dim() != 3:
+            raise ValueError("k must be [tokens, kv_heads, head_dim]")
+        T, D = k.shape[0], kv.c.head_dim
+        if slots is None:
+            raise ValueError("slots are required")
+        _one_device(kv.k_codes, k, v, slots, positions, inv_freq, k_gain, q, q_out, q_gain, k_values, v_values)
+        a = _lib.BpwKv4AppendArgs()
+        a.n_tokens, a.kv = T, kv.c
+        for name, t in (("k", k), ("v", v), ("q", q), ("q_out", q_out), ("k_values", k_values), ("v_values", v_values)):
+            setattr(a, name, _heads(t, T, D, name))
+            if name in ("q_out", "k_values", "v_values"):
+                _written(getattr(a, name), t, name)
+        a.d_slots = _checked(slots, "int64", T, "slots")
+        a.d_q_gain, a.d_k_gain = _checked(q_gain, "float32", D, "q_gain"), _checked(k_gain, "float32", D, "k_gain")
+        a.eps = float(eps)
+        a.rot = _rotation(positions, inv_freq, T, interleaved)
+        self._bind("bpw_kv4_append", a, (k, kv, v, slots, positions, inv_freq, k_gain, q, q_out, q_gain, k_values, v_values))
+
+
+def bpw_kv4_append(kv: PagedKv4, k, v, slots, positions=None, inv_freq=None, k_gain=None, q=None, q_out=None, q_gain=None,
+                   eps: float = 1e-6, interleaved: bool = False, k_values=None, v_values=None, stream=None) -> None:
+    """One run of a Kv4AppendPlan."""
+    Kv4AppendPlan(kv, k, v, slots, positions, inv_freq, k_gain, q, q_out, q_gain, eps, interleaved, k_values,
+                  v_values).run(stream)
+
+
+def _attn4_args(kv: PagedKv4, q, n_seqs: int, max_q: int, max_pages: int):
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, q_heads, head_dim]")
+    a = _lib.BpwKv4AttnArgs()
+    a.kv = kv.c
+    a.n_tokens, a.n_seqs, a.max_q, a.max_pages = q.shape[0], int(n_seqs), int(max_q), int(max_pages)
+    a.q = _heads(q, q.shape[0], kv.c.head_dim, "q")
+    return a
+
+
+def bpw_kv4_attn_workspace_bytes(kv: PagedKv4, q, n_seqs: int, max_q: int, max_pages: int | None = None) -> int:
+    """Workspace bytes of a Kv4AttnPlan over this cache and q [tokens, q_heads, head_dim]. max_pages: columns of the page
+    table (None: the cache's pages, which covers every table without repeated pages)."""
+    a = _attn4_args(kv, q, n_seqs, max_q, kv.c.n_pages if max_pages is None else max_pages)
+    return _lib.lib().bpw_kv4_attn_workspace_bytes(ctypes.byref(a))
+
+
+class Kv4AttnPlan(_Bound):
+    """bpw_kv4_attn: decode attention over a 4-bit cache. q and out [tokens, q_heads, head_dim] of bfloat16 or float16; table
+    int32 [sequences, max_pages], lens int32 [sequences] the positions of each; q_starts int32 [sequences + 1] the first
+    token of each; max_q the most tokens of one; d_ws a uint8 workspace; lse float32 [tokens, q_heads] or None; scale
+    None: 1 / sqrt(head_dim)."""
+
+    def __init__(self, kv: PagedKv4, q, out, table, lens, q_starts, max_q: int, d_ws, scale: float | None = None, lse=None):
+        if table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("table must be [sequences, max_pages] with contiguous rows")
+        if str(table.dtype) != "torch.int32":
+            raise TypeError(f"table must be torch.int32, got {table.dtype}")
+        if d_ws is None:
+            raise ValueError("a workspace is required")
+        if lens is None or q_starts is None:
+            raise ValueError("lens and q_starts are required")
+        _one_device(kv.k_codes, q, out, table, lens, q_starts, d_ws, lse)
+        n_seqs = table.shape[0]
+        a = _attn4_args(kv, q, n_seqs, max_q, table.shape[1])
+        a.out = _heads(out, q.shape[0], kv.c.head_dim, "out")
+        _written(a.out, out, "out")
+        a.d_lens = _checked(lens, "int32", n_seqs, "lens")
+        a.d_q_starts = _checked(q_starts, "int32", n_seqs + 1, "q_starts")
+        a.d_table = _gpu(table, "table")
+        a.table_stride = max(table.stride(0), table.shape[1]) if n_seqs == 1 else table.stride(0)
+        a.scale = kv.c.head_dim ** -0.5 if scale is None else float(scale)
+        a.d_lse = _shaped(lse, "float32", (q.shape[0], q.shape[1]), "lse")
+        self._bind("bpw_kv4_attn", a, (q, kv, out, table, lens, q_starts, lse), d_ws)
+
+
+def bpw_kv4_attn(kv: PagedKv4, q, out, table, lens, q_starts, max_q: int, d_ws, scale: float | None = None, lse=None,
+                 stream=None) -> None:
+    """One run of a Kv4AttnPlan."""
+    Kv4AttnPlan(kv, q, out, table, lens, q_starts, max_q, d_ws, scale, lse).run(stream)
+
+
+def bpw_token_logprobs_workspace_bytes(n_tokens: int, vocab: int, n_top: int = 0) -> int:
+    return _lib.lib().bpw_token_logprobs_workspace_bytes(int(n_tokens), int(vocab), int(n_top))
+
+
+class TokenLogprobsPlan(_Bound):
+    """bpw_token_logprobs: of softmax(scale * logits), logits [tokens, vocab] (any row stride): logprobs float32 [tokens] of
+    tokens int32 [tokens] (both None: none), entropy float32 [tokens] or None, top_tokens int32 and top_logprobs float32
+    [tokens, n_top] the n_top <= 32 most likely, ties to the lowest index (both None: none). scale: 1 / temperature. d_ws
+    may be None where bpw_token_logprobs_workspace_bytes is 0."""
+
+    def __init__(self, logits, tokens, logprobs, d_ws, entropy=None, top_tokens=None, top_logprobs=None, scale: float = 1.0):
+        if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+            raise ValueError("logits must be [tokens, vocab] with contiguous rows")
+        if (tokens is None) != (logprobs is None):
+            raise ValueError("tokens and logprobs go together")
+        if (top_tokens is None) != (top_logprobs is None):
+            raise ValueError("top_tokens and top_logprobs go together")
+        T, V = logits.shape
+        K = 0
+        if top_tokens is not None:
+            if top_tokens.dim() != 2 or top_tokens.shape[0] != T or tuple(top_logprobs.shape) != tuple(top_tokens.shape):
+                raise ValueError(f"top_tokens and top_logprobs must both be [{T}, n_top]")
+            K = top_tokens.shape[1]
+        _one_device(logits, tokens, logprobs, d_ws, entropy, top_tokens, top_logprobs)
+        a = _lib.BpwTokenLogprobsArgs()
+        a.n_tokens, a.vocab, a.n_top, a.dtype = T, V, K, _dtype_code(logits, "logits")
+        a.scale = float(scale)
+        a.d_logits, a.row_stride = _gpu(logits, "logits"), logits.stride(0) if T > 1 else 0
+        a.d_tokens, a.d_logprobs = _checked(tokens, "int32", T, "tokens"), _checked(logprobs, "float32", T, "logprobs")
+        a.d_entropy = _checked(entropy, "float32", T, "entropy")
+        if K:
+            a.d_top_tokens = _checked(top_tokens, "int32", T * K, "top_tokens")
+            a.d_top_logprobs = _checked(top_logprobs, "float32", T * K, "top_logprobs")
+        if d_ws is None:  # (refused by the library where one is needed)
+            d_ws = logits.new_empty(0)
+        self._bind("bpw_token_logprobs", a, (logits, tokens, logprobs, entropy, top_tokens, top_logprobs), d_ws)
+
+
+def bpw_token_logprobs(logits, tokens, logprobs, d_ws, entropy=None, top_tokens=None, top_logprobs=None,
+                       scale: float = 1.0, stream=None) -> None:
+    """One run of a TokenLogprobsPlan."""
+    TokenLogprobsPlan(logits, tokens, logprobs, d_ws, entropy, top_tokens, top_logprobs, scale).run(stream)
 
 
 # ------------------------------------------------------------------------------ measurement

@@ -134,6 +134,42 @@ class BpwVerifyArgs(ctypes.Structure):
                 ("d_sample_u", ctypes.c_void_p), ("d_out_tokens", ctypes.c_void_p), ("d_accepted", ctypes.c_void_p)]
 
 
+class BpwPromptAttnArgs(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int32), ("n_seqs", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q", BpwHeads), ("k", BpwHeads), ("v", BpwHeads), ("out", BpwHeads),
+                ("d_lse", ctypes.c_void_p), ("d_starts", ctypes.c_void_p)]
+
+
+class BpwPagedKv4(ctypes.Structure):
+    _fields_ = [("d_k", ctypes.c_void_p), ("d_v", ctypes.c_void_p), ("d_k_scale", ctypes.c_void_p),
+                ("d_v_scale", ctypes.c_void_p), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32)] + [
+        (f"{x}_{y}_stride", ctypes.c_int64) for x in ("k", "v", "ks", "vs") for y in ("page", "head", "row")]
+
+
+class BpwKv4AppendArgs(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int32), ("reserved", ctypes.c_uint32), ("k", BpwHeads), ("v", BpwHeads),
+                ("q", BpwHeads), ("q_out", BpwHeads), ("k_values", BpwHeads), ("v_values", BpwHeads),
+                ("d_slots", ctypes.c_void_p), ("d_q_gain", ctypes.c_void_p), ("d_k_gain", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("reserved2", ctypes.c_uint32), ("rot", BpwRotation), ("kv", BpwPagedKv4)]
+
+
+class BpwKv4AttnArgs(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int32), ("n_seqs", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q", BpwHeads), ("out", BpwHeads), ("d_lse", ctypes.c_void_p),
+                ("d_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int32),
+                ("reserved", ctypes.c_uint32), ("d_lens", ctypes.c_void_p), ("d_q_starts", ctypes.c_void_p),
+                ("kv", BpwPagedKv4)]
+
+
+class BpwTokenLogprobsArgs(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int32), ("vocab", ctypes.c_int32), ("n_top", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_uint32),
+                ("d_logits", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("d_tokens", ctypes.c_void_p),
+                ("d_logprobs", ctypes.c_void_p), ("d_entropy", ctypes.c_void_p), ("d_top_tokens", ctypes.c_void_p),
+                ("d_top_logprobs", ctypes.c_void_p)]
+
+
 class BpwError(RuntimeError):
     """A non-OK bpw_status, with the library's reason and (for validation) the offending position."""
 
@@ -230,6 +266,12 @@ def lib():
         "bpw_attn_shared_prefix": (i32, [ctypes.POINTER(BpwAttnArgs), vp, sz, vp]),
         "bpw_verify_draft_workspace_bytes": (sz, [i32, i32]),
         "bpw_verify_draft": (i32, [ctypes.POINTER(BpwVerifyArgs), vp, sz, vp]),
+        "bpw_prompt_attn": (i32, [ctypes.POINTER(BpwPromptAttnArgs), vp]),
+        "bpw_kv4_append": (i32, [ctypes.POINTER(BpwKv4AppendArgs), vp]),
+        "bpw_kv4_attn_workspace_bytes": (sz, [ctypes.POINTER(BpwKv4AttnArgs)]),
+        "bpw_kv4_attn": (i32, [ctypes.POINTER(BpwKv4AttnArgs), vp, sz, vp]),
+        "bpw_token_logprobs_workspace_bytes": (sz, [i32, i32, i32]),
+        "bpw_token_logprobs": (i32, [ctypes.POINTER(BpwTokenLogprobsArgs), vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)

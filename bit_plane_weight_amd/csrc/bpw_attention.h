@@ -1167,22 +1167,28 @@ __global__ __launch_bounds__(64 * kShortWaves<DP>) void attn_short_kernel(AttnAr
     }
 }
 
-template <class T, int DP, int MP, int MS>
-static int run_attn(const AttnArgs &a, hipStream_t st) {
-    attn_split_kernel<T, DP, MP, MS><<<(unsigned)a.n_wgs, kAttnThreads, (size_t)(5 * (a.n_seqs + 1)) * 4, st>>>(a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return (int)e;
+// The second launch: the parts of every query row.
+template <class T, int DP>
+static int run_join(const AttnArgs &a, int mp, int ms, hipStream_t st) {
     const int rows = a.n_seqs * a.max_q * a.q_heads;
     if (rows < kJoinRows) {
-        attn_join_kernel<T, DP><<<(unsigned)rows, kAttnThreads, 0, st>>>(a, MP, MS);
+        attn_join_kernel<T, DP><<<(unsigned)rows, kAttnThreads, 0, st>>>(a, mp, ms);
         return (int)hipGetLastError();
     }
     const int wgs = (rows + kAttnWaves - 1) / kAttnWaves;
+    hipError_t e = hipSuccess;
     for (int first = 0; first < wgs && e == hipSuccess; first += kMaxWgs) {
-        attn_join_rows_kernel<T, DP><<<(unsigned)min(wgs - first, kMaxWgs), kAttnThreads, 0, st>>>(a, MP, MS, first * kAttnWaves, rows);
+        attn_join_rows_kernel<T, DP><<<(unsigned)min(wgs - first, kMaxWgs), kAttnThreads, 0, st>>>(a, mp, ms, first * kAttnWaves, rows);
         e = hipGetLastError();
     }
     return (int)e;
+}
+
+template <class T, int DP, int MP, int MS>
+static int run_attn(const AttnArgs &a, hipStream_t st) {
+    attn_split_kernel<T, DP, MP, MS><<<(unsigned)a.n_wgs, kAttnThreads, (size_t)(5 * (a.n_seqs + 1)) * 4, st>>>(a);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? (int)e : run_join<T, DP>(a, MP, MS, st);
 }
 
 // Heads beyond 64 take tiles of 16 rows only from registers: with 32 the outputs spill, and reading the keys twice costs

@@ -1,5 +1,6 @@
 // bpw_decode.h - records and launchers shared by the host checks (bpw_decode_host.cpp) and the kernels
-// of the decode-step operators (bpw_heads.hip, bpw_attention*.hip, bpw_verify.hip). Not part of the ABI.
+// of the decode-step operators (bpw_heads.hip, bpw_attention*.hip, bpw_verify.hip), and those that bpw_requests_host.cpp
+// checks (bpw_prompt*.hip, bpw_kv4_append.hip, bpw_kv4_attention*.hip, bpw_logprobs.hip). Not part of the ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -150,5 +151,91 @@ struct VerifyArgs {
     int32_t n_seqs, max_drafts, vocab, chunks;
 };
 int launch_verify(const VerifyArgs &a, int32_t dtype, void *stream);
+
+// ---------------------------------------------------------------- whole prompts
+
+constexpr int kPromptTile = 64;  // positions a workgroup takes at a time
+
+struct PromptArgs {
+    const void *q, *k, *v;
+    void *out;
+    float *lse;
+    int64_t q_ts, q_hs, k_hs, v_hs, o_ts, o_hs;
+    int32_t k_ts, v_ts;
+    const int32_t *starts;
+    int32_t n_tokens, n_seqs, q_heads, kv_heads, group, head_dim;
+    int32_t slots;           // tiles of query rows of a key/value head, empty ones among them (prompt_slot)
+    int32_t first_wg;        // of this launch
+    float scale_log2;
+};
+
+// Tiles of `rows` query rows: those of a sequence whose first token has `before` rows before it begin at this slot, which
+// leaves room for all of its own, as floor(x + n) >= floor(x) + floor(n) and a sequence adds one. So the slots of a
+// sequence follow from its own start, and no launch or scan has to count tiles.
+inline __host__ __device__ int32_t prompt_slot(int32_t before, int32_t seq, int32_t rows) { return before / rows + seq; }
+
+int launch_prompt_d64(const PromptArgs &a, int32_t dtype, int32_t rows, void *stream);
+int launch_prompt_d128(const PromptArgs &a, int32_t dtype, int32_t rows, void *stream);
+int launch_prompt_d256(const PromptArgs &a, int32_t dtype, int32_t rows, void *stream);
+
+// ---------------------------------------------------------------- a cache held in 4 bits
+
+constexpr int kKv4Block = 32;   // elements that share a power of two
+
+// Codes and powers of a cache's keys or values, strides in bytes.
+struct Kv4Rows {
+    uint8_t *codes, *scales;
+    int64_t ps, hs, s_ps, s_hs;
+    int32_t rs, s_rs;
+};
+
+struct Kv4AppendArgs {
+    HeadSet q, k, v;         // out of k and v: the values that the codes stand for, or null
+    Kv4Rows kc, vc;
+    const int32_t *positions;
+    const double *inv_freq;
+    const int64_t *slots;
+    int64_t n_slots;
+    int32_t n_tokens, head_dim, rot_dim, interleaved;
+    int32_t page_log2;
+    int32_t lanes_log2;      // lanes of one head, eight elements each
+    int32_t vec;             // rows are read and written 16 bytes at a time
+    int32_t first_wg;        // of this launch
+    float eps;
+};
+int launch_kv4_append(const Kv4AppendArgs &a, int32_t dt_in, int32_t dt_out, void *stream);
+
+// Attention over it: AttnArgs without a prefix (its k and v are not used), dealt and joined as there.
+struct Attn4Args {
+    AttnArgs a;
+    Kv4Rows kc, vc;
+};
+int launch_attn4_d64(const Attn4Args &a, int32_t dtype, bool one_launch, void *stream);
+int launch_attn4_d128(const Attn4Args &a, int32_t dtype, bool one_launch, void *stream);
+int launch_attn4_d256(const Attn4Args &a, int32_t dtype, bool one_launch, void *stream);
+
+// ---------------------------------------------------------------- log probabilities
+
+constexpr int kLogprobThreads = 256;
+constexpr int kLogprobRound = 8 * kLogprobThreads;  // entries a workgroup takes at a time, eight neighbours a lane
+constexpr int kLogprobTop = 32;
+
+struct LogprobArgs {
+    const void *logits;
+    int64_t row_stride;
+    const int32_t *tokens;
+    float *logprobs, *entropy;
+    int32_t *top_tokens;
+    float *top_logprobs;
+    int32_t n_tokens, vocab, n_top;
+    int32_t parts;           // workgroups of a row
+    int32_t part_rounds;     // rounds of each
+    int32_t first;           // first row of this launch
+    float scale;
+    // workspace, where a row has several parts
+    float4 *stats;           // [n_tokens][parts]: largest logit, sum, sum of weighted differences
+    uint64_t *tops;          // [n_tokens][parts][n_top]
+};
+int launch_logprobs(const LogprobArgs &a, int32_t dtype, void *stream);
 
 }  // namespace bpw

@@ -1,0 +1,12 @@
+// bpw_prompt_d64.hip - the attention kernels of bpw_prompt.h for head sizes padded to 64.
+#include "bpw_prompt.h"
+
+namespace bpw {
+
+int launch_prompt_d64(const PromptArgs &a, int32_t dtype, int32_t rows, void *stream) {
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (dtype == 1) return run_prompt<__bf16, 64>(a, rows, s);
+    return run_prompt<_Float16, 64>(a, rows, s);
+}
+
+}  // namespace bpw

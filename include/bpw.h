@@ -639,6 +639,139 @@ size_t bpw_verify_draft_workspace_bytes(int32_t n_seqs, int32_t vocab);
 /* d_ws: 256-byte aligned, written by every call: calls that share one must not overlap. */
 bpw_status bpw_verify_draft(const bpw_verify_draft_args *a, void *d_ws, size_t ws_len, void *stream);
 
+/* ------------------------------------------------------------------------ whole prompts */
+
+/* Causal attention over whole prompts, packed one after another: sequence b has the tokens d_starts[b] ..
+ * d_starts[b + 1] - 1, and each of them sees itself and those of its sequence before it. Query head h reads key/value
+ * head h / (q.heads / k.heads):
+ *   out = sum_i softmax_i(scale * <q, k_i>) v_i,   lse = log sum_i exp(scale * <q, k_i>)  (natural log).
+ * Scores, maxima, sums and outputs are held in float32; the softmax weights are rounded to the inputs' type for the
+ * matrix cores (float16: to 2^-30 of the largest at the finest), and out is divided by the sum of the rounded weights. A
+ * NaN among the scores that a token sees makes its out and lse NaN; what it does not see does not reach its results,
+ * whatever it is (NaN in a later token's value). Starts are cut to [0, n_tokens]; tokens of no sequence (before the first
+ * start, behind the last) are not written, and an empty sequence is none. The sums have a fixed order: the same arguments
+ * give the same bits. One launch, no workspace.
+ * q, k, v and out share a type (BPW_BF16 or BPW_F16) and head_dim, a multiple of 8, 8 .. 256; pointers are 16-byte aligned
+ * and strides multiples of 8 elements, a token's of k and v at most 2^24. q.heads is a multiple of k.heads; k.heads equals
+ * v.heads. out may not overlap the inputs. n_tokens * q.heads / k.heads is at most 2^30, n_seqs 1 .. 2^20. */
+typedef struct bpw_prompt_attn_args {
+    int32_t n_tokens, n_seqs, head_dim;
+    float scale;                      /* finite and above 0, usually 1 / sqrt(head_dim) */
+    bpw_heads q, k, v, out;
+    float *d_lse;                     /* device float [n_tokens][q.heads] or NULL */
+    const int32_t *d_starts;          /* device int32 [n_seqs + 1], rising */
+} bpw_prompt_attn_args;
+
+bpw_status bpw_prompt_attn(const bpw_prompt_attn_args *a, void *stream);
+
+/* ------------------------------------------------------------------------ a cache held in 4 bits */
+
+/* A paged key/value cache of 4.25 bits an element. 32 neighbours of a head (a block) share a power of two, 2^(byte - 127),
+ * and each is a half byte: a sign above a number of one bit of mantissa and two of exponent, 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * (codes 0 .. 7; 8 .. 15 are their negatives). Byte i of a row holds element 2i in its low half and 2i + 1 in its high
+ * half. Power bytes are 0 .. 252; 255 makes all of its block NaN; 253 and 254 are not used. Position i of a page, head h:
+ * codes at d_k[page * k_page_stride + h * k_head_stride + i * k_row_stride] (head_dim / 2 bytes), powers at d_k_scale
+ * likewise (head_dim / 32 bytes); V likewise. Strides are in bytes. */
+typedef struct bpw_paged_kv4 {
+    uint8_t *d_k, *d_v;               /* device, 16-byte aligned; strides multiples of 16 */
+    uint8_t *d_k_scale, *d_v_scale;   /* device, any alignment and strides */
+    int32_t kv_heads;
+    int32_t head_dim;                 /* a multiple of 32, 32 .. 256 */
+    int32_t page_size;                /* positions of a page: a power of two, 16 .. 1024 */
+    int32_t n_pages;
+    int64_t k_page_stride, k_head_stride, k_row_stride;
+    int64_t v_page_stride, v_head_stride, v_row_stride;
+    int64_t ks_page_stride, ks_head_stride, ks_row_stride;
+    int64_t vs_page_stride, vs_head_stride, vs_row_stride;
+} bpw_paged_kv4;
+
+/* Append n_tokens keys and values to a 4-bit cache at slot d_slots[t] = page * page_size + offset (a slot outside
+ * [0, n_pages * page_size) writes nothing there; valid slots must differ from one another). Keys take norm and rotation as
+ * in bpw_qk_norm_rope on the way, held in float64, because an element may lie next to the border of two codes; values are
+ * taken as they are. A block's power of two is the smallest, 2^-125 .. 2^125, that leaves no element above 7 of it, so
+ * that none is off by more than it; elements go to the nearest code, of two as near to the even one, and to 6 above that;
+ * a block of zeros has 2^-125. A block with an infinity or NaN gets power byte 255 and codes 0.
+ * k_values and v_values (heads 0 leaves them out, independently) get the values that the codes stand for, every token's,
+ * padding tokens' too: what a prompt's own attention reads so that it sees what later steps see. The queries of the same
+ * tokens may be normed and rotated in the same launch (q, q_out, as in bpw_kv_append; in float32). k, v and q share a type
+ * (float32, bfloat16 or float16); q_out, k_values and v_values share one (bfloat16 or float16), rounded to it once. */
+typedef struct bpw_kv4_append_args {
+    int32_t n_tokens;
+    uint32_t reserved;                /* 0 */
+    bpw_heads k, v, q, q_out, k_values, v_values;
+    const int64_t *d_slots;           /* device int64 [n_tokens] */
+    const float *d_q_gain, *d_k_gain; /* device float [head_dim] or NULL: no norm */
+    float eps;                        /* finite, >= 0 */
+    uint32_t reserved2;               /* 0 */
+    bpw_rotation rot;
+    bpw_paged_kv4 kv;
+} bpw_kv4_append_args;
+
+bpw_status bpw_kv4_append(const bpw_kv4_append_args *a, void *stream);
+
+/* Attention of a decode step over a 4-bit cache. Sequence b has the query tokens d_q_starts[b] .. d_q_starts[b + 1] - 1
+ * (n_b of them, at most max_q; none for an idle sequence) and sees its d_lens[b] positions, held by the pages of row b of
+ * d_table (the query tokens' own among them, last): query token j of n_b the first d_lens[b] - (n_b - 1 - j). Sequences
+ * that share positions may name the same pages. Heads, out and lse as in bpw_attn_shared_prefix, a token that sees
+ * nothing gets out = 0 and lse = -inf, and device values out of range, unseen cache contents and padding are treated as
+ * there. Codes and powers become bfloat16 without rounding, float16 queries go in as two bfloat16 numbers without
+ * rounding, and the softmax weights as two, to 2^-17 of each: out carries no error of 16-bit products.
+ * Long sequences are split over the GPU and the parts joined by a second launch; where the table holds few positions and
+ * not many rows read them, one launch does it all (by the table's columns, as the lengths are on the device). The joins
+ * have a fixed order: the same arguments give the same bits.
+ * q and out share a type (BPW_BF16 or BPW_F16); their pointers are 16-byte aligned and strides multiples of 8 elements;
+ * q.heads is a multiple of kv_heads. 1 <= n_seqs <= 1024. */
+typedef struct bpw_kv4_attn_args {
+    int32_t n_tokens, n_seqs, max_q;
+    float scale;                      /* finite and above 0, usually 1 / sqrt(head_dim) */
+    bpw_heads q, out;
+    float *d_lse;                     /* device float [n_tokens][q.heads] or NULL */
+    const int32_t *d_table;           /* device int32 [n_seqs][table_stride] */
+    int64_t table_stride;             /* >= max_pages */
+    int32_t max_pages;                /* entries of a table row; max_pages * page_size <= 2^30 */
+    uint32_t reserved;                /* 0 */
+    const int32_t *d_lens;            /* device int32 [n_seqs] */
+    const int32_t *d_q_starts;        /* device int32 [n_seqs + 1], rising from 0 */
+    bpw_paged_kv4 kv;
+} bpw_kv4_attn_args;
+
+/* Device workspace bytes of a call with these arguments (0 if they are refused). */
+size_t bpw_kv4_attn_workspace_bytes(const bpw_kv4_attn_args *a);
+/* d_ws: 256-byte aligned, written by every call: calls that share one must not overlap. */
+bpw_status bpw_kv4_attn(const bpw_kv4_attn_args *a, void *d_ws, size_t ws_len, void *stream);
+
+/* ------------------------------------------------------------------------ log probabilities */
+
+/* Log probabilities of given tokens, with entropy and top alternatives. Row t of the logits x, p = softmax(scale * x):
+ *   logprobs[t] = log p[tokens[t]],   entropy[t] = -sum_v p_v log p_v  (natural log, 0 log 0 = 0),
+ *   top_tokens[t][0 .. n_top) = the entries of the largest logits, falling, ties to the lowest index, and top_logprobs
+ *   their log p.
+ * Logits of -inf have no mass (log p = -inf) and are never among the top: places that are left get token -1 and -inf. A
+ * row of nothing but -inf gives logprob -inf and entropy 0. A NaN or +inf in a row makes its logprob, entropy and
+ * top_logprobs NaN; NaN is never among the top tokens. A token outside [0, vocab) gets -inf (NaN in such a row).
+ * Differences to the largest logit (of at most 3.4e38; beyond it they are infinite) and their sums are held in float32, in
+ * a fixed order: the same arguments give the same bits. One launch where there are many rows, two where rows are split over the GPU. */
+typedef struct bpw_token_logprobs_args {
+    int32_t n_tokens;                 /* >= 0 */
+    int32_t vocab;                    /* 1 .. 2^24 */
+    int32_t n_top;                    /* 0 .. 32 */
+    int32_t dtype;                    /* of d_logits: a bpw_dtype */
+    float scale;                      /* 1 / temperature: finite and above 0 */
+    uint32_t reserved;                /* 0 */
+    const void *d_logits;             /* device [n_tokens][vocab], rows row_stride elements apart */
+    int64_t row_stride;
+    const int32_t *d_tokens;          /* device int32 [n_tokens] or NULL: no logprobs */
+    float *d_logprobs;                /* device float [n_tokens], NULL where d_tokens is */
+    float *d_entropy;                 /* device float [n_tokens] or NULL */
+    int32_t *d_top_tokens;            /* device int32 [n_tokens][n_top] (NULL if n_top is 0) */
+    float *d_top_logprobs;            /* device float [n_tokens][n_top] (NULL if n_top is 0) */
+} bpw_token_logprobs_args;
+
+/* Device workspace bytes (0 if a size is out of range, and where none is needed). */
+size_t bpw_token_logprobs_workspace_bytes(int32_t n_tokens, int32_t vocab, int32_t n_top);
+/* d_ws: 256-byte aligned, written by every call: calls that share one must not overlap. NULL where none is needed. */
+bpw_status bpw_token_logprobs(const bpw_token_logprobs_args *a, void *d_ws, size_t ws_len, void *stream);
+
 /* ------------------------------------------------------------------------ measurement helpers */
 
 /* Streaming-read probe (Tritium paper, "Method": achieved bandwidth is divided by a streaming-read
