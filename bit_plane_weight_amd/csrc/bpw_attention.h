@@ -450,11 +450,11 @@ __device__ __forceinline__ void wait_loads_to_lds() { asm volatile("s_waitcnt vm
 
 // Chunk keys. Rows of 128 bytes (DP = 64) come two to the 256 bytes of all banks, longer ones one or less.
 template <int DP>
-__device__ __forceinline__ int key_of_k(int row) {
+__device__ __forceinline__ constexpr int key_of_k(int row) {
     return DP == 64 ? (row >> 1) & 7 : row & 15;
 }
 template <int DP>
-__device__ __forceinline__ int key_of_v(int row) {
+__device__ __forceinline__ constexpr int key_of_v(int row) {
     return DP == 64 ? ((row >> 1) & 1) << 2 : ((row & 3) << 2) | ((row >> 2) & 3);
 }
 

@@ -154,8 +154,6 @@ int launch_verify(const VerifyArgs &a, int32_t dtype, void *stream);
 
 // ---------------------------------------------------------------- whole prompts
 
-constexpr int kPromptTile = 64;  // positions a workgroup takes at a time
-
 struct PromptArgs {
     const void *q, *k, *v;
     void *out;
@@ -174,9 +172,9 @@ struct PromptArgs {
 // sequence follow from its own start, and no launch or scan has to count tiles.
 inline __host__ __device__ int32_t prompt_slot(int32_t before, int32_t seq, int32_t rows) { return before / rows + seq; }
 
-int launch_prompt_d64(const PromptArgs &a, int32_t dtype, int32_t rows, void *stream);
-int launch_prompt_d128(const PromptArgs &a, int32_t dtype, int32_t rows, void *stream);
-int launch_prompt_d256(const PromptArgs &a, int32_t dtype, int32_t rows, void *stream);
+int launch_prompt_d64(const PromptArgs &a, int32_t dtype, bool many, void *stream);
+int launch_prompt_d128(const PromptArgs &a, int32_t dtype, bool many, void *stream);
+int launch_prompt_d256(const PromptArgs &a, int32_t dtype, bool many, void *stream);
 
 // ---------------------------------------------------------------- a cache held in 4 bits
 

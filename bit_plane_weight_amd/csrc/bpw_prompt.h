@@ -32,12 +32,35 @@ __device__ __forceinline__ int prompt_seq(const PromptArgs &a, int slot, int row
     }
 }
 
-template <class T, int DP, int WQ>
-__global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void prompt_kernel(PromptArgs a) {
+// The halves of a word that are finite, zeros for the others; a half's number where it is not finite, zero otherwise.
+template <class T>
+__device__ __forceinline__ uint32_t finite_halves(uint32_t x) {
+    constexpr uint32_t lo = __is_same(T, __bf16) ? 0x7F80u : 0x7C00u, hi = lo << 16;
+    return ((x & lo) == lo ? 0u : x & 0xFFFFu) | ((x & hi) == hi ? 0u : x & 0xFFFF0000u);
+}
+template <class T>
+__device__ __forceinline__ float odd_value(uint32_t half) {
+    constexpr uint32_t ones = __is_same(T, __bf16) ? 0x7F80u : 0x7C00u;
+    return (half & ones) == ones ? (float)__builtin_bit_cast(T, (uint16_t)half) : 0.0f;
+}
+
+typedef __attribute__((address_space(3))) const u32v4 lds_u32v4;
+typedef __attribute__((address_space(3))) const u32x2 lds_u32x2;
+
+// Shape of a kernel: a wave holds S sets of 32 query rows, WQ waves lie along the rows of a tile and the others along the
+// positions, of which a workgroup takes KT at a time and a wave two blocks of 32.
+template <int DP_, int S_, int WQ_>
+struct PromptShape {
+    static constexpr int DP = DP_, S = S_, WQ = WQ_;
+    static constexpr int PARTS = kAttnWaves / WQ, KT = 64 * PARTS, ROWS = 32 * S * WQ;
+};
+
+template <class T, class P, bool LSE>
+__global__ __launch_bounds__(kAttnThreads, 1) void prompt_kernel(PromptArgs a) {
+    constexpr int DP = P::DP, S = P::S, WQ = P::WQ, PARTS = P::PARTS, KT = P::KT, M = P::ROWS;
     constexpr int ROW = DP * 2, CPR = DP / 8, RPI = 64 / CPR;  // row bytes, chunks of a row, rows of one load
-    constexpr int KC = DP / 16, DB = DP / 32, M = 32 * WQ;
-    constexpr int PARTS = kAttnWaves / WQ, NB = kPromptTile / 32 / PARTS;  // waves along a tile, blocks of 32 of each
-    __shared__ WideLds<DP> lds;
+    constexpr int KC = DP / 16, DB = DP / 32, TILE = KT * ROW;  // bytes of a tile of keys or values
+    __shared__ __attribute__((aligned(4096))) uint8_t lds[4 * TILE];  // keys twice, values twice
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, g = lane >> 5, part = wave / WQ;
     const int D = a.head_dim;
@@ -49,28 +72,27 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void prompt_kernel
     const int len = t1 - t0, n_rows = len * a.group, row0 = (slot - prompt_slot(t0 * a.group, b, M)) * M;
     if (row0 < 0 || row0 >= n_rows) return;
     const int end = (min(row0 + M, n_rows) - 1) / a.group + 1;  // positions that the tile's last row sees
+    // tiles of positions, and those of them that every row sees whole
+    const int tiles = (end + KT - 1) / KT, full = (row0 / a.group + 1) / KT;
 
-    const int row_first = row0 + 32 * (wave % WQ), row = row_first + n;
-    const int token = row / a.group, hq = head * a.group + row - token * a.group;
-    const int vis = row < n_rows ? token + 1 : len;
-    // what all and what some of the wave's rows see
-    const int all_see = __builtin_amdgcn_readfirstlane(row_first / a.group + 1);
-    const int some_see = row_first < n_rows ? (min(row_first + 32, n_rows) - 1) / a.group + 1 : 0;
-
-    u32v4 q[KC];
-    {
+    const int row_first = row0 + 32 * S * (wave % WQ);
+    const int some_see = row_first < n_rows ? (min(row_first + 32 * S, n_rows) - 1) / a.group + 1 : 0;
+    u32v4 q[S][KC];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const int row = row_first + 32 * s + n, token = row / a.group, hq = head * a.group + row - token * a.group;
         const T *p = static_cast<const T *>(a.q) + (int64_t)(t0 + token) * a.q_ts + (int64_t)hq * a.q_hs;
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
-            q[c] = u32v4{0, 0, 0, 0};
-            if (row < n_rows && 16 * c + 8 * g < D) q[c] = *reinterpret_cast<const u32v4 *>(p + 16 * c + 8 * g);
+            q[s][c] = u32v4{0, 0, 0, 0};
+            if (row < n_rows && 16 * c + 8 * g < D) q[s][c] = *reinterpret_cast<const u32v4 *>(p + 16 * c + 8 * g);
         }
     }
     const T *kbase = static_cast<const T *>(a.k) + (int64_t)t0 * a.k_ts + (int64_t)head * a.k_hs;
     const T *vbase = static_cast<const T *>(a.v) + (int64_t)t0 * a.v_ts + (int64_t)head * a.v_hs;
 
-    constexpr int LOADS = 16 / RPI, GROUP = LOADS < 4 ? LOADS : 4;  // loads of a wave's sixteen rows, of one asm block
-    const uint32_t lds_k = (uint32_t)(size_t)(lds_u8 *)lds.k, lds_v = (uint32_t)(size_t)(lds_u8 *)lds.v;
+    constexpr int LOADS = 16 / RPI, GROUP = LOADS < 4 ? LOADS : 4;  // loads of sixteen rows, of one asm block
+    const uint32_t lds0 = (uint32_t)(size_t)(lds_u8 *)lds;
     uint32_t ks[LOADS], vs[LOADS];
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
@@ -78,260 +100,354 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void prompt_kernel
         ks[i] = 2 * (r * a.k_ts + 8 * ((lane % CPR) ^ key_of_k<DP>(r))) - 1024 * (i % GROUP);
         vs[i] = 2 * (r * a.v_ts + 8 * ((lane % CPR) ^ key_of_v<DP>(r))) - 1024 * (i % GROUP);
     }
-    // Moves tile `pos` to LDS, this wave's 16 positions of it. Positions past the sequence and elements past head_dim become
-    // zeros (a zero weight times whatever memory holds there would not be one).
-    const auto issue = [&](int buf, int pos) {
-        const int first = pos + 16 * wave;
-        const T *kp = kbase + (int64_t)first * a.k_ts, *vp = vbase + (int64_t)first * a.v_ts;
-        const uint32_t at = buf * (kPromptTile * ROW) + 16 * wave * ROW;
-        if (pos + kPromptTile <= len && D == DP) {
+    // Moves this wave's positions of tile `t` of the keys (or values) to LDS, sixteen of each 64, to the buffer of the tile two
+    // before. Positions past the sequence and elements past head_dim become zeros (a zero weight times whatever memory holds
+    // there would not be one).
+    const auto issue = [&](const T *base, int32_t stride, const uint32_t (&offset)[LOADS], bool values, int t) {
+        if (t >= tiles) return;
 #pragma unroll
-            for (int i = 0; i < LOADS; i += GROUP) {
-                load_to_lds<GROUP>(lds_k + at + 1024 * i, kp, reinterpret_cast<const uint32_t(&)[GROUP]>(ks[i]));
-                load_to_lds<GROUP>(lds_v + at + 1024 * i, vp, reinterpret_cast<const uint32_t(&)[GROUP]>(vs[i]));
+        for (int x = 0; x < KT / 64; ++x) {
+            const int first = KT * t + 64 * x + 16 * wave;
+            const T *p = base + (int64_t)first * stride;
+            const uint32_t at = (values ? 2 * TILE : 0) + (t & 1) * TILE + (64 * x + 16 * wave) * ROW;
+            if (first + 16 <= len && D == DP) {
+#pragma unroll
+                for (int i = 0; i < LOADS; i += GROUP)
+                    load_to_lds<GROUP>(lds0 + at + 1024 * i, p, reinterpret_cast<const uint32_t(&)[GROUP]>(offset[i]));
+                continue;
             }
-            return;
-        }
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            const int r = RPI * i + lane / CPR;  // of the wave's sixteen
-            const bool in = first + r < len;
-            const int ck = (lane % CPR) ^ key_of_k<DP>(r), cv = (lane % CPR) ^ key_of_v<DP>(r);
-            const uint32_t ko[1] = {ks[i] + 1024 * (i % GROUP)}, vo[1] = {vs[i] + 1024 * (i % GROUP)};
-            if (in && 8 * ck < D)
-                load_to_lds<1>(lds_k + at + 1024 * i, kp, ko);
-            else
-                *reinterpret_cast<u32v4 *>(&lds.k[buf][16 * wave * ROW + 1024 * i + 16 * lane]) = u32v4{0, 0, 0, 0};
-            if (in && 8 * cv < D)
-                load_to_lds<1>(lds_v + at + 1024 * i, vp, vo);
-            else
-                *reinterpret_cast<u32v4 *>(&lds.v[buf][16 * wave * ROW + 1024 * i + 16 * lane]) = u32v4{0, 0, 0, 0};
+            for (int i = 0; i < LOADS; ++i) {
+                const int r = RPI * i + lane / CPR;  // of the sixteen
+                const int chunk = (lane % CPR) ^ (values ? key_of_v<DP>(r) : key_of_k<DP>(r));
+                const uint32_t o[1] = {offset[i] + 1024 * (i % GROUP)};
+                if (first + r < len && 8 * chunk < D)
+                    load_to_lds<1>(lds0 + at + 1024 * i, p, o);
+                else
+                    *reinterpret_cast<u32v4 *>(&lds[at + 1024 * i + 16 * lane]) = u32v4{0, 0, 0, 0};
+            }
         }
     };
+    const auto issue_k = [&](int t) { issue(kbase, a.k_ts, ks, false, t); };
+    const auto issue_v = [&](int t) { issue(vbase, a.v_ts, vs, true, t); };
 
-    // LDS addresses of this lane's reads; blocks of 32 (and 16) positions are whole keys apart
-    uint32_t ka[KC], va[DB][2];
+    // LDS addresses of this lane's reads of the current tiles. The chunk of element group c is chosen by an exclusive-or of the
+    // first one's address (blocks of 32 and 16 positions are whole keys apart), and so is the other buffer.
+    uint32_t ka = lds0 + (64 * part + n) * ROW + ((g ^ key_of_k<DP>(n)) * 16), va;
+    constexpr uint32_t V8 = 16 * (key_of_v<DP>(8) ^ key_of_v<DP>(0));  // of the row 8 further on
+    {
+        const int i = lane & 15, r = 4 * g + (i >> 2), chunk = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
+        va = lds0 + 2 * TILE + (64 * part + r) * ROW + ((chunk ^ key_of_v<DP>(r)) * 16) + (i & 1) * 8;
+    }
+    const auto key_frag = [&](int blk, int c) { return *(lds_u32v4 *)((ka ^ (32 * c)) + blk * 32 * ROW); };
+    const auto value_frag = [&](int x, int c) {  // positions 16 x .. 16 x + 15 of this wave's
+        const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)((va ^ (64 * c)) + 16 * x * ROW)));
+        const u32x2 z = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)((va ^ (64 * c) ^ V8) + (16 * x + 8) * ROW)));
+        return u32v4{y.x, y.y, z.x, z.y};
+    };
+
+    // sc: scores of two blocks of 32 positions; w, p: weights of the last one, in float32 and as operands
+    f32x16 o[S][DB], sc[2][S];
+    f32x8 w[S][2];
+    u32v4 p[S][2];
+    float m[S], l[S], lr[S], most[S];
 #pragma unroll
-    for (int c = 0; c < KC; ++c) ka[c] = n * ROW + (((2 * c + g) ^ key_of_k<DP>(n)) * 16);
+    for (int s = 0; s < S; ++s) {
+        m[s] = kNone;
+        l[s] = lr[s] = 0.0f;
 #pragma unroll
-    for (int c = 0; c < DB; ++c)
+        for (int c = 0; c < DB; ++c) o[s][c] = f32x16{};
+    }
+    const auto scores = [&](int which, int blk) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int i = lane & 15, r = 8 * h + 4 * g + (i >> 2);
-            const int chunk = 4 * c + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
-            va[c][h] = r * ROW + ((chunk ^ key_of_v<DP>(r)) * 16) + (i & 1) * 8;
+        for (int s = 0; s < S; ++s) sc[which][s] = f32x16{};
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+            const u32v4 f = key_frag(blk, c);
+#pragma unroll
+            for (int s = 0; s < S; ++s) sc[which][s] = mma32<T>(f, q[s][c], sc[which][s]);
         }
-
-    f32x16 o[DB];
+    };
+    const auto values = [&](int blk) {
 #pragma unroll
-    for (int c = 0; c < DB; ++c) o[c] = f32x16{};
-    float m = kNone, l = 0.0f, lr = 0.0f;
-
-    int pos0 = 0;
-    issue(0, 0);
-    // Tile `pos0`, which lies in LDS buffer `buf`.
-    const auto tile = [&](auto which) {
-        constexpr int buf = decltype(which)::value;
-        wait_loads_to_lds();
-        __syncthreads();  // this tile is there, and nobody reads the one before it any more
-        if (pos0 + kPromptTile < end) issue(buf ^ 1, pos0 + kPromptTile);
-        const int here = pos0 + 32 * part * NB;  // this wave's first position
-        pos0 += kPromptTile;
-        if (here >= some_see) return;
-        const bool hidden = here + 32 * NB > all_see;
-
-        constexpr int GK = 4, NGB = KC / GK, NG = NB * NGB;
-        f32x16 sc[NB];
-        u32v4 kf[2][GK], vf[2][DB], p[NB][2];
-        const auto read_k = [&](int x) {
-            const uint8_t *q0 = &lds.k[buf][(part * NB + x / NGB) * 32 * ROW];
-#pragma unroll
-            for (int c = 0; c < GK; ++c) kf[x & 1][c] = *reinterpret_cast<const u32v4 *>(q0 + ka[(x * GK + c) % KC]);
-        };
-        const auto read_v = [&](int x) {  // positions 16 x .. 16 x + 15 of this wave's blocks
-            const uint8_t *v0 = &lds.v[buf][(32 * part * NB + 16 * x) * ROW];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int c = 0; c < DB; ++c) {
-                const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds_u8 *)(v0 + va[c][0])));
-                const u32x2 z = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds_u8 *)(v0 + va[c][1])));
-                vf[x & 1][c] = u32v4{y.x, y.y, z.x, z.y};
+                const u32v4 f = value_frag(2 * blk + h, c);
+#pragma unroll
+                for (int s = 0; s < S; ++s) o[s][c] = mma32<T>(f, p[s][h], o[s][c]);
             }
-        };
-        const auto scores = [&](int blk) {
-            sc[blk] = f32x16{};
+    };
+    const auto weigh_set = [&](int which, int s, float shift) {
+        float top = 0.0f;
 #pragma unroll
-            for (int x = blk * NGB; x < (blk + 1) * NGB; ++x) {
-                if (x + 1 < NG) read_k(x + 1);
+        for (int r = 0; r < 16; ++r) {
+            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[which][s][r], a.scale_log2, -shift));
+            w[s][r >> 3][r & 7] = e;
+            top = fmaxf(top, e);
+        }
+        most[s] = top;
+    };
+    const auto weigh = [&](int which) {
 #pragma unroll
-                for (int c = 0; c < GK; ++c) sc[blk] = mma32<T>(kf[x & 1][c], q[(x * GK + c) % KC], sc[blk]);
-            }
-        };
-        // Values that only some rows see and that are not finite: one token at a time, the last first, with the values
-        // that it does not see set to zero; only its rows take the result.
-        const auto values_by_token = [&](int x, u32v4 w) {
-            for (int t = (min(row_first + 32, n_rows) - 1) / a.group; t >= row_first / a.group; --t) {
+        for (int s = 0; s < S; ++s) weigh_set(which, s, m[s]);
+    };
+    // The weights are taken against a shift, not the exact maximum: while none passes kShiftLimit nothing is lost, in float32 or
+    // in 16 bits, and no maximum is formed. Otherwise (the first block, a score far above all before it) the shift
+    // becomes the maximum less kLift. (A shift of minus infinity gives infinities or NaN.)
+    const auto raise = [&](int which) {
+        bool high = false;
 #pragma unroll
-                for (int c = 0; c < DB; ++c) {
+        for (int s = 0; s < S; ++s) high = high || !(most[s] < kShiftLimit<T>);
+        if (!__any(high)) return;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int at = here + 16 * x + 8 * (e >> 1) + 4 * g + 2 * (e & 1);
-                        if (at > t) vf[x & 1][c][e] &= 0xFFFF0000u;
-                        if (at + 1 > t) vf[x & 1][c][e] &= 0x0000FFFFu;
-                    }
-                    const f32x16 y = mma32<T>(vf[x & 1][c], w, o[c]);
+        for (int s = 0; s < S; ++s) {
+            float top = kNone;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[c][e] = token == t ? y[e] : o[c][e];
-                }
-            }
-        };
-        const auto values = [&](int blk) {
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[which][s][r]);
+            top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
+            const float up = fmaxf(m[s], top - kLift<T>);
+            const float f = up == m[s] ? 1.0f : __builtin_amdgcn_exp2f(m[s] - up);
+            m[s] = up;
+            l[s] *= f;
+            lr[s] *= f;
 #pragma unroll
-            for (int x = 2 * blk; x < 2 * blk + 2; ++x) {
-                if (x + 1 < 2 * NB) read_v(x + 1);
-                if (hidden) {
-                    uint32_t found = 0;
+            for (int c = 0; c < DB; ++c) o[s][c] *= f;
+            weigh_set(which, s, up == kNone ? 0.0f : up);
+        }
+    };
+    // Weights in 16 bits: half a step of relative error each; o is divided by the sum of the rounded weights, so that errors
+    // they share cancel. lse takes the sum of the unrounded ones.
+    const auto pack = [&]() {
 #pragma unroll
-                    for (int c = 0; c < DB; ++c)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) found |= maybe_not_finite<T>(vf[x & 1][c][e]);
-                    if (__any(found != 0)) {
-                        values_by_token(x, p[blk][x & 1]);
-                        continue;
-                    }
-                }
-#pragma unroll
-                for (int c = 0; c < DB; ++c) o[c] = mma32<T>(vf[x & 1][c], p[blk][x & 1], o[c]);
-            }
-        };
-        f32x8 w[2];
-        float sum;
-        const auto hide = [&](int blk) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                if (here + 32 * blk + 8 * (r >> 2) + 4 * g + (r & 3) >= vis) sc[blk][r] = kNone;
-        };
-        const auto weigh = [&](int blk, float shift) {
-            float part_sum[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[blk][r], a.scale_log2, -shift));
-                w[r >> 3][r & 7] = e;
-                part_sum[r >> 3] += e;
-            }
-            sum = part_sum[0] + part_sum[1];
-        };
-        // The shift raised where a lane's sum passes the limit (as in attend()), the weights in 16 bits: half a step of relative
-        // error each; o is divided by the sum of the rounded weights, so that errors they share cancel.
-        const auto settle = [&](int blk) {
-            if (__any(!(sum < kShiftLimit<T>))) {
-                float top = kNone;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[blk][r]);
-                top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
-                const float up = fmaxf(m, top - kLift<T>);
-                const float f = up == m ? 1.0f : __builtin_amdgcn_exp2f(m - up);
-                m = up;
-                l *= f;
-                lr *= f;
-#pragma unroll
-                for (int c = 0; c < DB; ++c) o[c] *= f;
-                weigh(blk, up == kNone ? 0.0f : up);
-            }
-            l += sum;
+        for (int s = 0; s < S; ++s)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                p[blk][h] = __builtin_bit_cast(u32v4, __builtin_convertvector(w[h], typename Vec8<T>::type));
-                lr = sum8<T>(p[blk][h], lr);
+                if constexpr (LSE) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) sum += w[s][h][r];
+                    l[s] += sum;
+                }
+                p[s][h] = __builtin_bit_cast(u32v4, __builtin_convertvector(w[s][h], typename Vec8<T>::type));
+                lr[s] = sum8<T>(p[s][h], lr[s]);
             }
-        };
-        read_k(0);
-        scores(0);
-        read_v(0);
-        __builtin_amdgcn_sched_barrier(0);
-        if (hidden) hide(0);
-        weigh(0, m);
-        if constexpr (NB == 2) scores(1);
-        settle(0);
-        if constexpr (NB == 2) {
-            if (hidden) hide(1);
-            values(0);
-            weigh(1, m);
-            settle(1);
-        }
-        values(NB - 1);
     };
-    while (true) {
-        tile(std::integral_constant<int, 0>{});
-        if (pos0 >= end) break;
-        tile(std::integral_constant<int, 1>{});
-        if (pos0 >= end) break;
+
+    issue_k(0);
+    issue_v(0);
+    issue_k(1);
+    int t = 0;
+    // Tiles that every row sees whole, a block of 32 positions after another: the products of the last block's values beside
+    // this block's exponentials, those of the next block's scores beside the rounding of its weights. Keys run a tile ahead.
+    if (full > 0) {
+        wait_loads_to_lds();
+        __syncthreads();
+        scores(0, 0);
+        weigh(0);
+        raise(0);
+        pack();
+        scores(1, 1);
+        ka ^= TILE;
+        for (; t + 1 < full; ++t) {
+            wait_loads_to_lds();
+            __syncthreads();  // these tiles are there, and nobody reads those before them any more
+            issue_v(t + 1);
+            issue_k(t + 2);
+            values(0);
+            weigh(1);
+            raise(1);
+            pack();
+            scores(0, 0);
+            values(1);
+            weigh(0);
+            raise(0);
+            pack();
+            scores(1, 1);
+            ka ^= TILE;
+            va ^= TILE;
+        }
+        wait_loads_to_lds();
+        __syncthreads();
+        issue_v(t + 1);
+        issue_k(t + 2);
+        values(0);
+        weigh(1);
+        raise(1);
+        pack();
+        values(1);
+        va ^= TILE;
+        ++t;
+    }
+    for (; t < tiles; ++t) {  // tiles on the diagonal, each step by itself
+        wait_loads_to_lds();
+        __syncthreads();
+        issue_v(t + 1);
+#pragma unroll 1
+        for (int blk = 0; blk < 2; ++blk) {
+            const int here = KT * t + 64 * part + 32 * blk;
+            if (here >= some_see) break;
+#pragma unroll
+            for (int s = 0; s < S; ++s) sc[0][s] = f32x16{};
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                const u32v4 f = key_frag(blk, c);
+#pragma unroll
+                for (int s = 0; s < S; ++s) sc[0][s] = mma32<T>(f, q[s][c], sc[0][s]);
+            }
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const int row = row_first + 32 * s + n, vis = row < n_rows ? row / a.group + 1 : len;
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (here + 8 * (r >> 2) + 4 * g + (r & 3) >= vis) sc[0][s][r] = kNone;
+            }
+            weigh(0);
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (m[s] == kNone) most[s] = __builtin_inff();  // (rows that have seen nothing: their weights are NaN here)
+            raise(0);
+            pack();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int x = 2 * blk + h;
+                uint32_t found = 0;
+#pragma unroll
+                for (int c = 0; c < DB; ++c) {
+                    const u32v4 f = value_frag(x, c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) found |= maybe_not_finite<T>(f[e]);
+                }
+                const bool odd = __any(found != 0);
+#pragma unroll
+                for (int c = 0; c < DB; ++c) {
+                    u32v4 f = value_frag(x, c);
+                    if (odd) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) f[e] = finite_halves<T>(f[e]);
+                    }
+#pragma unroll
+                    for (int s = 0; s < S; ++s) o[s][c] = mma32<T>(f, p[s][h], o[s][c]);
+                }
+                if (odd) {
+                    // Values that are not finite, taken out above as a weight of zero does not hide them, are added to the rows
+                    // that see them (times any weight above zero they stay what they are).
+#pragma unroll 1
+                    for (int i = 0; i < 16; ++i) {
+                        const int r = 64 * part + 16 * x + i;  // of the tile
+#pragma unroll
+                        for (int c = 0; c < DB; ++c)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const u32x2 v = *(lds_u32x2 *)(lds0 + 2 * TILE + (t & 1) * TILE + r * ROW + (((4 * c + j) ^ key_of_v<DP>(r)) * 16) + 8 * g);
+#pragma unroll
+                                for (int s = 0; s < S; ++s) {
+                                    const int row = row_first + 32 * s + n;
+                                    const bool sees = row < n_rows && KT * t + r <= row / a.group;
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const float y = odd_value<T>((e & 2 ? v.y : v.x) >> (16 * (e & 1)));
+                                        o[s][c][4 * j + e] += sees ? y : 0.0f;
+                                    }
+                                }
+                            }
+                    }
+                }
+            }
+        }
+        __syncthreads();  // nobody reads these keys any more
+        issue_k(t + 2);
+        ka ^= TILE;
+        va ^= TILE;
     }
 
-    l += __shfl_xor(l, 32);
-    lr += __shfl_xor(lr, 32);
-    m = stored_shift(m, l);
-    if constexpr (PARTS == 2) {  // the second wave of the same rows hands over through LDS
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        l[s] += __shfl_xor(l[s], 32);
+        lr[s] += __shfl_xor(lr[s], 32);
+        m[s] = stored_shift(m[s], lr[s]);
+    }
+    if constexpr (PARTS == 2) {  // the wave of the same rows' other positions hands over through LDS
         constexpr int PAD = DP + 4;
-        float *box = reinterpret_cast<float *>(&lds) + (wave % WQ) * (32 * PAD);
-        float4 *ml = reinterpret_cast<float4 *>(reinterpret_cast<float *>(&lds) + WQ * 32 * PAD) + 32 * (wave % WQ);
-        static_assert((WQ * 32 * PAD + 4 * 32 * WQ) * 4 <= sizeof(WideLds<DP>), "the join fits the tiles' LDS");
+        static_assert(WQ * S * 32 * (PAD + 4) * 4 <= sizeof lds, "the join fits the tiles' LDS");
+        float *box = reinterpret_cast<float *>(lds) + (wave % WQ) * (S * 32 * PAD);
+        float4 *ml = reinterpret_cast<float4 *>(reinterpret_cast<float *>(lds) + WQ * S * 32 * PAD) + S * 32 * (wave % WQ);
         __syncthreads();
         if (part == 1) {
 #pragma unroll
-            for (int c = 0; c < DB; ++c)
+            for (int s = 0; s < S; ++s) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    *reinterpret_cast<f32x4 *>(box + n * PAD + 32 * c + 8 * r + 4 * g) =
-                        f32x4{o[c][4 * r], o[c][4 * r + 1], o[c][4 * r + 2], o[c][4 * r + 3]};
-            if (g == 0) ml[n] = make_float4(m, l, lr, 0.0f);
+                for (int c = 0; c < DB; ++c)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        *reinterpret_cast<f32x4 *>(box + (32 * s + n) * PAD + 32 * c + 8 * r + 4 * g) =
+                            f32x4{o[s][c][4 * r], o[s][c][4 * r + 1], o[s][c][4 * r + 2], o[s][c][4 * r + 3]};
+                if (g == 0) ml[32 * s + n] = make_float4(m[s], l[s], lr[s], 0.0f);
+            }
         }
         __syncthreads();
         if (part == 1) return;
-        const float4 x = ml[n];
-        const float up = fmaxf(m, x.x);
-        const float f0 = m == kNone ? 0.0f : __builtin_amdgcn_exp2f(m - up), f1 = x.x == kNone ? 0.0f : __builtin_amdgcn_exp2f(x.x - up);
-        m = up;
-        l = l * f0 + x.y * f1;
-        lr = lr * f0 + x.z * f1;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const float4 x = ml[32 * s + n];
+            const float up = fmaxf(m[s], x.x);
+            const float f0 = m[s] == kNone ? 0.0f : __builtin_amdgcn_exp2f(m[s] - up), f1 = x.x == kNone ? 0.0f : __builtin_amdgcn_exp2f(x.x - up);
+            m[s] = up;
+            l[s] = l[s] * f0 + x.y * f1;
+            lr[s] = lr[s] * f0 + x.z * f1;
+#pragma unroll
+            for (int c = 0; c < DB; ++c)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const f32x4 y = *reinterpret_cast<const f32x4 *>(box + (32 * s + n) * PAD + 32 * c + 8 * r + 4 * g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[s][c][4 * r + e] = o[s][c][4 * r + e] * f0 + y[e] * f1;
+                }
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const int row = row_first + 32 * s + n, token = row / a.group, hq = head * a.group + row - token * a.group;
+        if (row >= n_rows) continue;
+        const float inv = 1.0f / lr[s];
+        typedef T T4 __attribute__((ext_vector_type(4)));
+        T *out = static_cast<T *>(a.out) + (int64_t)(t0 + token) * a.o_ts + (int64_t)hq * a.o_hs;
 #pragma unroll
         for (int c = 0; c < DB; ++c)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const f32x4 y = *reinterpret_cast<const f32x4 *>(box + n * PAD + 32 * c + 8 * r + 4 * g);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[c][4 * r + e] = o[c][4 * r + e] * f0 + y[e] * f1;
+                const int d = 32 * c + 8 * r + 4 * g;
+                if (d < D)
+                    *reinterpret_cast<T4 *>(out + d) = __builtin_convertvector(
+                        (f32x4{o[s][c][4 * r], o[s][c][4 * r + 1], o[s][c][4 * r + 2], o[s][c][4 * r + 3]}) * inv, T4);
             }
+        if (LSE && g == 0) a.lse[(int64_t)(t0 + token) * a.q_heads + hq] = (m[s] + __builtin_amdgcn_logf(l[s])) * 0.69314718055994531f;
     }
-    if (row >= n_rows) return;
-    const float inv = 1.0f / lr;
-    typedef T T4 __attribute__((ext_vector_type(4)));
-    T *out = static_cast<T *>(a.out) + (int64_t)(t0 + token) * a.o_ts + (int64_t)hq * a.o_hs;
-#pragma unroll
-    for (int c = 0; c < DB; ++c)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int d = 32 * c + 8 * r + 4 * g;
-            if (d < D)
-                *reinterpret_cast<T4 *>(out + d) =
-                    __builtin_convertvector((f32x4{o[c][4 * r], o[c][4 * r + 1], o[c][4 * r + 2], o[c][4 * r + 3]}) * inv, T4);
-        }
-    if (a.lse && g == 0) a.lse[(int64_t)(t0 + token) * a.q_heads + hq] = (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
 }
 
-template <class T, int DP>
-static int run_prompt(PromptArgs a, int32_t rows, hipStream_t s) {
+template <class T, class P>
+static int run_prompt_shape(PromptArgs a, hipStream_t s) {
+    a.slots = prompt_slot(a.n_tokens * a.group, a.n_seqs, P::ROWS);
     const int64_t wgs = (int64_t)a.slots * a.kv_heads;
     if (wgs > INT32_MAX) return (int)hipErrorInvalidValue;
     for (;; a.first_wg += kMaxWgs) {
         const int64_t left = wgs - a.first_wg;
         const unsigned grid = (unsigned)(left < kMaxWgs ? left : kMaxWgs);
-        if (rows == 64)
-            prompt_kernel<T, DP, 2><<<grid, kAttnThreads, 0, s>>>(a);
+        if (a.lse)
+            prompt_kernel<T, P, true><<<grid, kAttnThreads, 0, s>>>(a);
         else
-            prompt_kernel<T, DP, 4><<<grid, kAttnThreads, 0, s>>>(a);
+            prompt_kernel<T, P, false><<<grid, kAttnThreads, 0, s>>>(a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || left <= kMaxWgs) return (int)e;
     }
+}
+
+template <class T, int DP>
+static int run_prompt(const PromptArgs &a, bool many, hipStream_t s) {
+    if constexpr (DP == 256)  // (the outputs of 32 rows fill the registers, two tiles of 64 positions the LDS)
+        return run_prompt_shape<T, PromptShape<256, 1, 4>>(a, s);
+    else
+        return many ? run_prompt_shape<T, PromptShape<DP, 2, 4>>(a, s) : run_prompt_shape<T, PromptShape<DP, 2, 2>>(a, s);
 }
 
 }  // namespace bpw

@@ -3,10 +3,10 @@
 
 namespace bpw {
 
-int launch_prompt_d64(const PromptArgs &a, int32_t dtype, int32_t rows, void *stream) {
+int launch_prompt_d64(const PromptArgs &a, int32_t dtype, bool many, void *stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (dtype == 1) return run_prompt<__bf16, 64>(a, rows, s);
-    return run_prompt<_Float16, 64>(a, rows, s);
+    if (dtype == 1) return run_prompt<__bf16, 64>(a, many, s);
+    return run_prompt<_Float16, 64>(a, many, s);
 }
 
 }  // namespace bpw
