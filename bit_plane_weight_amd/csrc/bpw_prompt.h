@@ -32,6 +32,18 @@ __device__ __forceinline__ int prompt_seq(const PromptArgs &a, int slot, int row
     }
 }
 
+// c + the two numbers of a word.
+template <class T>
+__device__ __forceinline__ float add2(uint32_t x, float c) {
+    if constexpr (__is_same(T, __bf16)) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, x), bf16x2{(__bf16)1.0f, (__bf16)1.0f}, c, false);
+    } else {
+        typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, x), f16x2{(_Float16)1.0f, (_Float16)1.0f}, c, false);
+    }
+}
+
 // The halves of a word that are finite, zeros for the others; a half's number where it is not finite, zero otherwise.
 template <class T>
 __device__ __forceinline__ uint32_t finite_halves(uint32_t x) {
@@ -218,20 +230,62 @@ __global__ __launch_bounds__(kAttnThreads, 1) void prompt_kernel(PromptArgs a) {
     };
     // Weights in 16 bits: half a step of relative error each; o is divided by the sum of the rounded weights, so that errors
     // they share cancel. lse takes the sum of the unrounded ones.
+    const auto pack_pair = [&](int s, int h, int i) {  // weights 2 i and 2 i + 1 of operand h
+        typedef T T2 __attribute__((ext_vector_type(2)));
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        const f32x2 y = {w[s][h][2 * i], w[s][h][2 * i + 1]};
+        if constexpr (LSE) l[s] += y.x + y.y;
+        const T2 z = __builtin_convertvector(y, T2);
+        p[s][h][i] = __builtin_bit_cast(uint32_t, z);
+        lr[s] = add2<T>(p[s][h][i], lr[s]);
+    };
     const auto pack = [&]() {
 #pragma unroll
-        for (int s = 0; s < S; ++s)
+        for (int e = 0; e < 8 * S; ++e) pack_pair(e / 8, e / 4 % 2, e % 4);
+    };
+    // The main loop's two regions. A wave issues its instructions one after another, and the matrix cores take one of its products
+    // (32 cycles) while the vector units take what stands behind it: so each product is followed by its share of the other
+    // work and of the operand reads, two operands ahead, and kept in that order.
+    constexpr int VF = 2 * DB, PB = S * VF, PA = S * KC, LEAD = 2;  // operands and products; products before sc is there
+    u32v4 kf[KC], vf[VF];
+    const auto first_keys = [&](int blk) { kf[0] = key_frag(blk, 0), kf[1] = key_frag(blk, 1); };
+    const auto first_values = [&](int blk) { vf[0] = value_frag(2 * blk, 0), vf[1] = value_frag(2 * blk + 1 / DB, 1 % DB); };
+    // Products of block vblk's values; weights of sc[which].
+    const auto values_and_weights = [&](int vblk, int which) {
+        float top[S] = {};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if constexpr (LSE) {
-                    float sum = 0.0f;
+        for (int i = 0; i < PB; ++i) {
+            const int j = i / S, s = i % S;
+            if (s == 0 && j + 2 < VF) vf[j + 2] = value_frag(2 * vblk + (j + 2) / DB, (j + 2) % DB);
+            o[s][j % DB] = mma32<T>(vf[j], p[s][j / DB], o[s][j % DB]);
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) sum += w[s][h][r];
-                    l[s] += sum;
-                }
-                p[s][h] = __builtin_bit_cast(u32v4, __builtin_convertvector(w[s][h], typename Vec8<T>::type));
-                lr[s] = sum8<T>(p[s][h], lr[s]);
+            for (int e = max(0, i - LEAD) * 16 * S / (PB - LEAD); e < max(0, i + 1 - LEAD) * 16 * S / (PB - LEAD); ++e) {
+                const int x = e / 16, r = e % 16;
+                const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[which][x][r], a.scale_log2, -m[x]));
+                w[x][r >> 3][r & 7] = y;
+                top[x] = fmaxf(top[x], y);
             }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int x = 0; x < S; ++x) most[x] = top[x];
+    };
+    // Products of block kblk's scores, into sc[which]; the weights in 16 bits.
+    const auto scores_and_rounding = [&](int kblk, int which) {
+        f32x16 z[S];
+#pragma unroll
+        for (int x = 0; x < S; ++x) z[x] = f32x16{};
+#pragma unroll
+        for (int i = 0; i < PA; ++i) {
+            const int c = i / S, x = i % S;
+            if (x == 0 && c + 2 < KC) kf[c + 2] = key_frag(kblk, c + 2);
+            z[x] = mma32<T>(kf[c], q[x][c], z[x]);
+#pragma unroll
+            for (int e = i * 8 * S / PA; e < (i + 1) * 8 * S / PA; ++e) pack_pair(e / 8, e / 4 % 2, e % 4);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int x = 0; x < S; ++x) sc[which][x] = z[x];
     };
 
     issue_k(0);
@@ -254,16 +308,16 @@ __global__ __launch_bounds__(kAttnThreads, 1) void prompt_kernel(PromptArgs a) {
             __syncthreads();  // these tiles are there, and nobody reads those before them any more
             issue_v(t + 1);
             issue_k(t + 2);
-            values(0);
-            weigh(1);
+            first_values(0);
+            first_keys(0);
+            values_and_weights(0, 1);
             raise(1);
-            pack();
-            scores(0, 0);
-            values(1);
-            weigh(0);
+            first_values(1);
+            scores_and_rounding(0, 0);
+            first_keys(1);
+            values_and_weights(1, 0);
             raise(0);
-            pack();
-            scores(1, 1);
+            scores_and_rounding(1, 1);
             ka ^= TILE;
             va ^= TILE;
         }
