@@ -32,15 +32,26 @@ __device__ __forceinline__ int prompt_seq(const PromptArgs &a, int slot, int row
     }
 }
 
-// c + the two numbers of a word.
+// 16 bytes a lane from a buffer (offsets beyond its end give zeros) to LDS at `to` + 16 * lane; `to` and the buffer are the same
+// in all lanes. Waited for by vmcnt; asm, as load_to_lds() is.
+__device__ __forceinline__ void buffer_to_lds(uint32_t to, uint32_t offset, u32v4 buffer) {
+    uint32_t keep;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+                 : "=&s"(keep)
+                 : "s"(to), "v"(offset), "s"(buffer)
+                 : "memory");
+}
+
+// c + the two numbers of a word. (Not by a dot product: v_dot2 holds the matrix cores up, 50 cycles a product with one
+// beside it, 33 without.)
 template <class T>
 __device__ __forceinline__ float add2(uint32_t x, float c) {
     if constexpr (__is_same(T, __bf16)) {
-        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, x), bf16x2{(__bf16)1.0f, (__bf16)1.0f}, c, false);
+        return (c + __builtin_bit_cast(float, x << 16)) + __builtin_bit_cast(float, x & 0xFFFF0000u);
     } else {
         typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, x), f16x2{(_Float16)1.0f, (_Float16)1.0f}, c, false);
+        const f16x2 y = __builtin_bit_cast(f16x2, x);
+        return __builtin_fmaf((float)y.y, 1.0f, __builtin_fmaf((float)y.x, 1.0f, c));
     }
 }
 
@@ -103,45 +114,35 @@ __global__ __launch_bounds__(kAttnThreads, 1) void prompt_kernel(PromptArgs a) {
     const T *kbase = static_cast<const T *>(a.k) + (int64_t)t0 * a.k_ts + (int64_t)head * a.k_hs;
     const T *vbase = static_cast<const T *>(a.v) + (int64_t)t0 * a.v_ts + (int64_t)head * a.v_hs;
 
-    constexpr int LOADS = 16 / RPI, GROUP = LOADS < 4 ? LOADS : 4;  // loads of sixteen rows, of one asm block
+    // Moves of tiles to LDS, 16 bytes a lane. A wave takes sixteen of each 64 positions, RPI a load, by a buffer that ends with
+    // them: positions past the sequence, elements past head_dim (lanes with an offset beyond every buffer) and
+    // tiles past the last become zeros (a zero weight times whatever memory holds there would not be one).
+    constexpr int LOADS = 16 / RPI;  // of sixteen positions
     const uint32_t lds0 = (uint32_t)(size_t)(lds_u8 *)lds;
     uint32_t ks[LOADS], vs[LOADS];
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-        const int r = RPI * i + lane / CPR;
-        ks[i] = 2 * (r * a.k_ts + 8 * ((lane % CPR) ^ key_of_k<DP>(r))) - 1024 * (i % GROUP);
-        vs[i] = 2 * (r * a.v_ts + 8 * ((lane % CPR) ^ key_of_v<DP>(r))) - 1024 * (i % GROUP);
+        const int r = RPI * i + lane / CPR, ck = (lane % CPR) ^ key_of_k<DP>(r), cv = (lane % CPR) ^ key_of_v<DP>(r);
+        ks[i] = 8 * ck < D ? 2 * (r * a.k_ts + 8 * ck) : 0x80000000u;
+        vs[i] = 8 * cv < D ? 2 * (r * a.v_ts + 8 * cv) : 0x80000000u;
     }
-    // Moves this wave's positions of tile `t` of the keys (or values) to LDS, sixteen of each 64, to the buffer of the tile two
-    // before. Positions past the sequence and elements past head_dim become zeros (a zero weight times whatever memory holds
-    // there would not be one).
-    const auto issue = [&](const T *base, int32_t stride, const uint32_t (&offset)[LOADS], bool values, int t) {
-        if (t >= tiles) return;
-#pragma unroll
-        for (int x = 0; x < KT / 64; ++x) {
-            const int first = KT * t + 64 * x + 16 * wave;
-            const T *p = base + (int64_t)first * stride;
-            const uint32_t at = (values ? 2 * TILE : 0) + (t & 1) * TILE + (64 * x + 16 * wave) * ROW;
-            if (first + 16 <= len && D == DP) {
-#pragma unroll
-                for (int i = 0; i < LOADS; i += GROUP)
-                    load_to_lds<GROUP>(lds0 + at + 1024 * i, p, reinterpret_cast<const uint32_t(&)[GROUP]>(offset[i]));
-                continue;
-            }
-#pragma unroll
-            for (int i = 0; i < LOADS; ++i) {
-                const int r = RPI * i + lane / CPR;  // of the sixteen
-                const int chunk = (lane % CPR) ^ (values ? key_of_v<DP>(r) : key_of_k<DP>(r));
-                const uint32_t o[1] = {offset[i] + 1024 * (i % GROUP)};
-                if (first + r < len && 8 * chunk < D)
-                    load_to_lds<1>(lds0 + at + 1024 * i, p, o);
-                else
-                    *reinterpret_cast<u32v4 *>(&lds[at + 1024 * i + 16 * lane]) = u32v4{0, 0, 0, 0};
-            }
-        }
+    constexpr int MOVES = KT / 64 * LOADS;  // loads of a wave's share of a tile
+    const auto move = [&](const T *base, int32_t stride, const uint32_t (&offset)[LOADS], uint32_t to, int t, int i) {
+        const int first = KT * t + 64 * (i / LOADS) + 16 * wave, here = t < tiles ? min(16, len - first) : 0;
+        const uint64_t at = (uint64_t)(base + (int64_t)first * stride);
+        const u32v4 buffer = {(uint32_t)at, (uint32_t)(at >> 32), (uint32_t)max(0, 2 * ((here - 1) * stride + D)), 0x00020000u};
+        buffer_to_lds(lds0 + to + (t & 1) * TILE + (64 * (i / LOADS) + 16 * wave) * ROW + 1024 * (i % LOADS), offset[i % LOADS], buffer);
     };
-    const auto issue_k = [&](int t) { issue(kbase, a.k_ts, ks, false, t); };
-    const auto issue_v = [&](int t) { issue(vbase, a.v_ts, vs, true, t); };
+    const auto move_key = [&](int t, int i) { move(kbase, a.k_ts, ks, 0, t, i); };
+    const auto move_value = [&](int t, int i) { move(vbase, a.v_ts, vs, 2 * TILE, t, i); };
+    const auto move_keys = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < MOVES; ++i) move_key(t, i);
+    };
+    const auto move_values = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < MOVES; ++i) move_value(t, i);
+    };
 
     // LDS addresses of this lane's reads of the current tiles. The chunk of element group c is chosen by an exclusive-or of the
     // first one's address (blocks of 32 and 16 positions are whole keys apart), and so is the other buffer.
@@ -158,11 +159,12 @@ __global__ __launch_bounds__(kAttnThreads, 1) void prompt_kernel(PromptArgs a) {
         return u32v4{y.x, y.y, z.x, z.y};
     };
 
-    // sc: scores of two blocks of 32 positions; w, p: weights of the last one, in float32 and as operands
+    // sc: scores of two blocks of 32 positions; w, p: weights of the last one, in float32 and as operands; bs, bl: their sums
+    // over this lane's positions, rounded and not
     f32x16 o[S][DB], sc[2][S];
     f32x8 w[S][2];
     u32v4 p[S][2];
-    float m[S], l[S], lr[S], most[S];
+    float m[S], l[S], lr[S], bs[S], bl[S];
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         m[s] = kNone;
@@ -190,107 +192,101 @@ __global__ __launch_bounds__(kAttnThreads, 1) void prompt_kernel(PromptArgs a) {
                 for (int s = 0; s < S; ++s) o[s][c] = mma32<T>(f, p[s][h], o[s][c]);
             }
     };
-    const auto weigh_set = [&](int which, int s, float shift) {
-        float top = 0.0f;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[which][s][r], a.scale_log2, -shift));
-            w[s][r >> 3][r & 7] = e;
-            top = fmaxf(top, e);
-        }
-        most[s] = top;
+    const auto weigh_one = [&](int which, int s, int r, float shift) {
+        w[s][r >> 3][r & 7] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[which][s][r], a.scale_log2, -shift));
     };
-    const auto weigh = [&](int which) {
-#pragma unroll
-        for (int s = 0; s < S; ++s) weigh_set(which, s, m[s]);
-    };
-    // The weights are taken against a shift, not the exact maximum: while none passes kShiftLimit nothing is lost, in float32 or
-    // in 16 bits, and no maximum is formed. Otherwise (the first block, a score far above all before it) the shift
-    // becomes the maximum less kLift. (A shift of minus infinity gives infinities or NaN.)
-    const auto raise = [&](int which) {
-        bool high = false;
-#pragma unroll
-        for (int s = 0; s < S; ++s) high = high || !(most[s] < kShiftLimit<T>);
-        if (!__any(high)) return;
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            float top = kNone;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[which][s][r]);
-            top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
-            const float up = fmaxf(m[s], top - kLift<T>);
-            const float f = up == m[s] ? 1.0f : __builtin_amdgcn_exp2f(m[s] - up);
-            m[s] = up;
-            l[s] *= f;
-            lr[s] *= f;
-#pragma unroll
-            for (int c = 0; c < DB; ++c) o[s][c] *= f;
-            weigh_set(which, s, up == kNone ? 0.0f : up);
-        }
-    };
-    // Weights in 16 bits: half a step of relative error each; o is divided by the sum of the rounded weights, so that errors
-    // they share cancel. lse takes the sum of the unrounded ones.
-    const auto pack_pair = [&](int s, int h, int i) {  // weights 2 i and 2 i + 1 of operand h
+    // Weights 2 i and 2 i + 1 of operand h in 16 bits: half a step of relative error each; o is divided by the sum of the rounded
+    // weights, so that errors they share cancel. lse takes the sum of the unrounded ones.
+    const auto round_two = [&](int s, int h, int i) {
         typedef T T2 __attribute__((ext_vector_type(2)));
         typedef float f32x2 __attribute__((ext_vector_type(2)));
         const f32x2 y = {w[s][h][2 * i], w[s][h][2 * i + 1]};
-        if constexpr (LSE) l[s] += y.x + y.y;
-        const T2 z = __builtin_convertvector(y, T2);
-        p[s][h][i] = __builtin_bit_cast(uint32_t, z);
-        lr[s] = add2<T>(p[s][h][i], lr[s]);
+        p[s][h][i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, T2));
+        bs[s] = add2<T>(p[s][h][i], h + i == 0 ? 0.0f : bs[s]);
+        if constexpr (LSE) bl[s] = (h + i == 0 ? y.x : bl[s] + y.x) + y.y;
     };
-    const auto pack = [&]() {
+    const auto weigh = [&](int which, int s, float shift) {
 #pragma unroll
-        for (int e = 0; e < 8 * S; ++e) pack_pair(e / 8, e / 4 % 2, e % 4);
+        for (int r = 0; r < 16; ++r) weigh_one(which, s, r, shift);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) round_two(s, e / 4, e % 4);
     };
+    // The weights are taken against a shift, not the exact maximum: while a lane's sum of a block stays below kShiftLimit nothing
+    // is lost, in float32 or in 16 bits, and no maximum is formed. Otherwise (the first block, a score far above all
+    // before it, NaN) the shift becomes the maximum less kLift, and the block's weights are formed again.
+    const auto settle = [&](int which) {
+        bool high = false;
+#pragma unroll
+        for (int s = 0; s < S; ++s) high = high || !(bs[s] < kShiftLimit<T>);
+        if (__any(high)) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                float top = kNone;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[which][s][r]);
+                top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
+                const float up = fmaxf(m[s], top - kLift<T>);
+                const float f = up == m[s] ? 1.0f : __builtin_amdgcn_exp2f(m[s] - up);
+                m[s] = up;
+                l[s] *= f;
+                lr[s] *= f;
+#pragma unroll
+                for (int c = 0; c < DB; ++c) o[s][c] *= f;
+                weigh(which, s, up == kNone ? 0.0f : up);
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            lr[s] += bs[s];
+            if constexpr (LSE) l[s] += bl[s];
+        }
+    };
+
     // The main loop's two regions. A wave issues its instructions one after another, and the matrix cores take one of its products
     // (32 cycles) while the vector units take what stands behind it: so each product is followed by its share of the other
     // work and of the operand reads, two operands ahead, and kept in that order.
-    constexpr int VF = 2 * DB, PB = S * VF, PA = S * KC, LEAD = 2;  // operands and products; products before sc is there
+    constexpr int VF = 2 * DB, PB = S * VF, PA = S * KC;  // operands and products
     u32v4 kf[KC], vf[VF];
     const auto first_keys = [&](int blk) { kf[0] = key_frag(blk, 0), kf[1] = key_frag(blk, 1); };
     const auto first_values = [&](int blk) { vf[0] = value_frag(2 * blk, 0), vf[1] = value_frag(2 * blk + 1 / DB, 1 % DB); };
-    // Products of block vblk's values; weights of sc[which].
-    const auto values_and_weights = [&](int vblk, int which) {
-        float top[S] = {};
+    // Products of block vblk's values; weights of sc[which], of which `early` come before the first product (above 0: the
+    // operands are still on their way) or begin `-early` products later (the scores are). The loads of the tiles to come.
+    const auto values_and_weights = [&](int vblk, int which, int early, int loads_of) {
+        const int lead = early < 0 ? -early : 0, ahead = early > 0 ? early : 0;
+        const auto weights = [&](int e0, int e1) {
+#pragma unroll
+            for (int e = e0; e < e1; ++e) weigh_one(which, e / 16, e % 16, m[e / 16]);
+        };
+        weights(0, ahead);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < PB; ++i) {
-            const int j = i / S, s = i % S;
+            const int j = i / S, s = i % S, rest = 16 * S - ahead;
             if (s == 0 && j + 2 < VF) vf[j + 2] = value_frag(2 * vblk + (j + 2) / DB, (j + 2) % DB);
             o[s][j % DB] = mma32<T>(vf[j], p[s][j / DB], o[s][j % DB]);
+            weights(ahead + max(0, i - lead) * rest / (PB - lead), ahead + max(0, i + 1 - lead) * rest / (PB - lead));
+            if (loads_of >= 0)
 #pragma unroll
-            for (int e = max(0, i - LEAD) * 16 * S / (PB - LEAD); e < max(0, i + 1 - LEAD) * 16 * S / (PB - LEAD); ++e) {
-                const int x = e / 16, r = e % 16;
-                const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[which][x][r], a.scale_log2, -m[x]));
-                w[x][r >> 3][r & 7] = y;
-                top[x] = fmaxf(top[x], y);
-            }
+                for (int x = i * 2 * MOVES / PB; x < (i + 1) * 2 * MOVES / PB; ++x) x % 2 ? move_key(loads_of + 2, x / 2) : move_value(loads_of + 1, x / 2);
             __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int x = 0; x < S; ++x) most[x] = top[x];
     };
     // Products of block kblk's scores, into sc[which]; the weights in 16 bits.
     const auto scores_and_rounding = [&](int kblk, int which) {
-        f32x16 z[S];
-#pragma unroll
-        for (int x = 0; x < S; ++x) z[x] = f32x16{};
 #pragma unroll
         for (int i = 0; i < PA; ++i) {
-            const int c = i / S, x = i % S;
+            const int x = i / KC, c = i % KC;
             if (x == 0 && c + 2 < KC) kf[c + 2] = key_frag(kblk, c + 2);
-            z[x] = mma32<T>(kf[c], q[x][c], z[x]);
+            sc[which][x] = mma32<T>(kf[c], q[x][c], c ? sc[which][x] : f32x16{});
 #pragma unroll
-            for (int e = i * 8 * S / PA; e < (i + 1) * 8 * S / PA; ++e) pack_pair(e / 8, e / 4 % 2, e % 4);
+            for (int e = i * 8 * S / PA; e < (i + 1) * 8 * S / PA; ++e) round_two(e / 8, e / 4 % 2, e % 4);
             __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int x = 0; x < S; ++x) sc[which][x] = z[x];
     };
 
-    issue_k(0);
-    issue_v(0);
-    issue_k(1);
+    move_keys(0);
+    move_values(0);
+    move_keys(1);
     int t = 0;
     // Tiles that every row sees whole, a block of 32 positions after another: the products of the last block's values beside
     // this block's exponentials, those of the next block's scores beside the rounding of its weights. Keys run a tile ahead.
@@ -298,37 +294,35 @@ __global__ __launch_bounds__(kAttnThreads, 1) void prompt_kernel(PromptArgs a) {
         wait_loads_to_lds();
         __syncthreads();
         scores(0, 0);
-        weigh(0);
-        raise(0);
-        pack();
+#pragma unroll
+        for (int s = 0; s < S; ++s) weigh(0, s, m[s]);
+        settle(0);
         scores(1, 1);
         ka ^= TILE;
         for (; t + 1 < full; ++t) {
             wait_loads_to_lds();
             __syncthreads();  // these tiles are there, and nobody reads those before them any more
-            issue_v(t + 1);
-            issue_k(t + 2);
             first_values(0);
             first_keys(0);
-            values_and_weights(0, 1);
-            raise(1);
+            values_and_weights(0, 1, 8, t);
             first_values(1);
             scores_and_rounding(0, 0);
+            settle(1);
             first_keys(1);
-            values_and_weights(1, 0);
-            raise(0);
+            values_and_weights(1, 0, -2, -1);
             scores_and_rounding(1, 1);
+            settle(0);
             ka ^= TILE;
             va ^= TILE;
         }
         wait_loads_to_lds();
         __syncthreads();
-        issue_v(t + 1);
-        issue_k(t + 2);
+        move_values(t + 1);
+        move_keys(t + 2);
         values(0);
-        weigh(1);
-        raise(1);
-        pack();
+#pragma unroll
+        for (int s = 0; s < S; ++s) weigh(1, s, m[s]);
+        settle(1);
         values(1);
         va ^= TILE;
         ++t;
@@ -336,7 +330,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void prompt_kernel(PromptArgs a) {
     for (; t < tiles; ++t) {  // tiles on the diagonal, each step by itself
         wait_loads_to_lds();
         __syncthreads();
-        issue_v(t + 1);
+        move_values(t + 1);
 #pragma unroll 1
         for (int blk = 0; blk < 2; ++blk) {
             const int here = KT * t + 64 * part + 32 * blk;
@@ -356,12 +350,9 @@ __global__ __launch_bounds__(kAttnThreads, 1) void prompt_kernel(PromptArgs a) {
                 for (int r = 0; r < 16; ++r)
                     if (here + 8 * (r >> 2) + 4 * g + (r & 3) >= vis) sc[0][s][r] = kNone;
             }
-            weigh(0);
 #pragma unroll
-            for (int s = 0; s < S; ++s)
-                if (m[s] == kNone) most[s] = __builtin_inff();  // (rows that have seen nothing: their weights are NaN here)
-            raise(0);
-            pack();
+            for (int s = 0; s < S; ++s) weigh(0, s, m[s]);
+            settle(0);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int x = 2 * blk + h;
@@ -410,7 +401,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void prompt_kernel(PromptArgs a) {
             }
         }
         __syncthreads();  // nobody reads these keys any more
-        issue_k(t + 2);
+        move_keys(t + 2);
         ka ^= TILE;
         va ^= TILE;
     }

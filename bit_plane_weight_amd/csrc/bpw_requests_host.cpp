@@ -73,6 +73,8 @@ bpw_status bpw_prompt_attn(const bpw_prompt_attn_args *a, void *stream) {
     for (const bpw_heads *x : all)
         if (!wide(x->d, x->dtype, x->token_stride, x->head_stride, 0))
             return fail(BPW_E_INVAL, "%s: q, k, v and out need 16-byte alignment and strides of multiples of 8 elements", who);
+    if (a->n_tokens > 1 && (a->k.token_stride < a->head_dim || a->v.token_stride < a->head_dim))
+        return fail(BPW_E_INVAL, "%s: a token's stride of k or v is below head_dim %d: rows would overlap", who, (int)a->head_dim);
     if (a->k.token_stride > kMaxRowStride || a->v.token_stride > kMaxRowStride)
         return fail(BPW_E_UNSUPPORTED, "%s: a token's stride of k or v is above 2^24", who);
     const float scale_log2 = a->scale * 1.44269504088896341f;
@@ -86,8 +88,8 @@ bpw_status bpw_prompt_attn(const bpw_prompt_attn_args *a, void *stream) {
     bpw::PromptArgs p{};
     p.q = a->q.d, p.k = a->k.d, p.v = a->v.d, p.out = a->out.d, p.lse = a->d_lse;
     p.q_ts = a->q.token_stride, p.q_hs = a->q.head_stride;
-    p.k_ts = (int32_t)a->k.token_stride, p.k_hs = a->k.head_stride;
-    p.v_ts = (int32_t)a->v.token_stride, p.v_hs = a->v.head_stride;
+    p.k_ts = a->n_tokens > 1 ? (int32_t)a->k.token_stride : a->head_dim, p.k_hs = a->k.head_stride;
+    p.v_ts = a->n_tokens > 1 ? (int32_t)a->v.token_stride : a->head_dim, p.v_hs = a->v.head_stride;
     p.o_ts = a->out.token_stride, p.o_hs = a->out.head_stride;
     p.starts = a->d_starts;
     p.n_tokens = a->n_tokens, p.n_seqs = a->n_seqs;

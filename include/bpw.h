@@ -652,7 +652,7 @@ bpw_status bpw_verify_draft(const bpw_verify_draft_args *a, void *d_ws, size_t w
  * start, behind the last) are not written, and an empty sequence is none. The sums have a fixed order: the same arguments
  * give the same bits. One launch, no workspace.
  * q, k, v and out share a type (BPW_BF16 or BPW_F16) and head_dim, a multiple of 8, 8 .. 256; pointers are 16-byte aligned
- * and strides multiples of 8 elements, a token's of k and v at most 2^24. q.heads is a multiple of k.heads; k.heads equals
+ * and strides multiples of 8 elements, a token's of k and v at least head_dim (where there are several) and at most 2^24. q.heads is a multiple of k.heads; k.heads equals
  * v.heads. out may not overlap the inputs. n_tokens * q.heads / k.heads is at most 2^30, n_seqs 1 .. 2^20. */
 typedef struct bpw_prompt_attn_args {
     int32_t n_tokens, n_seqs, head_dim;
