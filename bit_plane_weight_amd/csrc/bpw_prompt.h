@@ -13,14 +13,18 @@
 // XCD's L2 holds one.
 #pragma once
 
+#include <utility>
+
 #include "bpw_attention.h"
 
 namespace bpw {
 
+#define BPW_INLINE __attribute__((always_inline))
+
 // The sequence whose tiles hold slot `slot`: the last whose first slot is not beyond it, or -1. Every wave by itself, 64
 // probes at a time. Starts that do not rise give some sequence.
-__device__ __forceinline__ int prompt_seq(const PromptArgs &a, int slot, int rows) {
-    const auto first = [&](int b) { return prompt_slot(min(max(a.starts[b], 0), a.n_tokens) * a.group, b, rows); };
+__device__ __forceinline__ int prompt_seq(const PromptArgs &a, int slot) {
+    const auto first = [&](int b) { return prompt_slot(min(max(a.starts[b], 0), a.n_tokens) * a.group, b); };
     int lo = 0, hi = a.n_seqs;
     while (true) {
         const int step = (hi - lo + 63) / 64, at = lo + (int)(threadIdx.x & 63) * step;
@@ -32,14 +36,14 @@ __device__ __forceinline__ int prompt_seq(const PromptArgs &a, int slot, int row
     }
 }
 
-// 16 bytes a lane from a buffer (offsets beyond its end give zeros) to LDS at `to` + 16 * lane; `to` and the buffer are the same
-// in all lanes. Waited for by vmcnt; asm, as load_to_lds() is.
-__device__ __forceinline__ void buffer_to_lds(uint32_t to, uint32_t offset, u32v4 buffer) {
-    uint32_t keep;
-    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
-                 : "=&s"(keep)
-                 : "s"(to), "v"(offset), "s"(buffer)
-                 : "memory");
+// 16 bytes a lane from a buffer (offsets beyond its end give zeros) to LDS at m0 + AT + 16 * lane, from `offset` + AT; m0 and the
+// buffer are the same in all lanes. Waited for by vmcnt; asm, as load_to_lds() is. m0 is set apart from the loads, because
+// each write of it waits for the loads to LDS before it (160 cycles a load); nothing else here uses it.
+__device__ __forceinline__ void lds_base(uint32_t at) { asm volatile("s_mov_b32 m0, %0\n\ts_nop 0" ::"s"(at) : "m0", "memory"); }
+template <int AT>
+__device__ __forceinline__ void buffer_to_lds(uint32_t offset, u32v4 buffer) {
+    static_assert(AT < 4096, "an instruction's offset has 12 bits");
+    asm volatile("buffer_load_dwordx4 %0, %1, 0 offen offset:%2 lds" ::"v"(offset), "s"(buffer), "n"(AT) : "memory");
 }
 
 // c + the two numbers of a word. (Not by a dot product: v_dot2 holds the matrix cores up, 50 cycles a product with one
@@ -67,81 +71,80 @@ __device__ __forceinline__ float odd_value(uint32_t half) {
     return (half & ones) == ones ? (float)__builtin_bit_cast(T, (uint16_t)half) : 0.0f;
 }
 
+// f(0), f(1), .. f(N - 1) with constants.
+template <int... I, class F>
+__device__ __forceinline__ void static_for_each(std::integer_sequence<int, I...>, F f) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F f) {
+    static_for_each(std::make_integer_sequence<int, N>{}, f);
+}
+
 typedef __attribute__((address_space(3))) const u32v4 lds_u32v4;
 typedef __attribute__((address_space(3))) const u32x2 lds_u32x2;
 
-// Shape of a kernel: a wave holds S sets of 32 query rows, WQ waves lie along the rows of a tile and the others along the
-// positions, of which a workgroup takes KT at a time and a wave two blocks of 32.
-template <int DP_, int S_, int WQ_>
-struct PromptShape {
-    static constexpr int DP = DP_, S = S_, WQ = WQ_;
-    static constexpr int PARTS = kAttnWaves / WQ, KT = 64 * PARTS, ROWS = 32 * S * WQ;
-};
-
-template <class T, class P, bool LSE>
-__global__ __launch_bounds__(kAttnThreads, 1) void prompt_kernel(PromptArgs a) {
-    constexpr int DP = P::DP, S = P::S, WQ = P::WQ, PARTS = P::PARTS, KT = P::KT, M = P::ROWS;
+// A workgroup of PARTS times four waves takes 128 query rows, 32 a wave, and 64 positions a part at a time: the waves of
+// part 1 the second 64 of each 128, joined with part 0's at the end.
+template <class T, int DP, int PARTS, bool LSE>
+__global__ __launch_bounds__(256 * PARTS, DP <= 128 ? 2 : 1) void prompt_kernel(PromptArgs a) {
+    constexpr int KT = 64 * PARTS, M = kPromptRows;
     constexpr int ROW = DP * 2, CPR = DP / 8, RPI = 64 / CPR;  // row bytes, chunks of a row, rows of one load
     constexpr int KC = DP / 16, DB = DP / 32, TILE = KT * ROW;  // bytes of a tile of keys or values
     __shared__ __attribute__((aligned(4096))) uint8_t lds[4 * TILE];  // keys twice, values twice
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n = lane & 31, g = lane >> 5, part = wave / WQ;
+    const int n = lane & 31, g = lane >> 5, part = wave >> 2;
     const int D = a.head_dim;
 
     const int id = a.first_wg + (int)blockIdx.x, head = id % a.kv_heads, slot = a.slots - 1 - id / a.kv_heads;
-    const int b = prompt_seq(a, slot, M);
+    const int b = prompt_seq(a, slot);
     if (b < 0) return;
     const int t0 = min(max(a.starts[b], 0), a.n_tokens), t1 = min(max(a.starts[b + 1], t0), a.n_tokens);
-    const int len = t1 - t0, n_rows = len * a.group, row0 = (slot - prompt_slot(t0 * a.group, b, M)) * M;
+    const int len = t1 - t0, n_rows = len * a.group, row0 = (slot - prompt_slot(t0 * a.group, b)) * M;
     if (row0 < 0 || row0 >= n_rows) return;
     const int end = (min(row0 + M, n_rows) - 1) / a.group + 1;  // positions that the tile's last row sees
-    // tiles of positions, and those of them that every row sees whole
-    const int tiles = (end + KT - 1) / KT, full = (row0 / a.group + 1) / KT;
+    const int tiles = (end + KT - 1) / KT;
 
-    const int row_first = row0 + 32 * S * (wave % WQ);
-    const int some_see = row_first < n_rows ? (min(row_first + 32 * S, n_rows) - 1) / a.group + 1 : 0;
-    u32v4 q[S][KC];
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const int row = row_first + 32 * s + n, token = row / a.group, hq = head * a.group + row - token * a.group;
+    const int row_first = row0 + 32 * (wave & 3), row = row_first + n;
+    const int token = row / a.group, hq = head * a.group + row - token * a.group;
+    const int vis = row < n_rows ? token + 1 : len;
+    const int all_see = __builtin_amdgcn_readfirstlane(row_first / a.group + 1);  // what every row of the wave sees
+    u32v4 q[KC];
+    {
         const T *p = static_cast<const T *>(a.q) + (int64_t)(t0 + token) * a.q_ts + (int64_t)hq * a.q_hs;
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
-            q[s][c] = u32v4{0, 0, 0, 0};
-            if (row < n_rows && 16 * c + 8 * g < D) q[s][c] = *reinterpret_cast<const u32v4 *>(p + 16 * c + 8 * g);
+            q[c] = u32v4{0, 0, 0, 0};
+            if (row < n_rows && 16 * c + 8 * g < D) q[c] = *reinterpret_cast<const u32v4 *>(p + 16 * c + 8 * g);
         }
     }
     const T *kbase = static_cast<const T *>(a.k) + (int64_t)t0 * a.k_ts + (int64_t)head * a.k_hs;
     const T *vbase = static_cast<const T *>(a.v) + (int64_t)t0 * a.v_ts + (int64_t)head * a.v_hs;
 
-    // Moves of tiles to LDS, 16 bytes a lane. A wave takes sixteen of each 64 positions, RPI a load, by a buffer that ends with
+    // Moves of tiles to LDS, 16 bytes a lane. A wave takes sixteen positions of a tile, RPI a load, by a buffer that ends with
     // them: positions past the sequence, elements past head_dim (lanes with an offset beyond every buffer) and
     // tiles past the last become zeros (a zero weight times whatever memory holds there would not be one).
-    constexpr int LOADS = 16 / RPI;  // of sixteen positions
+    constexpr int LOADS = 16 / RPI, GROUP = LOADS < 4 ? LOADS : 4;  // loads; after one setting of m0
+    constexpr int BACK = 1024 * (GROUP - 1);  // (a load's AT moves both addresses, so that buffers begin this much earlier)
     const uint32_t lds0 = (uint32_t)(size_t)(lds_u8 *)lds;
     uint32_t ks[LOADS], vs[LOADS];
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
         const int r = RPI * i + lane / CPR, ck = (lane % CPR) ^ key_of_k<DP>(r), cv = (lane % CPR) ^ key_of_v<DP>(r);
-        ks[i] = 8 * ck < D ? 2 * (r * a.k_ts + 8 * ck) : 0x80000000u;
-        vs[i] = 8 * cv < D ? 2 * (r * a.v_ts + 8 * cv) : 0x80000000u;
+        ks[i] = 8 * ck < D ? 2 * (r * a.k_ts + 8 * ck) + BACK - 1024 * (i % GROUP) : 0x80000000u;
+        vs[i] = 8 * cv < D ? 2 * (r * a.v_ts + 8 * cv) + BACK - 1024 * (i % GROUP) : 0x80000000u;
     }
-    constexpr int MOVES = KT / 64 * LOADS;  // loads of a wave's share of a tile
-    const auto move = [&](const T *base, int32_t stride, const uint32_t (&offset)[LOADS], uint32_t to, int t, int i) {
-        const int first = KT * t + 64 * (i / LOADS) + 16 * wave, here = t < tiles ? min(16, len - first) : 0;
-        const uint64_t at = (uint64_t)(base + (int64_t)first * stride);
-        const u32v4 buffer = {(uint32_t)at, (uint32_t)(at >> 32), (uint32_t)max(0, 2 * ((here - 1) * stride + D)), 0x00020000u};
-        buffer_to_lds(lds0 + to + (t & 1) * TILE + (64 * (i / LOADS) + 16 * wave) * ROW + 1024 * (i % LOADS), offset[i % LOADS], buffer);
-    };
-    const auto move_key = [&](int t, int i) { move(kbase, a.k_ts, ks, 0, t, i); };
-    const auto move_value = [&](int t, int i) { move(vbase, a.v_ts, vs, 2 * TILE, t, i); };
-    const auto move_keys = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < MOVES; ++i) move_key(t, i);
-    };
-    const auto move_values = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < MOVES; ++i) move_value(t, i);
+    const auto move_tile = [&](bool values, int t) BPW_INLINE {
+        const T *base = values ? vbase : kbase;
+        const int32_t stride = values ? a.v_ts : a.k_ts;
+        const int first = KT * t + 16 * wave, here = min(16, len - first);
+        const uint32_t there = (uint32_t)((-here & (t - tiles)) >> 31);  // all ones, or 0: nothing (without a branch)
+        const uint64_t at = (uint64_t)(base + (int64_t)first * stride) - BACK;
+        const u32v4 buffer = {(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (uint32_t)(2 * ((here - 1) * stride + D) + BACK) & there, 0x00020000u};
+        static_for<LOADS>([&](auto i) {
+            if constexpr (i % GROUP == 0) lds_base(lds0 + (values ? 2 * TILE : 0) + (t & 1) * TILE + 16 * wave * ROW + 1024 * i);
+            buffer_to_lds<1024 * (i % GROUP)>(values ? vs[i] : ks[i], buffer);
+        });
     };
 
     // LDS addresses of this lane's reads of the current tiles. The chunk of element group c is chosen by an exclusive-or of the
@@ -152,8 +155,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void prompt_kernel(PromptArgs a) {
         const int i = lane & 15, r = 4 * g + (i >> 2), chunk = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
         va = lds0 + 2 * TILE + (64 * part + r) * ROW + ((chunk ^ key_of_v<DP>(r)) * 16) + (i & 1) * 8;
     }
-    const auto key_frag = [&](int blk, int c) { return *(lds_u32v4 *)((ka ^ (32 * c)) + blk * 32 * ROW); };
-    const auto value_frag = [&](int x, int c) {  // positions 16 x .. 16 x + 15 of this wave's
+    const auto key_frag = [&](int blk, int c) BPW_INLINE { return *(lds_u32v4 *)((ka ^ (32 * c)) + blk * 32 * ROW); };
+    const auto value_frag = [&](int x, int c) BPW_INLINE {  // positions 16 x .. 16 x + 15 of this wave's
         const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)((va ^ (64 * c)) + 16 * x * ROW)));
         const u32x2 z = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)((va ^ (64 * c) ^ V8) + (16 * x + 8) * ROW)));
         return u32v4{y.x, y.y, z.x, z.y};
@@ -161,327 +164,282 @@ __global__ __launch_bounds__(kAttnThreads, 1) void prompt_kernel(PromptArgs a) {
 
     // sc: scores of two blocks of 32 positions; w, p: weights of the last one, in float32 and as operands; bs, bl: their sums
     // over this lane's positions, rounded and not
-    f32x16 o[S][DB], sc[2][S];
-    f32x8 w[S][2];
-    u32v4 p[S][2];
-    float m[S], l[S], lr[S], bs[S], bl[S];
+    f32x16 o[DB], sc[2];
+    f32x8 w[2];
+    u32v4 p[2];
+    float m = kNone, l = 0.0f, lr = 0.0f, bs, bl;
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-        m[s] = kNone;
-        l[s] = lr[s] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < DB; ++c) o[s][c] = f32x16{};
-    }
-    const auto scores = [&](int which, int blk) {
-#pragma unroll
-        for (int s = 0; s < S; ++s) sc[which][s] = f32x16{};
-#pragma unroll
-        for (int c = 0; c < KC; ++c) {
-            const u32v4 f = key_frag(blk, c);
-#pragma unroll
-            for (int s = 0; s < S; ++s) sc[which][s] = mma32<T>(f, q[s][c], sc[which][s]);
-        }
-    };
-    const auto values = [&](int blk) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int c = 0; c < DB; ++c) {
-                const u32v4 f = value_frag(2 * blk + h, c);
-#pragma unroll
-                for (int s = 0; s < S; ++s) o[s][c] = mma32<T>(f, p[s][h], o[s][c]);
-            }
-    };
-    const auto weigh_one = [&](int which, int s, int r, float shift) {
-        w[s][r >> 3][r & 7] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[which][s][r], a.scale_log2, -shift));
+    for (int c = 0; c < DB; ++c) o[c] = f32x16{};
+    const auto weigh_one = [&](int which, int r, float shift) BPW_INLINE {
+        w[r >> 3][r & 7] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[which][r], a.scale_log2, -shift));
     };
     // Weights 2 i and 2 i + 1 of operand h in 16 bits: half a step of relative error each; o is divided by the sum of the rounded
     // weights, so that errors they share cancel. lse takes the sum of the unrounded ones.
-    const auto round_two = [&](int s, int h, int i) {
+    const auto round_two = [&](int h, int i) BPW_INLINE {
         typedef T T2 __attribute__((ext_vector_type(2)));
         typedef float f32x2 __attribute__((ext_vector_type(2)));
-        const f32x2 y = {w[s][h][2 * i], w[s][h][2 * i + 1]};
-        p[s][h][i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, T2));
-        bs[s] = add2<T>(p[s][h][i], h + i == 0 ? 0.0f : bs[s]);
-        if constexpr (LSE) bl[s] = (h + i == 0 ? y.x : bl[s] + y.x) + y.y;
+        const f32x2 y = {w[h][2 * i], w[h][2 * i + 1]};
+        p[h][i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, T2));
+        bs = add2<T>(p[h][i], h + i == 0 ? 0.0f : bs);
+        if constexpr (LSE) bl = (h + i == 0 ? y.x : bl + y.x) + y.y;
     };
-    const auto weigh = [&](int which, int s, float shift) {
+    const auto weigh = [&](int which, float shift) BPW_INLINE {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) weigh_one(which, s, r, shift);
+        for (int r = 0; r < 16; ++r) weigh_one(which, r, shift);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) round_two(s, e / 4, e % 4);
+        for (int e = 0; e < 8; ++e) round_two(e / 4, e % 4);
     };
     // The weights are taken against a shift, not the exact maximum: while a lane's sum of a block stays below kShiftLimit nothing
     // is lost, in float32 or in 16 bits, and no maximum is formed. Otherwise (the first block, a score far above all
     // before it, NaN) the shift becomes the maximum less kLift, and the block's weights are formed again.
-    const auto settle = [&](int which) {
-        bool high = false;
+    const auto settle = [&](int which) BPW_INLINE {
+        if (__any(!(bs < kShiftLimit<T>))) {
+            float top = kNone;
 #pragma unroll
-        for (int s = 0; s < S; ++s) high = high || !(bs[s] < kShiftLimit<T>);
-        if (__any(high)) {
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[which][r]);
+            top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
+            const float up = fmaxf(m, top - kLift<T>);
+            const float f = up == m ? 1.0f : __builtin_amdgcn_exp2f(m - up);
+            m = up;
+            l *= f;
+            lr *= f;
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                float top = kNone;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[which][s][r]);
-                top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
-                const float up = fmaxf(m[s], top - kLift<T>);
-                const float f = up == m[s] ? 1.0f : __builtin_amdgcn_exp2f(m[s] - up);
-                m[s] = up;
-                l[s] *= f;
-                lr[s] *= f;
-#pragma unroll
-                for (int c = 0; c < DB; ++c) o[s][c] *= f;
-                weigh(which, s, up == kNone ? 0.0f : up);
-            }
+            for (int c = 0; c < DB; ++c) o[c] *= f;
+            weigh(which, up == kNone ? 0.0f : up);
         }
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            lr[s] += bs[s];
-            if constexpr (LSE) l[s] += bl[s];
-        }
+        lr += bs;
+        if constexpr (LSE) l += bl;
     };
-
+    // Positions that a row does not see, in the scores of block blk of tile t.
+    const auto hide = [&](int which, int t, int blk) BPW_INLINE {
+        const int first = KT * t + 64 * part + 32 * blk;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            if (first + 8 * (r >> 2) + 4 * g + (r & 3) >= vis) sc[which][r] = kNone;
+    };
     // The main loop's two regions. A wave issues its instructions one after another, and the matrix cores take one of its products
     // (32 cycles) while the vector units take what stands behind it: so each product is followed by its share of the other
     // work and of the operand reads, two operands ahead, and kept in that order.
-    constexpr int VF = 2 * DB, PB = S * VF, PA = S * KC;  // operands and products
+    constexpr int VF = 2 * DB;
     u32v4 kf[KC], vf[VF];
-    const auto first_keys = [&](int blk) { kf[0] = key_frag(blk, 0), kf[1] = key_frag(blk, 1); };
-    const auto first_values = [&](int blk) { vf[0] = value_frag(2 * blk, 0), vf[1] = value_frag(2 * blk + 1 / DB, 1 % DB); };
-    // Products of block vblk's values; weights of sc[which], of which `early` come before the first product (above 0: the
-    // operands are still on their way) or begin `-early` products later (the scores are). The loads of the tiles to come.
-    const auto values_and_weights = [&](int vblk, int which, int early, int loads_of) {
-        const int lead = early < 0 ? -early : 0, ahead = early > 0 ? early : 0;
-        const auto weights = [&](int e0, int e1) {
+    const auto first_keys = [&](int blk) BPW_INLINE { kf[0] = key_frag(blk, 0), kf[1] = key_frag(blk, 1); };
+    const auto first_values = [&](int blk) BPW_INLINE { vf[0] = value_frag(2 * blk, 0), vf[1] = value_frag(2 * blk + 1 / DB, 1 % DB); };
+    // Products of the values of block blk; weights of sc[which], of which the first `ahead` come before the products
+    // (whose operands are still on their way).
+    const auto values_and_weights = [&](int blk, int which, int ahead) BPW_INLINE {
 #pragma unroll
-            for (int e = e0; e < e1; ++e) weigh_one(which, e / 16, e % 16, m[e / 16]);
-        };
-        weights(0, ahead);
+        for (int e = 0; e < ahead; ++e) weigh_one(which, e, m);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < PB; ++i) {
-            const int j = i / S, s = i % S, rest = 16 * S - ahead;
-            if (s == 0 && j + 2 < VF) vf[j + 2] = value_frag(2 * vblk + (j + 2) / DB, (j + 2) % DB);
-            o[s][j % DB] = mma32<T>(vf[j], p[s][j / DB], o[s][j % DB]);
-            weights(ahead + max(0, i - lead) * rest / (PB - lead), ahead + max(0, i + 1 - lead) * rest / (PB - lead));
-            if (loads_of >= 0)
+        for (int i = 0; i < VF; ++i) {
+            if (i + 2 < VF) vf[i + 2] = value_frag(2 * blk + (i + 2) / DB, (i + 2) % DB);
+            o[i % DB] = mma32<T>(vf[i], p[i / DB], o[i % DB]);
 #pragma unroll
-                for (int x = i * 2 * MOVES / PB; x < (i + 1) * 2 * MOVES / PB; ++x) x % 2 ? move_key(loads_of + 2, x / 2) : move_value(loads_of + 1, x / 2);
+            for (int e = ahead + i * (16 - ahead) / VF; e < ahead + (i + 1) * (16 - ahead) / VF; ++e) weigh_one(which, e, m);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    // Products of block kblk's scores, into sc[which]; the weights in 16 bits.
-    const auto scores_and_rounding = [&](int kblk, int which) {
+    // Products of block blk's scores, into sc[which]; the weights in 16 bits.
+    const auto scores_and_rounding = [&](int blk, int which) BPW_INLINE {
 #pragma unroll
-        for (int i = 0; i < PA; ++i) {
-            const int x = i / KC, c = i % KC;
-            if (x == 0 && c + 2 < KC) kf[c + 2] = key_frag(kblk, c + 2);
-            sc[which][x] = mma32<T>(kf[c], q[x][c], c ? sc[which][x] : f32x16{});
+        for (int i = 0; i < KC; ++i) {
+            if (i + 2 < KC) kf[i + 2] = key_frag(blk, i + 2);
+            sc[which] = mma32<T>(kf[i], q[i], i ? sc[which] : f32x16{});
 #pragma unroll
-            for (int e = i * 8 * S / PA; e < (i + 1) * 8 * S / PA; ++e) round_two(e / 8, e / 4 % 2, e % 4);
+            for (int e = i * 8 / KC; e < (i + 1) * 8 / KC; ++e) round_two(e / 4, e % 4);
             __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    const auto scores = [&](int blk, int which) BPW_INLINE {
+#pragma unroll
+        for (int i = 0; i < KC; ++i) sc[which] = mma32<T>(key_frag(blk, i), q[i], i ? sc[which] : f32x16{});
     };
 
-    move_keys(0);
-    move_values(0);
-    move_keys(1);
+    const auto values = [&](int blk) BPW_INLINE {
+#pragma unroll
+        for (int i = 0; i < VF; ++i) o[i % DB] = mma32<T>(value_frag(2 * blk + i / DB, i % DB), p[i / DB], o[i % DB]);
+    };
+
+    // A block of 32 positions after another: the products of the last block's values beside this block's exponentials, those of
+    // the next block's scores beside the rounding of its weights. Keys run a tile ahead of values.
+    uint32_t odd = 0;  // a value that only some rows of the wave see is not finite: a weight of zero does not hide it
+    move_tile(false, 0);
+    move_tile(true, 0);
+    move_tile(false, 1);
+    wait_loads_to_lds();
+    __syncthreads();
+    scores(0, 0);
+    hide(0, 0, 0);
+    weigh(0, m);
+    settle(0);
+    scores(1, 1);
+    hide(1, 0, 1);
+    ka ^= TILE;
     int t = 0;
-    // Tiles that every row sees whole, a block of 32 positions after another: the products of the last block's values beside
-    // this block's exponentials, those of the next block's scores beside the rounding of its weights. Keys run a tile ahead.
-    if (full > 0) {
+    const auto arrive = [&] BPW_INLINE {
         wait_loads_to_lds();
-        __syncthreads();
-        scores(0, 0);
-#pragma unroll
-        for (int s = 0; s < S; ++s) weigh(0, s, m[s]);
-        settle(0);
-        scores(1, 1);
-        ka ^= TILE;
-        for (; t + 1 < full; ++t) {
-            wait_loads_to_lds();
-            __syncthreads();  // these tiles are there, and nobody reads those before them any more
-            first_values(0);
-            first_keys(0);
-            values_and_weights(0, 1, 8, t);
-            first_values(1);
-            scores_and_rounding(0, 0);
-            settle(1);
-            first_keys(1);
-            values_and_weights(1, 0, -2, -1);
-            scores_and_rounding(1, 1);
-            settle(0);
-            ka ^= TILE;
-            va ^= TILE;
-        }
-        wait_loads_to_lds();
-        __syncthreads();
-        move_values(t + 1);
-        move_keys(t + 2);
-        values(0);
-#pragma unroll
-        for (int s = 0; s < S; ++s) weigh(1, s, m[s]);
-        settle(1);
-        values(1);
-        va ^= TILE;
-        ++t;
-    }
-    for (; t < tiles; ++t) {  // tiles on the diagonal, each step by itself
-        wait_loads_to_lds();
-        __syncthreads();
-        move_values(t + 1);
+        __syncthreads();  // values t and keys t + 1 are there, and nobody reads those before them any more
+    };
+    const auto look_for_odd = [&] BPW_INLINE {
 #pragma unroll 1
-        for (int blk = 0; blk < 2; ++blk) {
-            const int here = KT * t + 64 * part + 32 * blk;
-            if (here >= some_see) break;
+        for (int j = 0; j < 4 * DB; j += 2) {
+            const u32v4 f = value_frag(j / DB, j % DB), h = value_frag(j / DB, j % DB + 1);
 #pragma unroll
-            for (int s = 0; s < S; ++s) sc[0][s] = f32x16{};
+            for (int e = 0; e < 4; ++e) odd |= maybe_not_finite<T>(f[e]) | maybe_not_finite<T>(h[e]);
+        }
+    };
+    const auto tile = [&](auto masked) BPW_INLINE {
+        first_values(0);
+        first_keys(0);
+        move_tile(true, t + 1);
+        move_tile(false, t + 2);
+        values_and_weights(0, 1, 4);
+        first_values(1);
+        scores_and_rounding(0, 0);
+        settle(1);
+        if constexpr (masked) hide(0, t + 1, 0);
+        first_keys(1);
+        values_and_weights(1, 0, 0);
+        scores_and_rounding(1, 1);
+        settle(0);
+        if constexpr (masked) hide(1, t + 1, 1);
+        ka ^= TILE;
+        va ^= TILE;
+    };
+    for (; KT * (t + 1) + 64 * part + 64 <= all_see && t + 1 < tiles; ++t) {
+        arrive();
+        tile(std::false_type{});
+    }
+    for (;; ++t) {
+        arrive();
+        if (KT * t + 64 * part + 64 > all_see) look_for_odd();
+        if (t + 1 == tiles) break;
+        tile(std::true_type{});
+    }
+    values(0);
+    weigh(1, m);
+    settle(1);
+    values(1);
+
+    // Values that are not finite and not seen by all: the tile of rows once more, step by step, with zeros in the place of such
+    // values, which are then added to the rows that see them (times any weight above zero they stay what they are).
+    if (__syncthreads_or((int)odd)) {
+        m = kNone;
+        l = lr = 0.0f;
 #pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                const u32v4 f = key_frag(blk, c);
+        for (int c = 0; c < DB; ++c) o[c] = f32x16{};
+        if (tiles & 1) ka ^= TILE;
+        if (!(tiles & 1)) va ^= TILE;
+        for (int t = 0; t < tiles; ++t) {
+            __syncthreads();
+            move_tile(false, t);
+            move_tile(true, t);
+            wait_loads_to_lds();
+            __syncthreads();
+#pragma unroll 1
+            for (int blk = 0; blk < 2; ++blk) {
+                scores(blk, 0);
+                hide(0, t, blk);
+                weigh(0, m);
+                settle(0);
+                const int first = KT * t + 64 * part + 32 * blk;
+                const bool some = first + 32 > all_see;
 #pragma unroll
-                for (int s = 0; s < S; ++s) sc[0][s] = mma32<T>(f, q[s][c], sc[0][s]);
-            }
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const int row = row_first + 32 * s + n, vis = row < n_rows ? row / a.group + 1 : len;
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (here + 8 * (r >> 2) + 4 * g + (r & 3) >= vis) sc[0][s][r] = kNone;
-            }
-#pragma unroll
-            for (int s = 0; s < S; ++s) weigh(0, s, m[s]);
-            settle(0);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int x = 2 * blk + h;
-                uint32_t found = 0;
-#pragma unroll
-                for (int c = 0; c < DB; ++c) {
-                    const u32v4 f = value_frag(x, c);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) found |= maybe_not_finite<T>(f[e]);
-                }
-                const bool odd = __any(found != 0);
-#pragma unroll
-                for (int c = 0; c < DB; ++c) {
-                    u32v4 f = value_frag(x, c);
-                    if (odd) {
+                for (int i = 0; i < VF; ++i) {
+                    u32v4 f = value_frag(2 * blk + i / DB, i % DB);
+                    if (some) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) f[e] = finite_halves<T>(f[e]);
                     }
-#pragma unroll
-                    for (int s = 0; s < S; ++s) o[s][c] = mma32<T>(f, p[s][h], o[s][c]);
+                    o[i % DB] = mma32<T>(f, p[i / DB], o[i % DB]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                if (odd) {
-                    // Values that are not finite, taken out above as a weight of zero does not hide them, are added to the rows
-                    // that see them (times any weight above zero they stay what they are).
+                if (!some) continue;
 #pragma unroll 1
-                    for (int i = 0; i < 16; ++i) {
-                        const int r = 64 * part + 16 * x + i;  // of the tile
+                for (int i = 0; i < 32; ++i) {
+                    const int r = 64 * part + 32 * blk + i;  // of the tile
+                    const bool sees = row < n_rows && first + i <= token;
 #pragma unroll
-                        for (int c = 0; c < DB; ++c)
+                    for (int c = 0; c < DB; ++c) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const u32x2 v = *(lds_u32x2 *)(lds0 + 2 * TILE + (t & 1) * TILE + r * ROW + (((4 * c + j) ^ key_of_v<DP>(r)) * 16) + 8 * g);
+                        for (int j = 0; j < 4; ++j) {
+                            const u32x2 v = *(lds_u32x2 *)(lds0 + 2 * TILE + (t & 1) * TILE + r * ROW + (((4 * c + j) ^ key_of_v<DP>(r)) * 16) + 8 * g);
 #pragma unroll
-                                for (int s = 0; s < S; ++s) {
-                                    const int row = row_first + 32 * s + n;
-                                    const bool sees = row < n_rows && KT * t + r <= row / a.group;
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        const float y = odd_value<T>((e & 2 ? v.y : v.x) >> (16 * (e & 1)));
-                                        o[s][c][4 * j + e] += sees ? y : 0.0f;
-                                    }
-                                }
+                            for (int e = 0; e < 4; ++e) {
+                                const float y = odd_value<T>((e & 2 ? v.y : v.x) >> (16 * (e & 1)));
+                                o[c][4 * j + e] += sees ? y : 0.0f;
                             }
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
                     }
                 }
             }
+            ka ^= TILE;
+            va ^= TILE;
         }
-        __syncthreads();  // nobody reads these keys any more
-        move_keys(t + 2);
-        ka ^= TILE;
-        va ^= TILE;
     }
 
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        l[s] += __shfl_xor(l[s], 32);
-        lr[s] += __shfl_xor(lr[s], 32);
-        m[s] = stored_shift(m[s], lr[s]);
-    }
-    if constexpr (PARTS == 2) {  // the wave of the same rows' other positions hands over through LDS
+    l += __shfl_xor(l, 32);
+    lr += __shfl_xor(lr, 32);
+    m = stored_shift(m, lr);
+    if constexpr (PARTS == 2) {  // part 1 hands over through LDS
         constexpr int PAD = DP + 4;
-        static_assert(WQ * S * 32 * (PAD + 4) * 4 <= sizeof lds, "the join fits the tiles' LDS");
-        float *box = reinterpret_cast<float *>(lds) + (wave % WQ) * (S * 32 * PAD);
-        float4 *ml = reinterpret_cast<float4 *>(reinterpret_cast<float *>(lds) + WQ * S * 32 * PAD) + S * 32 * (wave % WQ);
+        static_assert(M * (PAD + 4) * 4 <= sizeof lds, "the join fits the tiles' LDS");
+        float *box = reinterpret_cast<float *>(lds) + (32 * (wave & 3) + n) * PAD;
+        float4 *ml = reinterpret_cast<float4 *>(reinterpret_cast<float *>(lds) + M * PAD) + 32 * (wave & 3) + n;
         __syncthreads();
         if (part == 1) {
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
+            for (int c = 0; c < DB; ++c)
 #pragma unroll
-                for (int c = 0; c < DB; ++c)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        *reinterpret_cast<f32x4 *>(box + (32 * s + n) * PAD + 32 * c + 8 * r + 4 * g) =
-                            f32x4{o[s][c][4 * r], o[s][c][4 * r + 1], o[s][c][4 * r + 2], o[s][c][4 * r + 3]};
-                if (g == 0) ml[32 * s + n] = make_float4(m[s], l[s], lr[s], 0.0f);
-            }
+                for (int r = 0; r < 4; ++r)
+                    *reinterpret_cast<f32x4 *>(box + 32 * c + 8 * r + 4 * g) = f32x4{o[c][4 * r], o[c][4 * r + 1], o[c][4 * r + 2], o[c][4 * r + 3]};
+            if (g == 0) *ml = make_float4(m, l, lr, 0.0f);
         }
         __syncthreads();
         if (part == 1) return;
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const float4 x = ml[32 * s + n];
-            const float up = fmaxf(m[s], x.x);
-            const float f0 = m[s] == kNone ? 0.0f : __builtin_amdgcn_exp2f(m[s] - up), f1 = x.x == kNone ? 0.0f : __builtin_amdgcn_exp2f(x.x - up);
-            m[s] = up;
-            l[s] = l[s] * f0 + x.y * f1;
-            lr[s] = lr[s] * f0 + x.z * f1;
-#pragma unroll
-            for (int c = 0; c < DB; ++c)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const f32x4 y = *reinterpret_cast<const f32x4 *>(box + (32 * s + n) * PAD + 32 * c + 8 * r + 4 * g);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[s][c][4 * r + e] = o[s][c][4 * r + e] * f0 + y[e] * f1;
-                }
-        }
-    }
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const int row = row_first + 32 * s + n, token = row / a.group, hq = head * a.group + row - token * a.group;
-        if (row >= n_rows) continue;
-        const float inv = 1.0f / lr[s];
-        typedef T T4 __attribute__((ext_vector_type(4)));
-        T *out = static_cast<T *>(a.out) + (int64_t)(t0 + token) * a.o_ts + (int64_t)hq * a.o_hs;
+        const float4 x = *ml;
+        const float up = fmaxf(m, x.x);
+        const float f0 = m == kNone ? 0.0f : __builtin_amdgcn_exp2f(m - up), f1 = x.x == kNone ? 0.0f : __builtin_amdgcn_exp2f(x.x - up);
+        m = up;
+        l = l * f0 + x.y * f1;
+        lr = lr * f0 + x.z * f1;
 #pragma unroll
         for (int c = 0; c < DB; ++c)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int d = 32 * c + 8 * r + 4 * g;
-                if (d < D)
-                    *reinterpret_cast<T4 *>(out + d) = __builtin_convertvector(
-                        (f32x4{o[s][c][4 * r], o[s][c][4 * r + 1], o[s][c][4 * r + 2], o[s][c][4 * r + 3]}) * inv, T4);
+                const f32x4 y = *reinterpret_cast<const f32x4 *>(box + 32 * c + 8 * r + 4 * g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[c][4 * r + e] = o[c][4 * r + e] * f0 + y[e] * f1;
             }
-        if (LSE && g == 0) a.lse[(int64_t)(t0 + token) * a.q_heads + hq] = (m[s] + __builtin_amdgcn_logf(l[s])) * 0.69314718055994531f;
     }
+    if (row >= n_rows) return;
+    const float inv = 1.0f / lr;
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    T *out = static_cast<T *>(a.out) + (int64_t)(t0 + token) * a.o_ts + (int64_t)hq * a.o_hs;
+#pragma unroll
+    for (int c = 0; c < DB; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int d = 32 * c + 8 * r + 4 * g;
+            if (d < D)
+                *reinterpret_cast<T4 *>(out + d) =
+                    __builtin_convertvector((f32x4{o[c][4 * r], o[c][4 * r + 1], o[c][4 * r + 2], o[c][4 * r + 3]}) * inv, T4);
+        }
+    if (LSE && g == 0) a.lse[(int64_t)(t0 + token) * a.q_heads + hq] = (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
 }
 
-template <class T, class P>
-static int run_prompt_shape(PromptArgs a, hipStream_t s) {
-    a.slots = prompt_slot(a.n_tokens * a.group, a.n_seqs, P::ROWS);
+template <class T, int DP, int PARTS>
+static int run_prompt_parts(PromptArgs a, hipStream_t s) {
     const int64_t wgs = (int64_t)a.slots * a.kv_heads;
     if (wgs > INT32_MAX) return (int)hipErrorInvalidValue;
     for (;; a.first_wg += kMaxWgs) {
         const int64_t left = wgs - a.first_wg;
         const unsigned grid = (unsigned)(left < kMaxWgs ? left : kMaxWgs);
         if (a.lse)
-            prompt_kernel<T, P, true><<<grid, kAttnThreads, 0, s>>>(a);
+            prompt_kernel<T, DP, PARTS, true><<<grid, 256 * PARTS, 0, s>>>(a);
         else
-            prompt_kernel<T, P, false><<<grid, kAttnThreads, 0, s>>>(a);
+            prompt_kernel<T, DP, PARTS, false><<<grid, 256 * PARTS, 0, s>>>(a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || left <= kMaxWgs) return (int)e;
     }
@@ -489,10 +447,12 @@ static int run_prompt_shape(PromptArgs a, hipStream_t s) {
 
 template <class T, int DP>
 static int run_prompt(const PromptArgs &a, bool many, hipStream_t s) {
-    if constexpr (DP == 256)  // (the outputs of 32 rows fill the registers, two tiles of 64 positions the LDS)
-        return run_prompt_shape<T, PromptShape<256, 1, 4>>(a, s);
+    if constexpr (DP == 256)  // (two parts' tiles do not fit the LDS)
+        return run_prompt_parts<T, 256, 1>(a, s);
     else
-        return many ? run_prompt_shape<T, PromptShape<DP, 2, 4>>(a, s) : run_prompt_shape<T, PromptShape<DP, 2, 2>>(a, s);
+        return many ? run_prompt_parts<T, DP, 1>(a, s) : run_prompt_parts<T, DP, 2>(a, s);
 }
+
+#undef BPW_INLINE
 
 }  // namespace bpw

@@ -36,11 +36,9 @@ bpw::Kv4Rows kv4_values(const bpw_paged_kv4 &c) {
     return {c.d_v, c.d_v_scale, c.v_page_stride, c.v_head_stride, c.vs_page_stride, c.vs_head_stride, (int32_t)c.v_row_stride, (int32_t)c.vs_row_stride};
 }
 
-// Query rows of all key/value heads from which tiles of 256 rows are taken, below it 128: larger tiles read keys and values
-// less often, smaller ones spread over more CUs. Measured, us a call (128, 256): 41 k rows (2048 tokens, 20 / 5 heads of 128)
-// 48, 70; 131 k (4096 tokens of 32 heads) 191, 172; 216 k (24 prompts of up to 1500 tokens, 12 / 4 heads of 80) 172, 141;
-// 524 k (8 of 2048, 32 / 8 heads of 128) 475, 371.
-constexpr int64_t kPromptManyRows = 256 * 320;
+// Tiles of query rows of all key/value heads from which a workgroup takes one with four waves; below it with eight, as a CU
+// would have few of them.
+constexpr int64_t kPromptManyTiles = 512;
 
 int32_t padded(int32_t head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 
@@ -95,7 +93,8 @@ bpw_status bpw_prompt_attn(const bpw_prompt_attn_args *a, void *stream) {
     p.n_tokens = a->n_tokens, p.n_seqs = a->n_seqs;
     p.q_heads = a->q.heads, p.kv_heads = a->k.heads, p.group = group, p.head_dim = a->head_dim;
     p.scale_log2 = scale_log2;
-    const bool many = (int64_t)a->n_tokens * group * a->k.heads >= kPromptManyRows;
+    p.slots = bpw::prompt_slot(a->n_tokens * group, a->n_seqs);
+    const bool many = (int64_t)a->n_tokens * group * a->k.heads >= kPromptManyTiles * bpw::kPromptRows;
     const int32_t dp = padded(a->head_dim);
     const int e = dp == 64    ? bpw::launch_prompt_d64(p, dt, many, stream)
                   : dp == 128 ? bpw::launch_prompt_d128(p, dt, many, stream)
