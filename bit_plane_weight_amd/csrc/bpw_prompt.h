@@ -21,17 +21,28 @@ namespace bpw {
 
 #define BPW_INLINE __attribute__((always_inline))
 
-// The sequence whose tiles hold slot `slot`: the last whose first slot is not beyond it, or -1. Every wave by itself, 64
-// probes at a time. Starts that do not rise give some sequence.
-__device__ __forceinline__ int prompt_seq(const PromptArgs &a, int slot) {
-    const auto first = [&](int b) { return prompt_slot(min(max(a.starts[b], 0), a.n_tokens) * a.group, b); };
+// The sequence whose tiles of ROWS query rows hold a slot: its first token, its tokens, its first slot.
+struct PromptSeq {
+    int first, tokens, slot;
+};
+
+// It is the last sequence whose first slot is not beyond `slot`; no tokens if there is none. Every wave by itself, 63 probes at a
+// time, the last of which have the starts of the sequence and of the next. Starts that do not rise give some sequence.
+template <int ROWS>
+__device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs &a, int slot) {
+    const int lane = threadIdx.x & 63;
     int lo = 0, hi = a.n_seqs;
     while (true) {
-        const int step = (hi - lo + 63) / 64, at = lo + (int)(threadIdx.x & 63) * step;
-        const uint64_t below = __ballot(at < hi && first(at) <= slot);
-        if (!below) return -1;
-        lo += (63 - __builtin_clzll(below)) * step;
-        if (step == 1) return __builtin_amdgcn_readfirstlane(lo);
+        const int step = (hi - lo + 62) / 63, at = min(lo + lane * step, a.n_seqs);
+        const int start = min(max(a.starts[at], 0), a.n_tokens), first = prompt_slot(start * a.group, at, ROWS);
+        const uint64_t below = __ballot(lane < 63 && lo + lane * step < hi && first <= slot);
+        if (!below) return {0, 0, 0};
+        const int l = 63 - __builtin_clzll(below);
+        if (step == 1) {
+            const int t0 = __builtin_amdgcn_readlane(start, l), t1 = __builtin_amdgcn_readlane(start, l + 1);
+            return {t0, max(t1 - t0, 0), __builtin_amdgcn_readlane(first, l)};
+        }
+        lo += l * step;
         hi = min(lo + step, hi);
     }
 }
@@ -84,28 +95,27 @@ __device__ __forceinline__ void static_for(F f) {
 typedef __attribute__((address_space(3))) const u32v4 lds_u32v4;
 typedef __attribute__((address_space(3))) const u32x2 lds_u32x2;
 
-// A workgroup of PARTS times four waves takes 128 query rows, 32 a wave, and 64 positions a part at a time: the waves of
-// part 1 the second 64 of each 128, joined with part 0's at the end.
-template <class T, int DP, int PARTS, bool LSE>
-__global__ __launch_bounds__(256 * PARTS, DP <= 128 ? 2 : 1) void prompt_kernel(PromptArgs a) {
-    constexpr int KT = 64 * PARTS, M = kPromptRows;
+// A workgroup of four waves takes 128 / PARTS query rows, 32 a wave, and 64 positions at a time; with two PARTS the waves of part
+// p take the p-th 32 of them, and part 1's results are joined with part 0's at the end.
+template <class T, int DP, int PARTS, bool PIPE, bool LSE>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void prompt_kernel(PromptArgs a) {
+    constexpr int KT = 64, M = 128 / PARTS, NB = 2 / PARTS;  // positions and rows of a tile, blocks of 32 positions of a wave
     constexpr int ROW = DP * 2, CPR = DP / 8, RPI = 64 / CPR;  // row bytes, chunks of a row, rows of one load
     constexpr int KC = DP / 16, DB = DP / 32, TILE = KT * ROW;  // bytes of a tile of keys or values
     __shared__ __attribute__((aligned(4096))) uint8_t lds[4 * TILE];  // keys twice, values twice
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n = lane & 31, g = lane >> 5, part = wave >> 2;
+    const int n = lane & 31, g = lane >> 5, part = PARTS == 2 ? wave >> 1 : 0, rows_of = PARTS == 2 ? wave & 1 : wave;
     const int D = a.head_dim;
 
+    // Tiles of many positions first; workgroup id runs on XCD id % 8, so that with eight key/value heads each L2 holds one.
     const int id = a.first_wg + (int)blockIdx.x, head = id % a.kv_heads, slot = a.slots - 1 - id / a.kv_heads;
-    const int b = prompt_seq(a, slot);
-    if (b < 0) return;
-    const int t0 = min(max(a.starts[b], 0), a.n_tokens), t1 = min(max(a.starts[b + 1], t0), a.n_tokens);
-    const int len = t1 - t0, n_rows = len * a.group, row0 = (slot - prompt_slot(t0 * a.group, b)) * M;
-    if (row0 < 0 || row0 >= n_rows) return;
+    const PromptSeq seq = prompt_seq<M>(a, slot);
+    const int t0 = seq.first, len = seq.tokens, n_rows = len * a.group, row0 = (slot - seq.slot) * M;
+    if (row0 >= n_rows) return;
     const int end = (min(row0 + M, n_rows) - 1) / a.group + 1;  // positions that the tile's last row sees
     const int tiles = (end + KT - 1) / KT;
 
-    const int row_first = row0 + 32 * (wave & 3), row = row_first + n;
+    const int row_first = row0 + 32 * rows_of, row = row_first + n;
     const int token = row / a.group, hq = head * a.group + row - token * a.group;
     const int vis = row < n_rows ? token + 1 : len;
     const int all_see = __builtin_amdgcn_readfirstlane(row_first / a.group + 1);  // what every row of the wave sees
@@ -149,11 +159,11 @@ __global__ __launch_bounds__(256 * PARTS, DP <= 128 ? 2 : 1) void prompt_kernel(
 
     // LDS addresses of this lane's reads of the current tiles. The chunk of element group c is chosen by an exclusive-or of the
     // first one's address (blocks of 32 and 16 positions are whole keys apart), and so is the other buffer.
-    uint32_t ka = lds0 + (64 * part + n) * ROW + ((g ^ key_of_k<DP>(n)) * 16), va;
+    uint32_t ka = lds0 + (32 * part + n) * ROW + ((g ^ key_of_k<DP>(n)) * 16), va;
     constexpr uint32_t V8 = 16 * (key_of_v<DP>(8) ^ key_of_v<DP>(0));  // of the row 8 further on
     {
         const int i = lane & 15, r = 4 * g + (i >> 2), chunk = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
-        va = lds0 + 2 * TILE + (64 * part + r) * ROW + ((chunk ^ key_of_v<DP>(r)) * 16) + (i & 1) * 8;
+        va = lds0 + 2 * TILE + (32 * part + r) * ROW + ((chunk ^ key_of_v<DP>(r)) * 16) + (i & 1) * 8;
     }
     const auto key_frag = [&](int blk, int c) BPW_INLINE { return *(lds_u32v4 *)((ka ^ (32 * c)) + blk * 32 * ROW); };
     const auto value_frag = [&](int x, int c) BPW_INLINE {  // positions 16 x .. 16 x + 15 of this wave's
@@ -212,7 +222,7 @@ __global__ __launch_bounds__(256 * PARTS, DP <= 128 ? 2 : 1) void prompt_kernel(
     };
     // Positions that a row does not see, in the scores of block blk of tile t.
     const auto hide = [&](int which, int t, int blk) BPW_INLINE {
-        const int first = KT * t + 64 * part + 32 * blk;
+        const int first = KT * t + 32 * (part + blk);
 #pragma unroll
         for (int r = 0; r < 16; ++r)
             if (first + 8 * (r >> 2) + 4 * g + (r & 3) >= vis) sc[which][r] = kNone;
@@ -260,66 +270,87 @@ __global__ __launch_bounds__(256 * PARTS, DP <= 128 ? 2 : 1) void prompt_kernel(
         for (int i = 0; i < VF; ++i) o[i % DB] = mma32<T>(value_frag(2 * blk + i / DB, i % DB), p[i / DB], o[i % DB]);
     };
 
-    // A block of 32 positions after another: the products of the last block's values beside this block's exponentials, those of
-    // the next block's scores beside the rounding of its weights. Keys run a tile ahead of values.
     uint32_t odd = 0;  // a value that only some rows of the wave see is not finite: a weight of zero does not hide it
-    move_tile(false, 0);
-    move_tile(true, 0);
-    move_tile(false, 1);
-    wait_loads_to_lds();
-    __syncthreads();
-    scores(0, 0);
-    hide(0, 0, 0);
-    weigh(0, m);
-    settle(0);
-    scores(1, 1);
-    hide(1, 0, 1);
-    ka ^= TILE;
-    int t = 0;
-    const auto arrive = [&] BPW_INLINE {
-        wait_loads_to_lds();
-        __syncthreads();  // values t and keys t + 1 are there, and nobody reads those before them any more
-    };
     const auto look_for_odd = [&] BPW_INLINE {
-#pragma unroll 1
-        for (int j = 0; j < 4 * DB; j += 2) {
-            const u32v4 f = value_frag(j / DB, j % DB), h = value_frag(j / DB, j % DB + 1);
+#pragma unroll 4
+        for (int j = 0; j < 2 * NB * DB; ++j) {
+            const u32v4 f = value_frag(j / DB, j % DB);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) odd |= maybe_not_finite<T>(f[e]) | maybe_not_finite<T>(h[e]);
+            for (int e = 0; e < 4; ++e) odd |= maybe_not_finite<T>(f[e]);
         }
     };
-    const auto tile = [&](auto masked) BPW_INLINE {
-        first_values(0);
-        first_keys(0);
+    const int wave_end = row_first < n_rows ? (min(row_first + 32, n_rows) - 1) / a.group + 1 : 0;  // what some row of the wave sees
+    const auto arrive = [&] BPW_INLINE {
+        wait_loads_to_lds();
+        __syncthreads();  // what was on its way is there, and nobody reads the tiles before any more
+    };
+    int t = 0;
+    move_tile(false, 0);
+    move_tile(true, 0);
+    if constexpr (PIPE) {
+        // Tiles that all rows see, a block of 32 positions after another: the products of the last block's values beside this
+        // block's exponentials, those of the next block's scores beside the rounding of its weights.
+        const int full = (row0 / a.group + 1) / KT;
+        if (full > 0) {
+            move_tile(false, 1);  // keys run a tile ahead of values
+            arrive();
+            scores(0, 0);
+            weigh(0, m);
+            settle(0);
+            scores(1, 1);
+            ka ^= TILE;
+            for (; t + 1 < full; ++t) {
+                arrive();
+                first_values(0);
+                first_keys(0);
+                move_tile(true, t + 1);
+                move_tile(false, t + 2);
+                values_and_weights(0, 1, 4);
+                first_values(1);
+                scores_and_rounding(0, 0);
+                settle(1);
+                first_keys(1);
+                values_and_weights(1, 0, 0);
+                scores_and_rounding(1, 1);
+                settle(0);
+                ka ^= TILE;
+                va ^= TILE;
+            }
+            arrive();
+            move_tile(true, t + 1);
+            values(0);
+            weigh(1, m);
+            settle(1);
+            values(1);
+            va ^= TILE;
+            ++t;
+        }
+    }
+    for (; t < tiles; ++t) {
+        arrive();
+        move_tile(false, t + 1);
         move_tile(true, t + 1);
-        move_tile(false, t + 2);
-        values_and_weights(0, 1, 4);
-        first_values(1);
-        scores_and_rounding(0, 0);
-        settle(1);
-        if constexpr (masked) hide(0, t + 1, 0);
-        first_keys(1);
-        values_and_weights(1, 0, 0);
-        scores_and_rounding(1, 1);
-        settle(0);
-        if constexpr (masked) hide(1, t + 1, 1);
+        if (KT * t + 32 * part < wave_end) {
+            const bool all = KT * t + 64 <= all_see;
+            scores(0, 0);
+            if constexpr (NB == 2) scores(1, 1);
+            if (!all) {
+                look_for_odd();
+                hide(0, t, 0);
+                if constexpr (NB == 2) hide(1, t, 1);
+            }
+            weigh(0, m);
+            settle(0);
+            values(0);
+            if constexpr (NB == 2) {
+                weigh(1, m);
+                settle(1);
+                values(1);
+            }
+        }
         ka ^= TILE;
         va ^= TILE;
-    };
-    for (; KT * (t + 1) + 64 * part + 64 <= all_see && t + 1 < tiles; ++t) {
-        arrive();
-        tile(std::false_type{});
     }
-    for (;; ++t) {
-        arrive();
-        if (KT * t + 64 * part + 64 > all_see) look_for_odd();
-        if (t + 1 == tiles) break;
-        tile(std::true_type{});
-    }
-    values(0);
-    weigh(1, m);
-    settle(1);
-    values(1);
 
     // Values that are not finite and not seen by all: the tile of rows once more, step by step, with zeros in the place of such
     // values, which are then added to the rows that see them (times any weight above zero they stay what they are).
@@ -328,8 +359,7 @@ __global__ __launch_bounds__(256 * PARTS, DP <= 128 ? 2 : 1) void prompt_kernel(
         l = lr = 0.0f;
 #pragma unroll
         for (int c = 0; c < DB; ++c) o[c] = f32x16{};
-        if (tiles & 1) ka ^= TILE;
-        if (!(tiles & 1)) va ^= TILE;
+        if (tiles % 2) ka ^= TILE, va ^= TILE;
         for (int t = 0; t < tiles; ++t) {
             __syncthreads();
             move_tile(false, t);
@@ -337,12 +367,12 @@ __global__ __launch_bounds__(256 * PARTS, DP <= 128 ? 2 : 1) void prompt_kernel(
             wait_loads_to_lds();
             __syncthreads();
 #pragma unroll 1
-            for (int blk = 0; blk < 2; ++blk) {
+            for (int blk = 0; blk < NB; ++blk) {
                 scores(blk, 0);
                 hide(0, t, blk);
                 weigh(0, m);
                 settle(0);
-                const int first = KT * t + 64 * part + 32 * blk;
+                const int first = KT * t + 32 * (part + blk);
                 const bool some = first + 32 > all_see;
 #pragma unroll
                 for (int i = 0; i < VF; ++i) {
@@ -357,7 +387,7 @@ __global__ __launch_bounds__(256 * PARTS, DP <= 128 ? 2 : 1) void prompt_kernel(
                 if (!some) continue;
 #pragma unroll 1
                 for (int i = 0; i < 32; ++i) {
-                    const int r = 64 * part + 32 * blk + i;  // of the tile
+                    const int r = 32 * (part + blk) + i;  // of the tile
                     const bool sees = row < n_rows && first + i <= token;
 #pragma unroll
                     for (int c = 0; c < DB; ++c) {
@@ -385,8 +415,8 @@ __global__ __launch_bounds__(256 * PARTS, DP <= 128 ? 2 : 1) void prompt_kernel(
     if constexpr (PARTS == 2) {  // part 1 hands over through LDS
         constexpr int PAD = DP + 4;
         static_assert(M * (PAD + 4) * 4 <= sizeof lds, "the join fits the tiles' LDS");
-        float *box = reinterpret_cast<float *>(lds) + (32 * (wave & 3) + n) * PAD;
-        float4 *ml = reinterpret_cast<float4 *>(reinterpret_cast<float *>(lds) + M * PAD) + 32 * (wave & 3) + n;
+        float *box = reinterpret_cast<float *>(lds) + (32 * rows_of + n) * PAD;
+        float4 *ml = reinterpret_cast<float4 *>(reinterpret_cast<float *>(lds) + M * PAD) + 32 * rows_of + n;
         __syncthreads();
         if (part == 1) {
 #pragma unroll
@@ -429,17 +459,18 @@ __global__ __launch_bounds__(256 * PARTS, DP <= 128 ? 2 : 1) void prompt_kernel(
     if (LSE && g == 0) a.lse[(int64_t)(t0 + token) * a.q_heads + hq] = (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
 }
 
-template <class T, int DP, int PARTS>
+template <class T, int DP, int PARTS, bool PIPE>
 static int run_prompt_parts(PromptArgs a, hipStream_t s) {
+    a.slots = prompt_slot(a.n_tokens * a.group, a.n_seqs, 128 / PARTS);
     const int64_t wgs = (int64_t)a.slots * a.kv_heads;
     if (wgs > INT32_MAX) return (int)hipErrorInvalidValue;
     for (;; a.first_wg += kMaxWgs) {
         const int64_t left = wgs - a.first_wg;
         const unsigned grid = (unsigned)(left < kMaxWgs ? left : kMaxWgs);
         if (a.lse)
-            prompt_kernel<T, DP, PARTS, true><<<grid, 256 * PARTS, 0, s>>>(a);
+            prompt_kernel<T, DP, PARTS, PIPE, true><<<grid, 256, 0, s>>>(a);
         else
-            prompt_kernel<T, DP, PARTS, false><<<grid, 256 * PARTS, 0, s>>>(a);
+            prompt_kernel<T, DP, PARTS, PIPE, false><<<grid, 256, 0, s>>>(a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || left <= kMaxWgs) return (int)e;
     }
@@ -447,10 +478,7 @@ static int run_prompt_parts(PromptArgs a, hipStream_t s) {
 
 template <class T, int DP>
 static int run_prompt(const PromptArgs &a, bool many, hipStream_t s) {
-    if constexpr (DP == 256)  // (two parts' tiles do not fit the LDS)
-        return run_prompt_parts<T, 256, 1>(a, s);
-    else
-        return many ? run_prompt_parts<T, DP, 1>(a, s) : run_prompt_parts<T, DP, 2>(a, s);
+    return many ? run_prompt_parts<T, DP, 1, true>(a, s) : run_prompt_parts<T, DP, 2, false>(a, s);
 }
 
 #undef BPW_INLINE

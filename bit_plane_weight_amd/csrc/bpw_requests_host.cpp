@@ -93,8 +93,7 @@ bpw_status bpw_prompt_attn(const bpw_prompt_attn_args *a, void *stream) {
     p.n_tokens = a->n_tokens, p.n_seqs = a->n_seqs;
     p.q_heads = a->q.heads, p.kv_heads = a->k.heads, p.group = group, p.head_dim = a->head_dim;
     p.scale_log2 = scale_log2;
-    p.slots = bpw::prompt_slot(a->n_tokens * group, a->n_seqs);
-    const bool many = (int64_t)a->n_tokens * group * a->k.heads >= kPromptManyTiles * bpw::kPromptRows;
+    const bool many = (int64_t)a->n_tokens * group * a->k.heads >= kPromptManyTiles * 128;
     const int32_t dp = padded(a->head_dim);
     const int e = dp == 64    ? bpw::launch_prompt_d64(p, dt, many, stream)
                   : dp == 128 ? bpw::launch_prompt_d128(p, dt, many, stream)
