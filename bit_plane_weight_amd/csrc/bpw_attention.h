@@ -416,7 +416,8 @@ __device__ __forceinline__ f32x16 mma32<_Float16>(u32v4 a, u32v4 b, f32x16 c) {
 
 // Loads straight to LDS: N times 16 bytes a lane, the i-th from `base` (the same in all lanes) + offset[i] to LDS at
 // `dst` (the same) + 1024 i + 16 * lane. Waited for by vmcnt. Written as asm (m0, which holds the LDS
-// address, is put back) because the compiler makes every later LDS read wait for loads to LDS that it knows
+// address, is put back; five wait states stand before the first load, as a vector instruction may have written `base` or
+// `dst`) because the compiler makes every later LDS read wait for loads to LDS that it knows
 // of, whatever part of LDS they write; the asm writes no register that a load fills. An instruction's
 // offset moves both of its addresses, so the i-th lane offset is given 1024 i less.
 template <int N>
@@ -424,7 +425,7 @@ __device__ __forceinline__ void load_to_lds(uint32_t dst, const void *base, cons
     uint32_t keep;
     if constexpr (N == 4)
         asm volatile(
-            "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+            "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 2\n\t"
             "global_load_lds_dwordx4 %2, %6\n\tglobal_load_lds_dwordx4 %3, %6 offset:0x400\n\t"
             "global_load_lds_dwordx4 %4, %6 offset:0x800\n\tglobal_load_lds_dwordx4 %5, %6 offset:0xc00\n\t"
             "s_mov_b32 m0, %0"
@@ -433,7 +434,7 @@ __device__ __forceinline__ void load_to_lds(uint32_t dst, const void *base, cons
             : "memory");
     else if constexpr (N == 2)
         asm volatile(
-            "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+            "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 2\n\t"
             "global_load_lds_dwordx4 %2, %4\n\tglobal_load_lds_dwordx4 %3, %4 offset:0x400\n\t"
             "s_mov_b32 m0, %0"
             : "=&s"(keep)
@@ -441,7 +442,7 @@ __device__ __forceinline__ void load_to_lds(uint32_t dst, const void *base, cons
             : "memory");
     else
         asm volatile(
-            "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
+            "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 2\n\tglobal_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
             : "=&s"(keep)
             : "s"(dst), "v"(offset[0]), "s"(base)
             : "memory");

@@ -206,6 +206,7 @@ int launch_kv4_append(const Kv4AppendArgs &a, int32_t dt_in, int32_t dt_out, voi
 struct Attn4Args {
     AttnArgs a;
     Kv4Rows kc, vc;
+    int32_t dense;           // heads of the padded size; rows of powers follow one another, those of 16 positions whole words
 };
 int launch_attn4_d64(const Attn4Args &a, int32_t dtype, bool one_launch, void *stream);
 int launch_attn4_d128(const Attn4Args &a, int32_t dtype, bool one_launch, void *stream);

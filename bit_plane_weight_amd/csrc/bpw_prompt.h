@@ -13,7 +13,7 @@
 // XCD's L2 holds one.
 #pragma once
 
-#include <utility>
+#include <type_traits>
 
 #include "bpw_attention.h"
 
@@ -47,14 +47,25 @@ __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs &a, int slot) {
     }
 }
 
-// 16 bytes a lane from a buffer (offsets beyond its end give zeros) to LDS at m0 + AT + 16 * lane, from `offset` + AT; m0 and the
-// buffer are the same in all lanes. Waited for by vmcnt; asm, as load_to_lds() is. m0 is set apart from the loads, because
-// each write of it waits for the loads to LDS before it (160 cycles a load); nothing else here uses it.
-__device__ __forceinline__ void lds_base(uint32_t at) { asm volatile("s_mov_b32 m0, %0\n\ts_nop 0" ::"s"(at) : "m0", "memory"); }
-template <int AT>
-__device__ __forceinline__ void buffer_to_lds(uint32_t offset, u32v4 buffer) {
-    static_assert(AT < 4096, "an instruction's offset has 12 bits");
-    asm volatile("buffer_load_dwordx4 %0, %1, 0 offen offset:%2 lds" ::"v"(offset), "s"(buffer), "n"(AT) : "memory");
+// N times 16 bytes a lane from a buffer (offsets beyond its end give zeros): the i-th from offset[i] + 1024 i to LDS at `at` +
+// 1024 i + 16 * lane; `at` and the buffer are the same in all lanes. Waited for by vmcnt; asm, as load_to_lds() is. m0 is set
+// once, because each write of it waits for the loads to LDS before it (160 cycles a load); nothing else here uses it. A
+// vector instruction's write of a scalar register (v_readlane) needs five wait states before a load reads it, which the
+// compiler does not see to for asm.
+template <int N>
+__device__ __forceinline__ void buffer_to_lds(uint32_t at, u32v4 buffer, const uint32_t *offset) {
+    static_assert(N == 2 || N == 4, "an instruction's offset has 12 bits");
+    if constexpr (N == 4)
+        asm volatile(
+            "s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %2, %1, 0 offen lds\n\t"
+            "buffer_load_dwordx4 %3, %1, 0 offen offset:0x400 lds\n\tbuffer_load_dwordx4 %4, %1, 0 offen offset:0x800 lds\n\t"
+            "buffer_load_dwordx4 %5, %1, 0 offen offset:0xc00 lds"
+            ::"s"(at), "s"(buffer), "v"(offset[0]), "v"(offset[1]), "v"(offset[2]), "v"(offset[3]) : "m0", "memory");
+    else
+        asm volatile(
+            "s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %2, %1, 0 offen lds\n\t"
+            "buffer_load_dwordx4 %3, %1, 0 offen offset:0x400 lds"
+            ::"s"(at), "s"(buffer), "v"(offset[0]), "v"(offset[1]) : "m0", "memory");
 }
 
 // c + the two numbers of a word. (Not by a dot product: v_dot2 holds the matrix cores up, 50 cycles a product with one
@@ -80,16 +91,6 @@ template <class T>
 __device__ __forceinline__ float odd_value(uint32_t half) {
     constexpr uint32_t ones = __is_same(T, __bf16) ? 0x7F80u : 0x7C00u;
     return (half & ones) == ones ? (float)__builtin_bit_cast(T, (uint16_t)half) : 0.0f;
-}
-
-// f(0), f(1), .. f(N - 1) with constants.
-template <int... I, class F>
-__device__ __forceinline__ void static_for_each(std::integer_sequence<int, I...>, F f) {
-    (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, class F>
-__device__ __forceinline__ void static_for(F f) {
-    static_for_each(std::make_integer_sequence<int, N>{}, f);
 }
 
 typedef __attribute__((address_space(3))) const u32v4 lds_u32v4;
@@ -151,10 +152,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void prompt_kernel(PromptAr
         const uint32_t there = (uint32_t)((-here & (t - tiles)) >> 31);  // all ones, or 0: nothing (without a branch)
         const uint64_t at = (uint64_t)(base + (int64_t)first * stride) - BACK;
         const u32v4 buffer = {(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (uint32_t)(2 * ((here - 1) * stride + D) + BACK) & there, 0x00020000u};
-        static_for<LOADS>([&](auto i) {
-            if constexpr (i % GROUP == 0) lds_base(lds0 + (values ? 2 * TILE : 0) + (t & 1) * TILE + 16 * wave * ROW + 1024 * i);
-            buffer_to_lds<1024 * (i % GROUP)>(values ? vs[i] : ks[i], buffer);
-        });
+#pragma unroll
+        for (int i = 0; i < LOADS; i += GROUP)
+            buffer_to_lds<GROUP>(lds0 + (values ? 2 * TILE : 0) + (t & 1) * TILE + 16 * wave * ROW + 1024 * i, buffer, (values ? vs : ks) + i);
     };
 
     // LDS addresses of this lane's reads of the current tiles. The chunk of element group c is chosen by an exclusive-or of the
