@@ -7,10 +7,12 @@
 // l' = f l, t' = f (t + d l) with d = scale (m - M), f = exp(d). The shift of a lane is raised only when a logit passes it by
 // 2^16 in weight, so most rounds form no maximum against the running one.
 //
-// Bound: HBM, each logit read once. A wave takes 512 neighbours at a time, eight a lane, one round ahead of their use. The
-// best n entries are kept by each wave: a list of 64 places in LDS to which lanes add what exceeds the wave's
-// n-th best; a full list is ranked (each lane counts the keys above its own) and cut to n. The first
-// round's n-th largest of the 64 lanes' maxima is a first bar, so that little is added: n log(entries / n) in expectation.
+// Bound: HBM, each logit read once. A wave takes four rounds of 512 entries (eight a lane) while the next four are on their
+// way. 2048 rows of 128256 in bfloat16, the best one: 100 us (5.2 TB/s; 87 without best entries), 168 a round at a time;
+// 64 rows in float32, the best twenty: 21 us, 35 before. The vector units bound it then: 58 instructions for eight entries.
+// The best n entries are kept by each wave: a list of 64 places in LDS to which lanes add what exceeds a bar. The first is
+// the n-th largest of the 64 lanes' maxima over the first four rounds; a list of 2 n or a full one is ranked (each lane
+// counts the keys above its own) and cut to n, whose last is the next bar: n log(entries / n) are added in expectation.
 // Few rows are cut into parts, one workgroup each, joined by a second launch.
 #include "bpw_decode.h"
 #include "bpw_elem.h"
@@ -18,6 +20,7 @@
 namespace bpw {
 
 constexpr int kWavesLp = kLogprobThreads / 64;
+constexpr int kGroup = 4;  // rounds that a workgroup works on while as many are on their way
 constexpr float kLowest = -3.4028234663852886e38f;
 constexpr float kMinusInf = -__builtin_inff();
 constexpr float kLazy = 16.0f;  // log2 units that a logit may lie above the shift
@@ -42,14 +45,30 @@ __device__ __forceinline__ void lds_of_wave_settled() {  // what lanes of this w
     __builtin_amdgcn_wave_barrier();
 }
 
+// The float after x towards larger ones.
+__device__ __forceinline__ float above(float x) {
+    const int32_t b = __builtin_bit_cast(int32_t, x + 0.0f);
+    return __builtin_bit_cast(float, b < 0 ? b - 1 : b + 1);
+}
+
 // The best entries that a wave has seen, as keys.
 struct WaveTop {
     uint64_t *place;  // 64 places in LDS
     int n, want;      // places used, entries wanted (the same in all lanes)
     uint64_t bar;     // only keys above it are added
+    float logit;      // of the bar
 
-    __device__ __forceinline__ WaveTop(uint64_t *p, int k) : place(p), n(0), want(k), bar(0) {}
+    __device__ __forceinline__ WaveTop(uint64_t *p, int k) : place(p), n(0), want(k), bar(0), logit(kMinusInf) {}
 
+    // A first bar: the n-th largest of the lanes' values, to its upper 20 bits (2^-11 of it), which are found one by one.
+    __device__ __forceinline__ void bar_of_maxima(float x) {
+        const uint32_t mine = (uint32_t)(key_of(x, 0) >> 32);
+        uint32_t it = 0;
+        for (uint32_t bit = 1u << 31; bit >= 1u << 12; bit >>= 1)
+            if (__builtin_popcountll(__ballot(mine >= (it | bit))) >= want) it |= bit;
+        const float y = logit_of((uint64_t)it << 32);
+        if (y > kMinusInf) logit = y, bar = key_of(y, -1);  // (below every key of this logit)
+    }
     // Cut to the best, in order.
     __device__ __forceinline__ void rank() {
         const int lane = threadIdx.x & 63;
@@ -61,7 +80,16 @@ struct WaveTop {
         if (lane < n && above < want) place[above] = mine;
         lds_of_wave_settled();
         n = min(n, want);
-        if (n == want) bar = read_lane(lane < n ? place[lane] : 0, want - 1);
+        if (n == want) {
+            bar = read_lane(lane < n ? place[lane] : 0, want - 1);
+            logit = logit_of(bar);
+        }
+    }
+    // The keys of these lanes, for which there is room.
+    __device__ __forceinline__ void append(uint64_t mask, uint64_t key) {
+        const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+        if (mask >> (threadIdx.x & 63) & 1) place[at] = key;
+        n += __builtin_popcountll(mask);
     }
     // A key of each lane, those above the bar (0: none).
     __device__ __forceinline__ void add(uint64_t key) {
@@ -82,33 +110,34 @@ struct WaveTop {
 // Weights of a lane's entries against its shift m: l = sum 2^d, t = sum d 2^d, d = (x - m) c.
 struct LaneSums {
     float m, l, t;
-    __device__ __forceinline__ void to(float top, float c) {
-        const float d = fmaxf((m - top) * c, kLowest), f = __builtin_amdgcn_exp2f(d);
+    __device__ __forceinline__ void to(float top, float c) { move(top, (m - top) * c); }
+    __device__ __forceinline__ void move(float top, float by) {  // to the shift of `top`; by: the old one less the new one, in units of log 2
+        const float d = fmaxf(by, kLowest), f = __builtin_amdgcn_exp2f(d);
         t = f == 0.0f && l == l ? 0.0f : f * (t + d * l);  // (d * l may be infinite)
         l *= f;
         m = top;
     }
 };
 
+// A round of a row: 2048 entries, eight a lane, loaded 16 bytes at a time (rows of any alignment).
 template <class T>
-__device__ __forceinline__ void load_eight(const T *row, int64_t i, int vocab, float (&x)[8]) {
-    if (i >= 0 && i + 8 <= vocab) {  // 16-byte aligned
-        typedef float f4 __attribute__((ext_vector_type(4)));
-        if constexpr (sizeof(T) == 4) {
-            const f4 a = __builtin_nontemporal_load(reinterpret_cast<const f4 *>(row + i));
-            const f4 b = __builtin_nontemporal_load(reinterpret_cast<const f4 *>(row + i + 4));
+struct Round {
+    static constexpr int LOADS = sizeof(T) == 4 ? 2 : 1, EACH = 8 / LOADS;
+    typedef T Vec __attribute__((ext_vector_type(EACH), aligned(sizeof(T))));
+    Vec v[LOADS];
+    // the first entry of a lane's load j, from the round's; entry e is (at(e / EACH) + e % EACH)
+    static __device__ __forceinline__ int at(int j) { return j * EACH * kLogprobThreads + EACH * (int)threadIdx.x; }
+    static constexpr __device__ __forceinline__ int from_first(int e) { return e / EACH * EACH * kLogprobThreads + e % EACH; }
+    static __device__ __forceinline__ int index(int e) { return at(0) + from_first(e); }
+    __device__ __forceinline__ void load(const T *first) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = a[e], x[4 + e] = b[e];
-        } else {
-            const Raw8<T> a = __builtin_nontemporal_load(reinterpret_cast<const Raw8<T> *>(row + i));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = (float)a[e];
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = i + e >= 0 && i + e < vocab ? (float)row[i + e] : kMinusInf;
+        for (int j = 0; j < LOADS; ++j) v[j] = __builtin_nontemporal_load(reinterpret_cast<const Vec *>(first + at(j)));
     }
-}
+    __device__ __forceinline__ void values(float *x) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = (float)v[e / EACH][e % EACH];
+    }
+};
 
 // What a row's sums give, by the first wave: `top` holds its best entries in order.
 template <class T>
@@ -136,65 +165,137 @@ __device__ __forceinline__ void write_row(const LogprobArgs &a, int t, float m, 
 }
 
 template <class T, bool TOP>
-__global__ __launch_bounds__(kLogprobThreads) void logprobs_kernel(LogprobArgs a) {
+__global__ __launch_bounds__(kLogprobThreads, sizeof(T) == 2 ? 5 : 4) void logprobs_kernel(LogprobArgs a) {
     __shared__ uint64_t places[kWavesLp][64];
     __shared__ float sums[kWavesLp][3];
     __shared__ int counts[kWavesLp];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int t = a.first + (int)blockIdx.x / a.parts, part = (int)blockIdx.x % a.parts;
     const T *row = static_cast<const T *>(a.logits) + (int64_t)t * a.row_stride;
-    const int before = (int)(((uintptr_t)row & 15) / sizeof(T));  // the row's entries count from the last 16-byte border
     const float c = a.scale * kLog2e;
-    const int64_t end = min((int64_t)a.vocab, (int64_t)(part + 1) * a.part_rounds * kLogprobRound - before);
-    int64_t i = (int64_t)part * a.part_rounds * kLogprobRound - before + 8 * tid;
 
     WaveTop top(places[wave], a.n_top);
+    // The shift of a wave's lanes is one, `level` in units of log 2: the product m c rounded, so that an exponent is one fma, or,
+    // where that nears the largest float, the product itself (far).
     LaneSums s{kLowest, 0.0f, 0.0f};
-    float next[8], most = kLowest;
-    bool first = true;
-    float top_logit = kMinusInf;
-    load_eight(row, i, a.vocab, next);
-    for (; i - 8 * lane < end; i += kLogprobRound) {  // (the same in all lanes of a wave)
-        float x[8];
+    float most = kLowest, limit = kLowest, level = 0.0f;  // the largest logit; what raises the shift
+    bool far = true;
+    const auto level_of = [&] { return far ? (double)s.m * (double)c : (double)level; };
+    const int32_t begin = part * a.part_rounds, end = min(begin + a.part_rounds, (a.vocab + kLogprobRound - 1) / kLogprobRound);
+    const int32_t full = min(end, a.vocab / kLogprobRound);  // (the round that follows it may have some entries)
+    Round<T> next[kGroup];
+    if (begin < full) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = next[e];
-        const int64_t here = i;
-        if (i + kLogprobRound - 8 * lane < end) load_eight(row, i + kLogprobRound, a.vocab, next);
-        float mx = kMinusInf;
+        for (int u = 0; u < kGroup; ++u) next[u].load(row + (int64_t)min(begin + u, full - 1) * kLogprobRound);
+    }
+    for (int32_t r = begin; r < end; r += kGroup) {
+        float x[8 * kGroup];
+        if (r < full) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, x[e]);
-        most = fmaxf(most, mx);
-        if (__any((mx - s.m) * c > kLazy)) s.to(most, c);
+            for (int u = 0; u < kGroup; ++u) next[u].values(x + 8 * u);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float d = (x[e] - s.m) * c, w = __builtin_amdgcn_exp2f(d);
-            s.l += w;
-            s.t = __builtin_fmaf(fmaxf(d, -1024.0f), w, s.t);  // (0 for a weight of 0, whose d may be infinite)
+            for (int u = 0; u < kGroup; ++u) next[u].load(row + (int64_t)min(r + kGroup + u, full - 1) * kLogprobRound);
         }
-        if constexpr (TOP) {
-            if (first) {  // the n-th largest of the lanes' maxima: what is below it is not among the best
-                first = false;
-                int above = 0;
-                for (int j = 0; j < 64; ++j) {
-                    const float y = read_lane(mx, j);
-                    above += y > mx || (y == mx && j < lane) ? 1 : 0;
-                }
-                const uint64_t it = __ballot(above == a.n_top - 1);
-                const float y = read_lane(mx, __builtin_ctzll(it));
-                if (y > kMinusInf) top.bar = key_of(y, -1);  // (below every key of this logit)
-            } else if (!__any(mx > top_logit)) {
-                continue;  // (an equal logit further on is no better)
+        if (r + kGroup > full) {  // the row's last entries, and what is none
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = kMinusInf;
+            if (full < end) {
+                int32_t i = full * kLogprobRound + Round<T>::at(0);
+                asm volatile("" : "+v"(i));  // (nor are these addresses)
+                T z[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[e] = row[min(i + Round<T>::from_first(e), a.vocab - 1)];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = i + Round<T>::from_first(e) < a.vocab ? (float)z[e] : kMinusInf;
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top.add(x[e] > kMinusInf ? key_of(x[e], (int32_t)(here + e)) : 0);
-            top_logit = top.bar ? logit_of(top.bar) : kMinusInf;
+            for (int u = 0; u < kGroup; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[8 * u + e] = r + u > full ? kMinusInf : r + u == full ? y[e] : x[8 * u + e];
+        }
+        float mu[kGroup], mx = kMinusInf;
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) {
+            mu[u] = x[8 * u];
+#pragma unroll
+            for (int e = 1; e < 7; e += 2) mu[u] = fmaxf(fmaxf(mu[u], x[8 * u + e]), x[8 * u + e + 1]);
+            mu[u] = fmaxf(mu[u], x[8 * u + 7]);
+            mx = fmaxf(mx, mu[u]);
+        }
+        most = fmaxf(most, mx);
+        if (__ballot(mx > limit)) {
+            const float up = wave_max(most);
+            const double old = level_of();
+            limit = up + kLazy / c;
+            level = up * c;
+            far = !(fabsf(level) < 1e30f);
+            s.m = up;
+            s.move(up, (float)(old - level_of()));
+        }
+        const auto weigh = [&](auto exponent) __attribute__((always_inline)) {
+#pragma unroll
+            for (int e = 0; e < 8 * kGroup; ++e) {
+                const float d = exponent(x[e]), w = __builtin_amdgcn_exp2f(d);
+                s.l += w;
+                s.t = __builtin_fmaf(fmaxf(d, -1024.0f), w, s.t);  // (0 for a weight of 0, whose d may be infinite)
+            }
+        };
+        if (far)
+            weigh([&](float y) { return (y - s.m) * c; });
+        else
+            weigh([&](float y) { return __builtin_fmaf(y, c, -level); });
+        if constexpr (TOP) {
+            // Entries that may be among the best: in the first group those that reach the n-th largest of the lanes' maxima, later
+            // those above the n-th best so far (an equal logit further on is no better).
+            const bool first = r == begin;
+            if (first)
+                top.bar_of_maxima(mx);
+            else if (!__ballot(mx > top.logit))
+                continue;
+            float least = first ? fmaxf(top.logit, kLowest) : above(top.logit);
+            bool fits = true;
+#pragma unroll 1
+            for (int again = 0;; ++again) {
+                const int before = top.n;
+                fits = true;
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u) {
+                    if (!__ballot(mu[u] >= least)) continue;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint64_t mask = __ballot(x[8 * u + e] >= least);
+                        if (!mask) continue;
+                        fits = fits && top.n + __builtin_popcountll(mask) <= 64;
+                        if (fits) {
+                            float y = x[8 * u + e];
+                            int32_t i = Round<T>::at(0);
+                            asm volatile("" : "+v"(y), "+v"(i));  // (keys are not worth registers of their own before they are needed)
+                            top.append(mask, key_of(y, i + (r + u) * kLogprobRound + Round<T>::from_first(e)));
+                        }
+                    }
+                }
+                if (fits) break;
+                top.n = before;
+                if (again) break;
+                top.rank();
+                if (!first) least = above(top.logit);
+            }
+            if (!fits) {  // many at once (logits that rise, or are alike): one by one
+#pragma unroll 1
+                for (int e = 0; e < 8 * kGroup; ++e) {
+                    const int32_t i = (r + e / 8) * kLogprobRound + Round<T>::index(e % 8);
+                    const float y = r + e / 8 < end && i < a.vocab ? (float)row[i] : kMinusInf;
+                    top.add(y > kMinusInf ? key_of(y, i) : 0);
+                }
+            }
+            if (top.n >= 2 * top.want) top.rank();  // (a higher bar spares more groups than it costs)
         }
     }
-    if constexpr (TOP) top.rank();
 
     // the lanes, then the waves
     const float m_wave = wave_max(most);
-    s.to(m_wave, c);
+    s.move(m_wave, (float)(level_of() - (double)m_wave * (double)c));
     const float l_wave = wave_add(s.l), t_wave = wave_add(s.t);
     if (lane == 0) sums[wave][0] = m_wave, sums[wave][1] = l_wave, sums[wave][2] = t_wave, counts[wave] = top.n;
     __syncthreads();
@@ -211,7 +312,7 @@ __global__ __launch_bounds__(kLogprobThreads) void logprobs_kernel(LogprobArgs a
         all.t += y.t;
     }
     if constexpr (TOP) {
-#pragma unroll
+#pragma unroll 1
         for (int w = 1; w < kWavesLp; ++w) top.add(lane < counts[w] ? places[w][lane] : 0);
         top.rank();
         lds_of_wave_settled();
@@ -247,8 +348,10 @@ __global__ __launch_bounds__(64) void logprobs_join_kernel(LogprobArgs a) {
     WaveTop top(places, a.n_top);
     if constexpr (TOP) {
         const int total = a.parts * a.n_top;
+        // the best of every part first, so that the bar is soon high
         for (int i = lane; i - lane < total; i += 64) {
-            top.add(i < total ? a.tops[(int64_t)t * total + i] : 0);
+            const int place = i / a.parts, part = i - place * a.parts;
+            top.add(i < total ? a.tops[((int64_t)t * a.parts + part) * a.n_top + place] : 0);
         }
         top.rank();
         lds_of_wave_settled();

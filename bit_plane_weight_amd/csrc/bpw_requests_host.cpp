@@ -298,7 +298,7 @@ constexpr int64_t kLogprobWgs = 1024;  // workgroups that fill the GPU: four to 
 
 // Workgroups of a row and rounds of each: rows are cut where there are too few to fill the GPU.
 void logprob_parts(int32_t n_tokens, int32_t vocab, int32_t *parts, int32_t *rounds) {
-    const int32_t all = (int32_t)(((int64_t)vocab + 7 + bpw::kLogprobRound - 1) / bpw::kLogprobRound);  // (7: a row's first entries lie past a border)
+    const int32_t all = (vocab + bpw::kLogprobRound - 1) / bpw::kLogprobRound;
     const int64_t want = n_tokens >= kLogprobWgs ? 1 : (kLogprobWgs + n_tokens - 1) / n_tokens;
     *rounds = (int32_t)((all + want - 1) / want);
     *parts = (all + *rounds - 1) / *rounds;
