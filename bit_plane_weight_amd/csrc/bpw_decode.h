@@ -199,6 +199,7 @@ struct Kv4AppendArgs {
     int32_t vec;             // rows are read and written 16 bytes at a time
     int32_t first_wg;        // of this launch
     float eps;
+    double inv_head_dim;
 };
 int launch_kv4_append(const Kv4AppendArgs &a, int32_t dt_in, int32_t dt_out, void *stream);
 

@@ -161,6 +161,7 @@ bpw_status bpw_kv4_append(const bpw_kv4_append_args *a, void *stream) {
     for (const bpw_heads *x : all)
         if (x->heads && !wide(x->d, x->dtype, x->token_stride, x->head_stride, 0)) h.vec = 0;
     h.eps = a->eps;
+    h.inv_head_dim = 1.0 / c.head_dim;
     return hip_status(bpw::launch_kv4_append(h, a->k.dtype, dt_out, stream), "kv4 append launch");
 }
 
