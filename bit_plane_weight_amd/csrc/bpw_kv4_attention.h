@@ -142,11 +142,6 @@ __device__ __forceinline__ void attend4(const Attn4Args &b, const AttnSpan &s, u
             if (row < s.n_rows && d0 < D) x = *reinterpret_cast<const u32v4 *>(p + d0);
             split8(x, q[c], T());
         }
-        // waited for here, not in the loop, where a wait for them would be one for all loads to LDS
-#pragma unroll
-        for (int c = 0; c < KC; ++c)
-#pragma unroll
-            for (int x = 0; x < QP; ++x) asm volatile("" : "+v"(q[c][x]));
     }
     const int all_see = s.causal ? s.len - (s.n_tok - 1) : s.len;
 
@@ -349,6 +344,11 @@ __device__ __forceinline__ void attend4(const Attn4Args &b, const AttnSpan &s, u
     x.k32 = 32 * b.kc.rs, x.v32 = 32 * b.vc.rs, x.ks32 = 32 * b.kc.s_rs, x.vs32 = 32 * b.vc.s_rs;
     asm volatile("" : "+s"(x.k32), "+s"(x.v32), "+s"(x.ks32), "+s"(x.vs32));
     x.pages.fetch(a, s, kv0 >> a.page_log2);
+    // The queries are waited for with the pages, not in the loop, where a wait for them would be one for all loads to LDS.
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+        for (int i = 0; i < QP; ++i) asm volatile("" : "+v"(q[c][i]));
     uint32_t at = 0;
 #pragma unroll 1
     for (int i = 0; i < STEPS; ++i, next += kAttnStep, at += Ring::STEP) {

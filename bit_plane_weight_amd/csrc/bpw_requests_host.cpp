@@ -176,10 +176,15 @@ struct Attn4Shape {
     size_t po, pml, total;  // workspace: offsets of the parts, all
 };
 
-// As for the 16-bit cache: most positions (x padded head size) of a row of the page table for one launch, and most of all its
-// workgroups' steps (x padded head size).
-constexpr int64_t kShort4Work = 65536;
-constexpr int64_t kShort4Steps = 1 << 21;
+// One launch, a workgroup to an item (sequence, key/value head, 16 query rows), up to so many positions of a row of the page table
+// (x padded head size), more of them where the items alone fill half the CUs; otherwise even runs of positions and a join,
+// which take some 12 us at least. Heads of 128, 8 key/value heads, one sequence: 10.2 us in one launch against 11.9 at 1024 positions,
+// 14.9 against 12.7 at 2048; 64 sequences: 22.0 against 24.2, 33.7 against 35.6. Heads of 64, 64 sequences of 4096: 33 against 45,
+// one: 20 against 14. Heads of 256, 4 key/value heads: one sequence of 512 11.9 against 13.0, of 1024 17.1 against 12.9.
+constexpr int64_t kShort4Work = 163840, kShort4WorkFull = 262144;
+constexpr int64_t kShort4Items = 128;
+// And most of all its workgroups' steps (x padded head size), past which uneven lengths weigh more than the launch.
+constexpr int64_t kShort4Steps = 1 << 22;
 
 bpw_status attn4_shape(const bpw_kv4_attn_args *a, Attn4Shape *s) {
     const char *who = "kv4 attention";
@@ -206,7 +211,7 @@ bpw_status attn4_shape(const bpw_kv4_attn_args *a, Attn4Shape *s) {
         return fail(BPW_E_UNSUPPORTED, "%s: more work than one launch deals out", who);
     const int64_t most = items * units;
     s->n_wgs = (int32_t)(most < 2 ? 2 : most < bpw::kAttnWgs ? most : bpw::kAttnWgs);
-    s->one_launch = s->cap * s->dp <= kShort4Work && most * s->dp <= kShort4Steps;
+    s->one_launch = s->cap * s->dp <= (items >= kShort4Items ? kShort4WorkFull : kShort4Work) && most * s->dp <= kShort4Steps;
     const size_t rows = units > 0 ? (size_t)(items + (int64_t)bpw::kAttnWaves * s->n_wgs) * 16 : 0;  // a part per item and per run
     s->po = up256((size_t)(bpw::kSchedHead + 2 * (a->n_seqs + 1)) * 4);
     s->pml = s->po + up256(rows * (size_t)s->dp * 4);
