@@ -726,3 +726,14 @@ def test_logprobs_rows_of_any_alignment_in_a_graph(dev):
     bpw.bpw_token_logprobs(view, None, None, ws, entropy=ent)
     torch.cuda.synchronize()
     assert torch.allclose(ent, want[1], rtol=0, atol=1e-5)
+
+
+def test_answer_requests_example(dev):
+    """The operators together, from packed prompts to scored answers, the steps in a graph."""
+    import importlib.util
+    import os
+    from conftest import ROOT
+    spec = importlib.util.spec_from_file_location("answer_requests", os.path.join(ROOT, "examples", "answer_requests.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.main(["--requests", "5", "--longest", "150", "--answer", "4", "--check"])
