@@ -7,8 +7,9 @@
 // key lies on is decided after norm and rotation; these are held in float64, as in float32 one element in some 10^6 would
 // get the neighbouring code, a whole step away.
 //
-// Bound: HBM for prompts (8192 tokens of 32 + 8 + 8 heads of 128 in bfloat16: 52 us, 4.0 TB/s of reads and writes), the launch for
-// a decode step (64 tokens: 6.3 us). The wave's work is one head set's at a time, so that what differs between them is in
+// Bound: HBM for prompts (8192 tokens of 32 + 8 + 8 heads of 128 in bfloat16, 210 MB read and written: 58-60 us over memory that no
+// cache holds, 3.6 TB/s; 65 with one item on its way beside the one worked on, not two), the launch for a decode step (64
+// tokens: 6.1 us). The wave's work is one head set's at a time, so that what differs between them is in
 // scalar registers (93 us when lanes of a wave chose); sines and cosines are formed once for all heads of a token; a lane
 // holds eight neighbours of a head, a block is four lanes, its largest element two DPP steps away, and its 32 codes four
 // words of 32 bits, from the conversion instruction. Partners of a rotation go through LDS, 16 bytes of each lane beside
@@ -245,10 +246,17 @@ __global__ __launch_bounds__(kAppendThreads, 4) void kv4_append_kernel(Kv4Append
         if (gain) x = *reinterpret_cast<const f32x8u *>(gain + (in ? i0 : 0));
         return x;
     };
-    Item next;
-    settle();
-    if (token < tokens) load(next);
-    const f32x8 q_gain = gains(a.q.gain), k_gain = gains(a.k.gain);
+    // Two items are on their way while one is worked on.
+    Item next[2];
+    const auto advance = [&](Item &x) {
+        settle();
+        x.token = -1;
+        if (token < tokens) load(x);
+        item += kAppendThreads / 64;
+    };
+    advance(next[0]);
+    advance(next[1]);
+    const f32x8 q_gain = gains(a.q.gain);
     for (int i = threadIdx.x; i < TOKENS * half; i += kAppendThreads) {
         const int u = TOKENS == 1 ? 0 : i / half;
         double x = (double)a.positions[min(t0 + u, (int64_t)a.n_tokens - 1)] * a.inv_freq[i - u * half] * 0.15915494309189533577;  // turns
@@ -260,11 +268,7 @@ __global__ __launch_bounds__(kAppendThreads, 4) void kv4_append_kernel(Kv4Append
         qc[f] = (float)cos, qs[f] = (float)sin;
     }
     __syncthreads();
-    while (token < tokens) {
-        const Item x = next;
-        item += kAppendThreads / 64;
-        settle();
-        if (token < tokens) load(next);
+    const auto work = [&](const Item &x) __attribute__((always_inline)) {
         const HeadSet &s = x.set == 0 ? a.q : x.set == 1 ? a.k : a.v;
         TO *out = static_cast<TO *>(s.out);
         const bool has_out = out, valid = in && x.head < s.heads;
@@ -274,7 +278,7 @@ __global__ __launch_bounds__(kAppendThreads, 4) void kv4_append_kernel(Kv4Append
             double y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = in ? (double)(float)x.raw[e] : 0.0;
-            if (a.k.gain) norm(a, y, k_gain);
+            if (a.k.gain) norm(a, y, gains(a.k.gain));
             if (half) turn<double, CHUNKS>(a, y, i0, kc + x.token * half, ks + x.token * half, rows, chunk0);
             codes = quantise(y, power);
         } else {
@@ -285,11 +289,11 @@ __global__ __launch_bounds__(kAppendThreads, 4) void kv4_append_kernel(Kv4Append
                 if (a.q.gain) norm(a, y, q_gain);
                 if (half) turn<float, CHUNKS>(a, y, i0, qc + x.token * half, qs + x.token * half, reinterpret_cast<float *>(rows), chunk0);
                 if (valid) put_eight(out, f32x8{y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]}, a.vec);
-                continue;
+                return;
             }
             codes = quantise(y, power);
         }
-        if (!valid) continue;
+        if (!valid) return;
         if (x.slot >= 0 && x.slot < a.n_slots) {
             const Kv4Rows &r = x.set == 1 ? a.kc : a.vc;
             const int64_t page = x.slot >> a.page_log2, at = x.slot - (page << a.page_log2);
@@ -297,6 +301,15 @@ __global__ __launch_bounds__(kAppendThreads, 4) void kv4_append_kernel(Kv4Append
             if ((c & 3) == 0) r.scales[page * r.s_ps + at * r.s_rs + x.head * r.s_hs + (c >> 2)] = (uint8_t)power;
         }
         if (has_out) put_eight(out, stands_for(codes, power), a.vec);
+    };
+    while (next[0].token >= 0) {
+        Item x = next[0];
+        advance(next[0]);
+        work(x);
+        if (next[1].token < 0) break;
+        x = next[1];
+        advance(next[1]);
+        work(x);
     }
 }
 
