@@ -14,8 +14,8 @@
 // fill each other's gaps; with 64 rows a wave and one workgroup LDS is read half as often, and long prompts ran as fast,
 // all others slower. Tiles on the diagonal, whose hidden positions cost registers that the pipeline needs, come last, without it.
 // Measured (causal half counted): 16384 tokens of 32 / 8 heads of 128 1.91-2.04 ms, 1.08-1.15 PFLOP/s, against 3.33 ms product by
-// product; 2048 tokens of 20 / 5 heads 40 us; 4096 tokens of 16 / 4 heads of 256 150 us. LDS reads take as many
-// cycles as the products, and the clock under both falls to 1.7-2.0 GHz, which is what bounds long prompts now.
+// product; 2048 tokens of 20 / 5 heads 40 us; 4096 tokens of 16 / 4 heads of 256 150 us. The matrix cores are busy two
+// thirds of the time at the clock that this load sustains (1.6 to 2.0 GHz), which is what bounds long prompts now.
 // Tiles with the most positions start first. The key/value heads are dealt round the XCDs, so that with eight of them each
 // XCD's L2 holds one.
 #pragma once
