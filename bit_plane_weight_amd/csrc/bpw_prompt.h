@@ -110,7 +110,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void prompt_kernel(PromptAr
     constexpr int KT = 64, M = 128 / PARTS, NB = 2 / PARTS;  // positions and rows of a tile, blocks of 32 positions of a wave
     constexpr int ROW = DP * 2, CPR = DP / 8, RPI = 64 / CPR;  // row bytes, chunks of a row, rows of one load
     constexpr int KC = DP / 16, DB = DP / 32, TILE = KT * ROW;  // bytes of a tile of keys or values
-    __shared__ __attribute__((aligned(4096))) uint8_t lds[4 * TILE];  // keys twice, values twice
+    __shared__ __attribute__((aligned(2 * TILE))) uint8_t lds[4 * TILE];  // keys twice, values twice (a buffer is chosen by an exclusive-or)
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, g = lane >> 5, part = PARTS == 2 ? wave >> 1 : 0, rows_of = PARTS == 2 ? wave & 1 : wave;
     const int D = a.head_dim;

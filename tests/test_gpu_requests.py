@@ -109,6 +109,30 @@ def test_prompt_long_against_blocks(dev):
         a += n
 
 
+@pytest.mark.parametrize("counts,Hq,Hk,D,dt", [
+    ([900, 300, 120], 16, 2, 128, F16),
+    ([63, 1, 800, 0, 470], 16, 16, 96, BF16),
+    ([700, 333, 1, 290], 16, 4, 256, BF16),
+    ([450, 860], 16, 8, 200, F16),
+    ([64] * 33, 32, 8, 64, BF16),
+    ([1500, 600], 32, 4, 64, F16),
+])
+def test_prompt_many_rows(dev, counts, Hq, Hk, D, dt):
+    """Rows enough for workgroups of 128 of them and the pipeline: as it is, with scores that rise, with values and keys of NaN
+    and infinity that some rows of a tile see."""
+    p = Prompt(dev, counts, Hq, Hk, D, dt, seed=D, layout="fused", before=2, behind=1)
+    p.run()
+    p.check("as it is")
+    longest = 2 + sum(counts[:counts.index(max(counts))])
+    p.k[longest:longest + max(counts)] *= torch.linspace(0.1, 4, max(counts), device=dev).to(dt)[:, None, None]
+    p.run()
+    p.check("rising")
+    for at, n, what in ((max(counts) // 2, float("inf"), p.v), (max(counts) - 2, float("nan"), p.v), (max(counts) - 9, float("nan"), p.k)):
+        what[longest + at, 0] = n
+    p.run()
+    p.check("not finite")
+
+
 def test_prompt_many_sequences(dev):
     """More sequences than two rounds of probes tell apart, most of one token or none."""
     counts = [i % 7 % 3 for i in range(5000)]
