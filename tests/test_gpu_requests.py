@@ -340,6 +340,18 @@ def test_append4(dev, T, Hq, Hk, D, R, P, adjacent, src, dst, gains, layout):
     run_append(dev, T, Hq, Hk, D, R, P, adjacent, src, dst, gains, layout, seed=T * 31 + D)
 
 
+@pytest.mark.parametrize("T,Hq,Hk,D,R,P,adjacent,src,dst,gains,layout", [
+    (2049, 3, 2, 64, 64, 64, False, BF16, BF16, True, "hnd"),
+    (2200, 0, 1, 128, 64, 16, True, F32, F16, True, "nhd"),
+    (2048, 5, 1, 96, 96, 32, False, F16, F16, False, "odd"),
+    (2050, 2, 1, 256, 256, 64, False, F32, BF16, True, "hnd"),
+    (2051, 9, 1, 32, 18, 16, False, BF16, F16, True, "together"),
+])
+def test_append4_of_a_prompt(dev, T, Hq, Hk, D, R, P, adjacent, src, dst, gains, layout):
+    """Tokens enough for a workgroup to take two of them, the last one alone."""
+    run_append(dev, T, Hq, Hk, D, R, P, adjacent, src, dst, gains, layout, seed=T)
+
+
 @pytest.mark.parametrize("src", [F32, BF16, F16])
 def test_append4_borders_and_extremes(dev, src):
     """Every border of two codes and its neighbours at several powers, blocks of zeros, of the smallest and largest numbers, with
@@ -516,6 +528,26 @@ def test_attention4_paths(dev, path, dt):
     a.run("a value of NaN")
     a.len_t[0] = P + 3
     a.run("and it is not seen")
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("layout", ["nhd", "together", "odd"])
+@pytest.mark.parametrize("path", ATTENTION4_PATHS)
+def test_attention4_paths_of_any_strides(dev, path, layout, dt):
+    """Rows of powers apart from one another, or one after another from an odd address: read byte by byte."""
+    n_q, lens, Hq, Hk, D, P, pages = ATTENTION4_PATHS[path]
+    a = Attn4(dev, n_q, lens, Hq, Hk, D, P, dt, seed=61, max_pages=pages, layout="hnd" if layout == "odd" else layout)
+    if layout == "odd":
+        for i in (2, 3):
+            buf = torch.zeros(a.cache[i].numel() + 1, dtype=U8, device=dev)
+            buf[1:] = a.cache[i].flatten()
+            a.cache[i] = buf[1:].view(a.cache[i].shape)
+    a.run("as it is")
+    a.table[0, 0] = -1
+    a.run("a page is missing")
+    a.table[0, 0] = a.table[0, 1].item()
+    a.cache[3][a.table[0, 1].long(), 0, 3, -1] = 255
+    a.run("a value of NaN")
 
 
 @pytest.mark.parametrize("Hq,Hk,D,n,dt", [(3, 1, 64, 5, BF16), (8, 2, 128, 3, F16), (12, 2, 96, 7, BF16), (4, 4, 256, 9, F16)])
