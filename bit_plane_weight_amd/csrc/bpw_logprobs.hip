@@ -176,7 +176,7 @@ __global__ __launch_bounds__(kLogprobThreads, sizeof(T) == 2 ? 5 : 4) void logpr
 
     WaveTop top(places[wave], a.n_top);
     // The shift of a wave's lanes is one, `level` in units of log 2: the product m c rounded, so that an exponent is one fma, or,
-    // where that nears the largest float, the product itself (far).
+    // from 2^20 on, where the rounding is no longer small beside 1, the product itself (far).
     LaneSums s{kLowest, 0.0f, 0.0f};
     float most = kLowest, limit = kLowest, level = 0.0f;  // the largest logit; what raises the shift
     bool far = true;
@@ -229,7 +229,7 @@ __global__ __launch_bounds__(kLogprobThreads, sizeof(T) == 2 ? 5 : 4) void logpr
             const double old = level_of();
             limit = up + kLazy / c;
             level = up * c;
-            far = !(fabsf(level) < 1e30f);
+            far = !(fabsf(level) < 0x1p20f);
             s.m = up;
             s.move(up, (float)(old - level_of()));
         }

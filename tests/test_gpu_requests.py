@@ -756,6 +756,15 @@ def test_logprobs_nearly_certain(dev):
     assert np.all(np.abs(f64(lp) - want[0]) <= 4 * U) and np.all(np.abs(f64(ent) - want[1]) <= 4 * U + 1e-3 * want[1])
 
 
+@pytest.mark.parametrize("offset", [1e4, -3e4, 1e6, 1e9, -1e20, 1e29])
+def test_logprobs_far_from_zero(dev, offset):
+    """Logits that share a large offset: only their differences count."""
+    g = torch.Generator().manual_seed(17)
+    x = torch.randn(3, 20001, generator=g) * 3 + offset
+    for T in (1, 400):
+        run_logprobs(dev, x.repeat(T, 1), torch.tensor([5, 17, 20000]).int().repeat(T), 4, 1.25)
+
+
 def test_logprobs_rows_of_any_alignment_in_a_graph(dev):
     """Rows inside wider ones, at addresses no vector is aligned to; captured once, contents changed between replays; no tokens."""
     T, V, K = 5, 5003, 6
