@@ -105,11 +105,12 @@ typedef __attribute__((address_space(3))) const u32x2 lds_u32x2;
 
 // A workgroup of four waves takes 128 / PARTS query rows, 32 a wave, and 64 positions at a time; with two PARTS the waves of part
 // p take the p-th 32 of them, and part 1's results are joined with part 0's at the end.
-template <class T, int DP, int PARTS, bool PIPE, bool LSE>
+// Rows in LDS are of DP elements; products are formed of the first DU, a multiple of 32.
+template <class T, int DP, int DU, int PARTS, bool PIPE, bool LSE>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void prompt_kernel(PromptArgs a) {
     constexpr int KT = 64, M = 128 / PARTS, NB = 2 / PARTS;  // positions and rows of a tile, blocks of 32 positions of a wave
     constexpr int ROW = DP * 2, CPR = DP / 8, RPI = 64 / CPR;  // row bytes, chunks of a row, rows of one load
-    constexpr int KC = DP / 16, DB = DP / 32, TILE = KT * ROW;  // bytes of a tile of keys or values
+    constexpr int KC = DU / 16, DB = DU / 32, TILE = KT * ROW;  // bytes of a tile of keys or values
     __shared__ __attribute__((aligned(2 * TILE))) uint8_t lds[4 * TILE];  // keys twice, values twice (a buffer is chosen by an exclusive-or)
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, g = lane >> 5, part = PARTS == 2 ? wave >> 1 : 0, rows_of = PARTS == 2 ? wave & 1 : wave;
@@ -421,7 +422,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void prompt_kernel(PromptAr
     lr += __shfl_xor(lr, 32);
     m = stored_shift(m, lr);
     if constexpr (PARTS == 2) {  // part 1 hands over through LDS
-        constexpr int PAD = DP + 4;
+        constexpr int PAD = DU + 4;
         static_assert(M * (PAD + 4) * 4 <= sizeof lds, "the join fits the tiles' LDS");
         float *box = reinterpret_cast<float *>(lds) + (32 * rows_of + n) * PAD;
         float4 *ml = reinterpret_cast<float4 *>(reinterpret_cast<float *>(lds) + M * PAD) + 32 * rows_of + n;
@@ -467,7 +468,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void prompt_kernel(PromptAr
     if (LSE && g == 0) a.lse[(int64_t)(t0 + token) * a.q_heads + hq] = (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
 }
 
-template <class T, int DP, int PARTS, bool PIPE>
+template <class T, int DP, int DU, int PARTS, bool PIPE>
 static int run_prompt_parts(PromptArgs a, hipStream_t s) {
     a.slots = prompt_slot(a.n_tokens * a.group, a.n_seqs, 128 / PARTS);
     const int64_t wgs = (int64_t)a.slots * a.kv_heads;
@@ -476,17 +477,25 @@ static int run_prompt_parts(PromptArgs a, hipStream_t s) {
         const int64_t left = wgs - a.first_wg;
         const unsigned grid = (unsigned)(left < kMaxWgs ? left : kMaxWgs);
         if (a.lse)
-            prompt_kernel<T, DP, PARTS, PIPE, true><<<grid, 256, 0, s>>>(a);
+            prompt_kernel<T, DP, DU, PARTS, PIPE, true><<<grid, 256, 0, s>>>(a);
         else
-            prompt_kernel<T, DP, PARTS, PIPE, false><<<grid, 256, 0, s>>>(a);
+            prompt_kernel<T, DP, DU, PARTS, PIPE, false><<<grid, 256, 0, s>>>(a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || left <= kMaxWgs) return (int)e;
     }
 }
 
+template <class T, int DP, int DU>
+static int run_prompt_of(const PromptArgs &a, bool many, hipStream_t s) {
+    return many ? run_prompt_parts<T, DP, DU, 1, true>(a, s) : run_prompt_parts<T, DP, DU, 2, false>(a, s);
+}
+// Heads of up to three quarters of DP leave out the last quarter of the products (4096 tokens of 32 / 8 heads of 96: 124 us, 141 with
+// all of them; of 16 / 4 heads of 192 136, 160).
 template <class T, int DP>
 static int run_prompt(const PromptArgs &a, bool many, hipStream_t s) {
-    return many ? run_prompt_parts<T, DP, 1, true>(a, s) : run_prompt_parts<T, DP, 2, false>(a, s);
+    if constexpr (DP > 64)
+        if (a.head_dim <= DP * 3 / 4) return run_prompt_of<T, DP, DP * 3 / 4>(a, many, s);
+    return run_prompt_of<T, DP, DP>(a, many, s);
 }
 
 #undef BPW_INLINE
