@@ -150,31 +150,44 @@ __device__ __forceinline__ void attend4(const Attn4Args &b, const AttnSpan &s, u
     // lane's operands are neighbours there and the banks are shared evenly. Blocks past head_dim are the first one again.
     using Ring = Ring4<DP, DENSE>;
     constexpr int BLOCKS = Ring::BLOCKS, LOADS = Ring::LOADS, STEPS = Ring::STEPS, ALL = Ring::ALL;
-    // Load j of a step: where its part of the step begins in LDS, from the base that m0 has for it; its offset in this lane from the
-    // first row of its tile. Lanes of one load may be of two tiles (two), and, with DENSE, of keys and values.
+    // Load j of a step: where its part of the step begins in LDS, from the base that m0 has for it; its address in this lane for
+    // page 0 and the page's first rows. Lanes of one load may be of two tiles, and, with DENSE, of keys and values.
     constexpr auto lds_at = [](int j) { return j < 2 * LOADS ? 1024 * (j % 4) : (Ring::POWERS > 2048 ? 0 : Ring::POWERS) + 256 * (j - 2 * LOADS); };
-    int32_t off[ALL];
+    constexpr auto tile_of = [](int j, int lane) {
+        const int i = j < 2 * LOADS ? j : j - 2 * LOADS;
+        if (DENSE && j >= 2 * LOADS) return (lane & (DP == 256 ? 32 : 16)) != 0;
+        return LOADS == 1 ? lane >= 32 : LOADS == 2 ? (i & 1) != 0 : (i & 2) != 0;
+    };
+    constexpr auto values_of = [](int j, int lane) {
+        if (DENSE && j >= 2 * LOADS) return DP == 256 ? j > 2 * LOADS : (lane & 32) != 0;
+        return (j / LOADS & 1) != 0;
+    };
+    const bool own_pages = pmask == 15;  // tiles of 16 positions have pages of their own; otherwise a step is on one page
+    const uint8_t *lane_base[ALL];
 #pragma unroll
     for (int j = 0; j < ALL; ++j) {
+        int32_t off;
         const bool codes = j < 2 * LOADS;
         const int i = codes ? j : j - 2 * LOADS, x = (LOADS == 4 ? 64 * (i & 1) : 0) + lane, used = D / kKv4Block;
+        const bool values = values_of(j, lane);
         if (DENSE && !codes) {
-            off[j] = 4 * (lane & (DP == 256 ? 31 : 15));  // (DP 64: a tile has eight words, and the rest is not read)
-            if (DP == 64) off[j] &= 31;
+            off = 4 * (lane & (DP == 256 ? 31 : 15));  // (DP 64: a tile has eight words, and the rest is not read)
+            if (DP == 64) off &= 31;
         } else if (i < LOADS) {
             const int block = (x >> 4) % BLOCKS < used ? (x >> 4) % BLOCKS : 0;
-            off[j] = codes ? (x & 15) * b.kc.rs + 16 * block : (x & 15) * b.kc.s_rs + block;
+            off = codes ? (x & 15) * b.kc.rs + 16 * block : (x & 15) * b.kc.s_rs + block;
         } else if (codes) {
             const int block = x % BLOCKS < used ? x % BLOCKS : 0, r = (x / BLOCKS) & 15;
-            off[j] = (4 * (r & 3) + (r >> 2)) * b.vc.rs + 16 * block;
+            off = (4 * (r & 3) + (r >> 2)) * b.vc.rs + 16 * block;
         } else {
             const int block = (x >> 2) % BLOCKS < used ? (x >> 2) % BLOCKS : 0;
-            off[j] = (4 * (x / (4 * BLOCKS) & 3) + (x & 3)) * b.vc.s_rs + block;
+            off = (4 * (x / (4 * BLOCKS) & 3) + (x & 3)) * b.vc.s_rs + block;
         }
-        off[j] -= lds_at(j);
+        const uint8_t *base = codes ? (values ? b.vc.codes : b.kc.codes) : values ? b.vc.scales : b.kc.scales;
+        const int64_t hs = codes ? (values ? b.vc.hs : b.kc.hs) : values ? b.vc.s_hs : b.kc.s_hs;
+        const int32_t rs = codes ? (values ? b.vc.rs : b.kc.rs) : values ? b.vc.s_rs : b.kc.s_rs;
+        lane_base[j] = base + (s.head * hs + off + (tile_of(j, lane) && !own_pages ? 16 * rs : 0) - lds_at(j));
     }
-    const uint8_t *kbase = b.kc.codes + (int64_t)s.head * b.kc.hs, *ksbase = b.kc.scales + (int64_t)s.head * b.kc.s_hs;
-    const uint8_t *vbase = b.vc.codes + (int64_t)s.head * b.vc.hs, *vsbase = b.vc.scales + (int64_t)s.head * b.vc.s_hs;
     // this lane's reads
     const uint32_t kr = ring + (DP == 64 ? 256 * (g >> 1) + 16 * n + 8 * (g & 1) : (DP == 128 ? 256 : 512) * g + 16 * n);
     const uint32_t vr = ring + Ring::VALUES + DP / 2 * g + EL / 2 * n;
@@ -202,45 +215,24 @@ __device__ __forceinline__ void attend4(const Attn4Args &b, const AttnSpan &s, u
         uint32_t bad, none;  // tiles that no page holds: two bits a step on its way; the last ones
     };
     const auto place = [&](Issued &x, int pos, int id0, int id1) __attribute__((always_inline)) {
-        const uint8_t *k[2], *v[2], *ks[2], *vs[2];
         x.none = (id0 < 0 ? 1 : 0) | (id1 < 0 ? 2 : 0);
         const int64_t page = max(id0, 0), row = pos & pmask;  // (a tile without a page takes page 0's)
-        k[0] = kbase + page * b.kc.ps + row * b.kc.rs;
-        v[0] = vbase + page * b.vc.ps + row * b.vc.rs;
-        ks[0] = ksbase + page * b.kc.s_ps + row * b.kc.s_rs;
-        vs[0] = vsbase + page * b.vc.s_ps + row * b.vc.s_rs;
-        if (pmask > 15) {
-            k[1] = k[0] + 16 * b.kc.rs;
-            v[1] = v[0] + 16 * b.vc.rs;
-            ks[1] = ks[0] + 16 * b.kc.s_rs;
-            vs[1] = vs[0] + 16 * b.vc.s_rs;
-        } else {
-            const int64_t second = max(id1, 0);
-            k[1] = kbase + second * b.kc.ps;
-            v[1] = vbase + second * b.vc.ps;
-            ks[1] = ksbase + second * b.kc.s_ps;
-            vs[1] = vsbase + second * b.vc.s_ps;
-        }
+        const int64_t k = page * b.kc.ps + row * b.kc.rs, v = page * b.vc.ps + row * b.vc.rs;
+        const int64_t ks = page * b.kc.s_ps + row * b.kc.s_rs, vs = page * b.vc.s_ps + row * b.vc.s_rs;
 #pragma unroll
-        for (int j = 0; j < ALL; ++j) {
-            const bool codes = j < 2 * LOADS;
-            const int i = codes ? j : j - 2 * LOADS;
-            if (DENSE && !codes) {
-                const bool second = DP == 256 ? lane & 32 : lane & 16, values = DP == 256 ? i == 1 : lane & 32;
-                const uint8_t *kp = second ? ks[1] : ks[0], *vp = second ? vs[1] : vs[0];
-                x.p[j] = (values ? vp : kp) + off[j];
-            } else {
-                const bool second = LOADS == 1 ? lane >= 32 : LOADS == 2 ? i & 1 : i & 2;
-                if (i < LOADS)
-                    x.p[j] = (codes ? (second ? k[1] : k[0]) : (second ? ks[1] : ks[0])) + off[j];
-                else
-                    x.p[j] = (codes ? (second ? v[1] : v[0]) : (second ? vs[1] : vs[0])) + off[j];
+        for (int j = 0; j < ALL; ++j) x.p[j] = lane_base[j] + (j < 2 * LOADS ? (values_of(j, lane) ? v : k) : values_of(j, lane) ? vs : ks);
+        if (own_pages) {
+            const int64_t more = max(id1, 0) - page;
+#pragma unroll
+            for (int j = 0; j < ALL; ++j) {
+                const int64_t ps = j < 2 * LOADS ? (values_of(j, lane) ? b.vc.ps : b.kc.ps) : values_of(j, lane) ? b.vc.s_ps : b.kc.s_ps;
+                x.p[j] += tile_of(j, lane) ? more * ps : 0;
             }
         }
     };
     // Starts the loads of the step at `pos`; steps come in order.
     const auto issue = [&](Issued &x, int pos, uint32_t at) __attribute__((always_inline)) {
-        if (pmask == 15) {
+        if (own_pages) {
             const int id = x.pages.of(a, s, pos >> 4);
             place(x, pos, id, x.pages.of(a, s, (pos >> 4) + 1));
         } else if (pos == s.pos0 || (pos & pmask) == 0) {
