@@ -13,8 +13,8 @@
 //
 // Codes and powers go through LDS, moved there by the loads themselves some steps of 32 positions ahead, in an order that makes a
 // lane's operands neighbours (Ring4): with loads to registers a step of heads of 128 took 20 loads of 1 to 16 bytes a lane
-// and waited for all of them (8 sequences of 57000 positions, 8 heads: 125 us; this way 5 loads, 99 us). Bound there: the
-// vector units issue two thirds of the time (64 conversions, 32 v_perm, 24 for the weights' two parts of 215 in a step)
+// and waited for all of them (8 sequences of 57000 positions, 8 heads: 125 us; this way 5 loads, 90-93 us). Bound there: the
+// vector units issue half of the time (64 conversions, 32 v_perm, 24 for the weights' two parts of 215 in a step)
 // beside loads that alone take 84 us.
 #pragma once
 
@@ -23,8 +23,6 @@
 #include "bpw_attention.h"
 
 namespace bpw {
-
-constexpr uint32_t kPlainUnit = 0x3F800000u;  // 2^0, for positions whose weight is zero
 
 template <class T>
 constexpr int kQueryPieces = __is_same(T, __bf16) ? 1 : 2;
@@ -59,7 +57,7 @@ template <int DP, bool DENSE>
 struct Ring4 {
     static constexpr int BLOCKS = DP / kKv4Block;       // of a row
     static constexpr int LOADS = 32 * BLOCKS / 64;      // of a step's codes of keys (or values)
-    static constexpr int KEYS = 0, VALUES = 1024 * LOADS, POWERS = 2 * VALUES;
+    static constexpr int VALUES = 1024 * LOADS, POWERS = 2 * VALUES;
     static constexpr int POWER_LOADS = DENSE ? (DP == 256 ? 2 : 1) : 2 * LOADS;
     static constexpr int ALL = 2 * LOADS + POWER_LOADS, STEP = POWERS + 256 * POWER_LOADS;
     // Steps: 70 to 140 KB of a CU's LDS for two workgroups of four waves.
