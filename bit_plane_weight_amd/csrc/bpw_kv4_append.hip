@@ -8,7 +8,8 @@
 // get the neighbouring code, a whole step away.
 //
 // Bound: HBM for prompts (8192 tokens of 32 + 8 + 8 heads of 128 in bfloat16, 210 MB read and written: 58-60 us over memory that no
-// cache holds, 3.6 TB/s; 65 with one item on its way beside the one worked on, not two), the launch for a decode step (64
+// cache holds, 3.6 TB/s; three items are on their way beside the one worked on, with two 63 us, with four or five
+// 58-60), while the vector units issue half of the time; the launch for a decode step (64
 // tokens: 6.1 us). The wave's work is one head set's at a time, so that what differs between them is in
 // scalar registers (93 us when lanes of a wave chose); sines and cosines are formed once for all heads of a token; a lane
 // holds eight neighbours of a head, a block is four lanes, its largest element two DPP steps away, and its 32 codes four
@@ -246,16 +247,16 @@ __global__ __launch_bounds__(kAppendThreads, 4) void kv4_append_kernel(Kv4Append
         if (gain) x = *reinterpret_cast<const f32x8u *>(gain + (in ? i0 : 0));
         return x;
     };
-    // Two items are on their way while one is worked on.
-    Item next[2];
+    constexpr int AHEAD = 3;
+    Item next[AHEAD];
     const auto advance = [&](Item &x) {
         settle();
         x.token = -1;
         if (token < tokens) load(x);
         item += kAppendThreads / 64;
     };
-    advance(next[0]);
-    advance(next[1]);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) advance(next[i]);
     const f32x8 q_gain = gains(a.q.gain);
     for (int i = threadIdx.x; i < TOKENS * half; i += kAppendThreads) {
         const int u = TOKENS == 1 ? 0 : i / half;
@@ -302,14 +303,14 @@ __global__ __launch_bounds__(kAppendThreads, 4) void kv4_append_kernel(Kv4Append
         }
         if (has_out) put_eight(out, stands_for(codes, power), a.vec);
     };
-    while (next[0].token >= 0) {
-        Item x = next[0];
-        advance(next[0]);
-        work(x);
-        if (next[1].token < 0) break;
-        x = next[1];
-        advance(next[1]);
-        work(x);
+    while (true) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (next[i].token < 0) return;
+            const Item x = next[i];
+            advance(next[i]);
+            work(x);
+        }
     }
 }
 
