@@ -211,7 +211,9 @@ bpw_status attn4_shape(const bpw_kv4_attn_args *a, Attn4Shape *s) {
         return fail(BPW_E_UNSUPPORTED, "%s: more work than one launch deals out", who);
     const int64_t most = items * units;
     s->n_wgs = (int32_t)(most < 2 ? 2 : most < bpw::kAttnWgs ? most : bpw::kAttnWgs);
-    s->one_launch = s->cap * s->dp <= (items >= kShort4Items ? kShort4WorkFull : kShort4Work) && most * s->dp <= kShort4Steps;
+    // (a table without columns has no steps, but its items may be more than one grid takes)
+    s->one_launch = s->cap * s->dp <= (items >= kShort4Items ? kShort4WorkFull : kShort4Work) && most * s->dp <= kShort4Steps &&
+                    items <= bpw::kMaxWgs;
     const size_t rows = units > 0 ? (size_t)(items + (int64_t)bpw::kAttnWaves * s->n_wgs) * 16 : 0;  // a part per item and per run
     s->po = up256((size_t)(bpw::kSchedHead + 2 * (a->n_seqs + 1)) * 4);
     s->pml = s->po + up256(rows * (size_t)s->dp * 4);

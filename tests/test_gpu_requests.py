@@ -576,6 +576,22 @@ def test_attention4_many_sequences(dev):
     Attn4(dev, [1] * 1024, [1 + i % 3 for i in range(1024)], 2, 1, 256, 16, BF16, seed=31, max_pages=20).run()
 
 
+def test_attention4_more_workgroups_than_one_launch_over_an_empty_table(dev):
+    """A table without columns: nothing to see. A workgroup to each of its (sequence, head, tile) items would be a grid of more
+    than 2^32 threads, of which only the first would run."""
+    B, T, H, D = 1024, 144, 1024, 32
+    kv = bpw.PagedKv4(*kv4_cache(dev, 2, H, 16, D))
+    q = torch.randn(T, H, D, device=dev).to(BF16)
+    out, lse = torch.full_like(q, 77.0), torch.full((T, H), 77.0, device=dev)
+    table, lens = torch.empty(B, 0, dtype=I32, device=dev), torch.full((B,), 5, dtype=I32, device=dev)
+    starts = torch.zeros(B + 1, dtype=I32, device=dev)
+    starts[-1] = T  # the last sequence has the tokens
+    ws = torch.empty(bpw.bpw_kv4_attn_workspace_bytes(kv, q, B, T, 0), dtype=U8, device=dev)
+    bpw.bpw_kv4_attn(kv, q, out, table, lens, starts, T, ws, lse=lse)
+    torch.cuda.synchronize()
+    assert (out == 0).all() and (lse == -math.inf).all()
+
+
 def test_attention4_runtime_values_out_of_range(dev):
     """Lengths past the table cut, query tokens past the starts or max_q left out."""
     a = Attn4(dev, [1, 1, 3, 2], [100, 64, 40, 208], 4, 2, 64, 16, BF16, seed=9)
