@@ -216,8 +216,9 @@ bpw_status attn_shape(const bpw_attn_shared_prefix_args *a, AttnShape *s) {
         }
         s->splits = (int32_t)((tiles + s->split_units - 1) / s->split_units);
     }
-    const int64_t steps = (int64_t)a->n_seqs * c.kv_heads * ((rows_s + 15) / 16) * (up + us) * s->dp;
-    s->one_launch = (s->cap + 2 * a->prefix_len) * s->dp <= kShortWork && steps <= kShortSteps;
+    // (nothing to see has no steps, but its items may be more than one grid takes)
+    const int64_t items = (int64_t)a->n_seqs * c.kv_heads * ((rows_s + 15) / 16), steps = items * (up + us) * s->dp;
+    s->one_launch = (s->cap + 2 * a->prefix_len) * s->dp <= kShortWork && steps <= kShortSteps && items <= bpw::kMaxWgs;
     // one part per item and per run, or per piece of a wide prefix
     const int64_t waves = (int64_t)bpw::kAttnWaves * s->n_wgs;
     s->pieces_p = mp > 32 ? items_p * s->splits : up > 0 ? items_p + waves : 0;

@@ -689,6 +689,23 @@ def test_attention_more_rows_than_one_launch(dev, tokens, lens, Hq, Hk, prefix, 
     a.check()
 
 
+def test_attention_more_workgroups_than_one_launch_over_nothing(dev):
+    """No prefix and a table without columns: nothing to see. A workgroup to each of its (sequence, head, tile) items would be a
+    grid of more than 2^32 threads, of which only the first would run."""
+    B, T, H, D = 1024, 144, 1024, 32
+    k, v = (torch.zeros(2, H, 16, D, dtype=BF16, device=dev) for _ in range(2))
+    kv = bpw.PagedKv(k, v)
+    q = torch.randn(T, H, D, device=dev).to(BF16)
+    out, lse = torch.full_like(q, 77.0), torch.full((T, H), 77.0, device=dev)
+    table, lens = torch.empty(B, 0, dtype=torch.int32, device=dev), torch.full((B,), 5, dtype=torch.int32, device=dev)
+    starts = torch.zeros(B + 1, dtype=torch.int32, device=dev)
+    starts[-1] = T  # the last sequence has the tokens
+    ws = torch.empty(bpw.bpw_attn_shared_prefix_workspace_bytes(kv, q, 0, B, T, 0), dtype=torch.uint8, device=dev)
+    bpw.bpw_attn_shared_prefix(kv, q, out, None, 0, table, lens, starts, T, ws, lse=lse)
+    torch.cuda.synchronize()
+    assert (out == 0).all() and (lse == -torch.inf).all()
+
+
 def test_speculative_step_example(dev):
     """The operators together, from ternary projections to accepted tokens."""
     import importlib.util
