@@ -360,9 +360,20 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void prompt_kernel(PromptAr
         va ^= TILE;
     }
 
+    // In float16 a weight below 2^-31 of the largest is zero, and zero times an infinite value is NaN, which the value's own
+    // weight would not have made of it: looked for in the outputs.
+    if constexpr (__is_same(T, _Float16)) {
+        float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < DB; ++c)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) z[r & 3] = __builtin_fmaf(o[c][r], 0.0f, z[r & 3]);
+        const float any = (z[0] + z[1]) + (z[2] + z[3]);
+        if (any != any && lr == lr) odd = 1;
+    }
     wait_loads_to_lds();  // (zeros of tiles past the last: LDS is used anew)
-    // Values that are not finite and not seen by all: the tile of rows once more, step by step, with zeros in the place of such
-    // values, which are then added to the rows that see them (times any weight above zero they stay what they are).
+    // Values that are not finite and not seen by all, or that met a weight of zero: the tile of rows once more, step by step, with zeros
+    // in the place of such values, which are then added to the rows that see them (times any weight above zero they stay what they are).
     if (__syncthreads_or((int)odd)) {
         m = kNone;
         l = lr = 0.0f;
@@ -382,18 +393,19 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void prompt_kernel(PromptAr
                 weigh(0, m);
                 settle(0);
                 const int first = KT * t + 32 * (part + blk);
-                const bool some = first + 32 > all_see;
+                const bool some = __is_same(T, _Float16) || first + 32 > all_see;
+                uint32_t found = 0;
 #pragma unroll
                 for (int i = 0; i < VF; ++i) {
                     u32v4 f = value_frag(2 * blk + i / DB, i % DB);
                     if (some) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) f[e] = finite_halves<T>(f[e]);
+                        for (int e = 0; e < 4; ++e) found |= maybe_not_finite<T>(f[e]), f[e] = finite_halves<T>(f[e]);
                     }
                     o[i % DB] = mma32<T>(f, p[i / DB], o[i % DB]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                if (!some) continue;
+                if (!__any(found != 0)) continue;  // (all of the block's values were among the wave's operands)
 #pragma unroll 1
                 for (int i = 0; i < 32; ++i) {
                     const int r = 32 * (part + blk) + i;  // of the tile

@@ -646,8 +646,9 @@ bpw_status bpw_verify_draft(const bpw_verify_draft_args *a, void *d_ws, size_t w
  * head h / (q.heads / k.heads):
  *   out = sum_i softmax_i(scale * <q, k_i>) v_i,   lse = log sum_i exp(scale * <q, k_i>)  (natural log).
  * Scores, maxima, sums and outputs are held in float32; the softmax weights are rounded to the inputs' type for the
- * matrix cores (float16: to 2^-30 of the largest at the finest), and out is divided by the sum of the rounded weights. A
- * NaN among the scores that a token sees makes its out and lse NaN; what it does not see does not reach its results,
+ * matrix cores (float16: to 2^-30 of the largest at the finest), and out is divided by the sum of the rounded weights. An
+ * infinite value makes the outputs that see it infinite, also where its weight is none in float16 (NaN beside one of the
+ * other sign). A NaN among the scores that a token sees makes its out and lse NaN; what it does not see does not reach its results,
  * whatever it is (NaN in a later token's value). Starts are cut to [0, n_tokens]; tokens of no sequence (before the first
  * start, behind the last) are not written, and an empty sequence is none. The sums have a fixed order: the same arguments
  * give the same bits. One launch, no workspace.

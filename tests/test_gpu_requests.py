@@ -195,6 +195,29 @@ def test_prompt_nan_query_and_infinite_value(dev):
     assert torch.isnan(p.out[10, 1].float()).all() and torch.isnan(p.lse[10, 1]) and torch.isinf(p.out[30:70, 2:, 5].float()).all()
 
 
+@pytest.mark.parametrize("Hq,Hk,D,counts", [(4, 2, 64, [200, 90]), (4, 1, 128, [300]), (2, 2, 256, [260]), (6, 2, 80, [150, 70]),
+                                            (32, 4, 64, [1500, 600]), (16, 2, 128, [900, 300]), (16, 4, 256, [700])])
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_prompt_infinite_values_of_small_weight(dev, Hq, Hk, D, counts, dt):
+    """An infinite value makes the outputs that see it infinite, also where its weight, 2^-32 to 2^-100 of the largest, is none in
+    float16: beside the positions that all rows of a tile see, and on the diagonal."""
+    p = Prompt(dev, counts, Hq, Hk, D, dt, seed=D)
+    p.scale = 1.0
+    p.q.zero_(), p.k.zero_()
+    p.q[..., 0] = 1.0
+    n = counts[0]
+    p.k[:n, :, 0] = torch.randn(n, 1, device=dev).to(dt)
+    p.k[3, :, 0], p.k[n // 2, :, 0], p.k[n - 40, :, 0] = 30.0, -10.0, 45.0  # a weight of 2^-58 (to 2^-80) at n / 2
+    p.v[5, 0, 1], p.v[n // 2, -1, 2], p.v[n // 2, -1, 3], p.v[n - 30, 0, 4] = math.inf, -math.inf, math.inf, -math.inf
+    p.run()
+    p.check()
+    assert torch.isinf(p.out[5:n, :Hq // Hk, 1]).all() and torch.isinf(p.out[n // 2:n, -1, 2:4]).all()
+    p.v[n // 2 + 1, -1, 2] = math.inf  # and one of the other sign
+    p.run()
+    p.check("both signs")
+    assert torch.isnan(p.out[n // 2 + 1:n, -1, 2]).all() and torch.isinf(p.out[n // 2:n, -1, 3]).all()
+
+
 def test_prompt_float16_weights_far_below_the_largest(dev):
     """One position of 32 has all but 2^-25 of the weight and values of zero: the output is what the others add. A step of
     float16's subnormals is 2^-30 of the largest weight, half of one the error."""
