@@ -795,6 +795,24 @@ def test_logprobs_nearly_certain(dev):
     assert np.all(np.abs(f64(lp) - want[0]) <= 4 * U) and np.all(np.abs(f64(ent) - want[1]) <= 4 * U + 1e-3 * want[1])
 
 
+@pytest.mark.parametrize("dt", [F32, BF16, F16])
+@pytest.mark.parametrize("gap", [2.0, 8.0, 10.5, 11.0])
+def test_logprobs_nearly_certain_after_a_smaller_maximum(dev, dt, gap):
+    """A lane meets an entry `gap` below the row's largest long before that one, and nothing else. l is the sum of 1 and one weight,
+    off by half a step at 1 (all other additions add zero); the weight, and with it t, by the scale's roundings (3 U of the gap),
+    the exponential and the quotient (4 U each): less than 2^-18 of it."""
+    V, T = 12000, 1030  # one part a row, the two in the first and the second group of a lane's rounds
+    x = torch.full((1, V), -math.inf)
+    x[0, 40], x[0, 8192 + 40] = -gap, 0.0
+    x = x.to(dt)
+    lp, ent = torch.empty(T, device=dev), torch.empty(T, device=dev)
+    bpw.bpw_token_logprobs(x.to(dev).expand(T, V), torch.full((T,), 8192 + 40, dtype=I32, device=dev), lp, None, entropy=ent)
+    torch.cuda.synchronize()
+    want = request_ops.logprobs(f64(x), [8192 + 40], 0, 1.0)
+    assert np.all(np.abs(f64(lp) - want[0]) <= U + 2.0 ** -18 * abs(want[0]))
+    assert np.all(np.abs(f64(ent) - want[1]) <= U + 2.0 ** -18 * want[1])
+
+
 @pytest.mark.parametrize("offset", [1e4, -3e4, 1e6, 1e9, -1e20, 1e29])
 def test_logprobs_far_from_zero(dev, offset):
     """Logits that share a large offset: only their differences count."""
