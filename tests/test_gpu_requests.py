@@ -813,6 +813,26 @@ def test_logprobs_nearly_certain_after_a_smaller_maximum(dev, dt, gap):
     assert np.all(np.abs(f64(ent) - want[1]) <= U + 2.0 ** -18 * want[1])
 
 
+@pytest.mark.parametrize("V", [262144, 1 << 20])
+@pytest.mark.parametrize("weight", [0.55, 0.61, 0.7, 0.9])
+def test_logprobs_of_flat_rows(dev, V, weight):
+    """Entries nearly all alike, four above them: roundings of one chain of a lane's sums would all go the same way. l is a chain of 32
+    entries, of its groups, of 6 additions over lanes and 4 over waves; a weight is off by a product of two roundings' factor
+    (2 U of |d|) and 2^-22; log l by a step of it; the results by half a step."""
+    T, low = 1024, math.log(weight)  # (1024 rows: one part a row)
+    x = torch.full((1, V), low)
+    x[0, :1024:256] = 0.0  # (one to each of the waves that share a row: their shifts are alike)
+    lp, ent = torch.empty(T, device=dev), torch.empty(T, device=dev)
+    bpw.bpw_token_logprobs(x.to(dev).expand(T, V), torch.full((T,), V - 1, dtype=I32, device=dev), lp, None, entropy=ent)
+    torch.cuda.synchronize()
+    want = request_ops.logprobs(f64(x), [V - 1], 0, 1.0)
+    chain = U * (32 + V / 8192 + 10) + 2 * U * abs(low) + 2.0 ** -22
+    tol = chain + 3 * U * abs(want[0][0])
+    assert np.all(np.abs(f64(lp) - want[0]) <= tol), (f64(lp)[0] - want[0][0], tol)
+    # t / l: both chains, of at most |low| (a mean of the distances), its quotient's and its product's roundings among them
+    assert np.all(np.abs(f64(ent) - want[1]) <= tol + abs(low) * (2 * chain + 4 * U)), (f64(ent)[0] - want[1][0], tol)
+
+
 @pytest.mark.parametrize("offset", [1e4, -3e4, 1e6, 1e9, -1e20, 1e29])
 def test_logprobs_far_from_zero(dev, offset):
     """Logits that share a large offset: only their differences count."""
