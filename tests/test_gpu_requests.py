@@ -277,6 +277,42 @@ def test_prompt_same_bits_on_another_stream_and_in_a_graph(dev):
         assert same_bits(p.out, got)
 
 
+@pytest.mark.parametrize("counts,Hq,Hk,D,dt", [
+    ([1, 1, 2], 4, 2, 64, F16),
+    ([31, 33, 1, 64, 0, 65], 4, 4, 128, BF16),
+    ([300, 7], 6, 2, 80, BF16),
+    ([190, 3], 4, 2, 256, F16),
+    ([150], 5, 5, 192, BF16),
+    ([900, 300, 120], 16, 2, 128, F16),   # from here on rows enough for the pipeline
+    ([63, 1, 800, 0, 470], 16, 16, 96, BF16),
+    ([700, 333, 1, 290], 16, 4, 256, BF16),
+    ([450, 860], 16, 8, 200, F16),
+    ([700, 600], 16, 4, 160, BF16),
+    ([1500, 600], 32, 4, 64, F16),
+])
+def test_prompt_without_lse(dev, counts, Hq, Hk, D, dt):
+    """A kernel of its own, which forms no unrounded sums: the same outputs, bit for bit where they are numbers (no sum that lse
+    alone takes enters them), as they are, with scores that rise, with what is not finite."""
+    p = Prompt(dev, counts, Hq, Hk, D, dt, seed=D + 1, layout="fused", before=2, behind=1)
+    n = max(counts)
+    longest = 2 + sum(counts[:counts.index(n)])
+
+    def both(what):
+        p.run()
+        p.check(what)
+        out = torch.full_like(p.out, 77.0)
+        bpw.bpw_prompt_attn(p.q, p.k, p.v, out, p.starts, scale=p.scale)
+        torch.cuda.synchronize()
+        assert np.array_equal(f64(out), f64(p.out), equal_nan=True), what
+
+    both("as it is")
+    p.k[longest:longest + n] *= torch.linspace(0.1, 4, n, device=dev).to(dt)[:, None, None]
+    both("rising")
+    for at, x, what in ((n // 2, float("inf"), p.v), (n - 2, float("nan"), p.v), (n - 9, float("nan"), p.k)):
+        what[longest + max(at, 0), 0] = x
+    both("not finite")
+
+
 # ------------------------------------------------------------------------------ a cache held in 4 bits
 
 
