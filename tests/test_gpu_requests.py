@@ -723,6 +723,79 @@ def test_step4_in_a_graph(dev):
         assert same_bits(a.out, got) and same_bits(a.lse, lse)
 
 
+def two_launches(plan):
+    """Runs the plan and says whether it took the split and its join, which alone write the workspace."""
+    ws = plan._keep[1]
+    ws.fill_(255)
+    plan.run()
+    torch.cuda.synchronize()
+    return bool((ws != 255).any())
+
+
+def run_split(a, what=""):
+    """A call that has to take the two launches."""
+    a.out.fill_(77.0), a.lse.fill_(77.0)
+    assert two_launches(a.plan()), f"{what}: one launch"
+    a.check(what)
+
+
+def test_attention4_paths_are_those_they_are_named_for(dev):
+    for name, (n_q, lens, Hq, Hk, D, P, pages) in ATTENTION4_PATHS.items():
+        a = Attn4(dev, n_q, lens, Hq, Hk, D, P, BF16, seed=59, max_pages=pages)
+        assert two_launches(a.plan()) == name.startswith("split"), name
+
+
+def test_attention4_split_over_many_sequences(dev):
+    """Sequence counts past one thread's four and past a wave's 256, most idle or short; the most of all."""
+    n_q, lens = [i % 3 % 2 for i in range(700)], [(i * 7) % 41 if i % 5 else 0 for i in range(700)]
+    run_split(Attn4(dev, n_q, lens, 2, 1, 64, 16, F16, seed=3, max_pages=1000))
+    n_q, lens = [1 + i % 2 for i in range(300)], [(i * 37) % 611 for i in range(300)]
+    run_split(Attn4(dev, n_q, lens, 8, 2, 128, 32, BF16, seed=7, max_pages=400))
+    run_split(Attn4(dev, [1] * 1024, [1 + i % 3 for i in range(1024)], 2, 1, 256, 16, BF16, seed=31, max_pages=300))
+    run_split(Attn4(dev, [1] * 1024, [i % 70 for i in range(1024)], 2, 1, 32, 16, F16, seed=37, max_pages=1000, layout="nhd"))
+
+
+@pytest.mark.parametrize("D,P,pages,dt", [(64, 16, 1000, BF16), (128, 16, 500, F16), (256, 32, 150, BF16)])
+def test_attention4_split_runtime_values_out_of_range(dev, D, P, pages, dt):
+    """Lengths past the table cut, query tokens past the starts or max_q left out."""
+    a = Attn4(dev, [1, 1, 3, 2], [100, 64, 40, 208], 4, 2, D, P, dt, seed=9, max_pages=pages)
+    a.len_t[3], a.len_t[2] = 2 ** 31 - 1, -5
+    run_split(a, "lengths")
+    a.max_q = 2
+    run_split(a, "max_q")
+    a.starts[-1], a.starts[1] = 100, -3
+    run_split(a, "starts")
+
+
+@pytest.mark.parametrize("D,Hq,dt", [(64, 8, BF16), (128, 10, F16), (256, 4, BF16)])
+def test_attention4_split_in_a_graph_and_on_another_stream(dev, D, Hq, dt):
+    """Split and join captured once; queries, pages and lengths change between replays; the same bits on another stream."""
+    lens = [300, 2000, 65, 1, 900]
+    a = Attn4(dev, [1, 2, 1, 1, 3], lens, Hq, 2, D, 16, dt, seed=23, max_pages=1000)
+    plan = a.plan()
+    assert two_launches(plan)
+    a.check("eager")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan.run()
+    side = torch.cuda.Stream()
+    for i, order in enumerate(([0, 1, 2, 3, 4], [4, 0, 3, 1, 2], [1, 4, 0, 2, 3])):
+        a.q.normal_(std=0.3)
+        a.table.copy_(a.table[order].clone())
+        a.len_t.copy_(torch.tensor(lens, dtype=I32, device=dev)[order].clone())
+        lens = [lens[x] for x in order]
+        a.out.fill_(77.0), a.lse.fill_(77.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        a.check(f"replay {i}")
+        got, lse = a.out.clone(), a.lse.clone()
+        a.out.fill_(77.0)
+        side.wait_stream(torch.cuda.current_stream())
+        plan.run(side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert same_bits(a.out, got) and same_bits(a.lse, lse)
+
+
 # ------------------------------------------------------------------------------ log probabilities
 
 
