@@ -176,14 +176,27 @@ struct Attn4Shape {
     size_t po, pml, total;  // workspace: offsets of the parts, all
 };
 
-// One launch, a workgroup to an item (sequence, key/value head, 16 query rows), up to so many positions of a row of the page table
-// (x padded head size), more of them where the items alone fill half the CUs; otherwise even runs of positions and a join,
-// which take some 12 us at least. Heads of 128, 8 key/value heads, one sequence: 10.2 us in one launch against 11.9 at 1024 positions,
-// 14.9 against 12.7 at 2048; 64 sequences: 22.0 against 24.2, 33.7 against 35.6. Heads of 64, 64 sequences of 4096: 33 against 45,
-// one: 20 against 14. Heads of 256, 4 key/value heads: one sequence of 512 11.9 against 13.0, of 1024 17.1 against 12.9.
-constexpr int64_t kShort4Work = 163840, kShort4WorkFull = 262144;
-constexpr int64_t kShort4Items = 128;
-// And most of all its workgroups' steps (x padded head size), past which uneven lengths weigh more than the launch.
+// One launch, a workgroup to an item (sequence, key/value head, 16 query rows), or even runs of positions over all waves and a
+// join, which take 9 us at least. Measured (us, one launch against two; tables full; 32 query heads to 8 key/value heads at 64 and
+// 128, 16 to 4 at 256; a token to a sequence unless said).
+// Up to so many positions of a row of the page table (x padded head size): one sequence of heads of 128 9.8 : 9.7 at 1024 positions,
+// 12.0 : 10.8 at 1536; of heads of 256 11.5 : 11.0 at 512, 16.7 : 11.6 at 1024.
+constexpr int64_t kShort4Work = 163840;
+// And from 128 items on, half of the CUs: 16 sequences of heads of 64 14.3 : 16.0 at 2560, 19.6 : 18.7 at 4096, 26.4 : 22.3 at 6144; 32 of
+// them 20.1 : 25.4 at 4096; 16 of heads of 128 15.0 : 17.2 at 2048, 17.0 : 18.8 at 2560, 23.7 : 23.2 at 4096; 64 of them 33.1 : 34.9 at
+// 2048, 54.4 : 56.5 at 4096, but, with lengths spread from 1 on, 59.5 : 49.4 at 6144.
+constexpr int64_t kShort4WorkFull = 262144, kShort4Items = 128;
+// And so many steps of a wave beside one more for every 16 items, as few items leave CUs idle for as long: one sequence of heads of
+// 64 8.7 : 9.4 at 1024 positions (4 steps), 10.5 : 9.7 at 1536 (6), 14.0 : 10.9 at 2560 (10); 4 of them 10.7 : 11.4, 14.3 : 12.4 at the
+// last two.
+constexpr int64_t kShort4WaveSteps = 5;
+// And so many items beside one for every 16 query rows, by padded head size, about two turns of all workgroups (heads of 128: one to a CU,
+// of 64, whose turns are short, more): 64 sequences of 512 positions, heads of 128 14.8 : 17.5, 128 29.5 : 24.6, 512 110.6 : 72.1;
+// heads of 256 128 26.3 : 35.6, 256 51.3 : 49.9, 512 99.1 : 82.2; heads of 64 512 55.2 : 53.8, 1024 113.5 : 101.4. Rows cost the join:
+// 8 sequences of 64 tokens of heads of 128 33.6 : 36.4 (1024 items).
+int64_t short4_items(int32_t padded_dim) { return padded_dim == 64 ? 4096 : padded_dim == 128 ? 512 : 1024; }
+// And most of all items' steps (x padded head size), where the items are many by their rows: 4 sequences of 200 tokens of heads of 128
+// 55.4 : 53.4 at 512 positions, 113.2 : 101.3 at 2048; 2 of 1000 185 : 160 at 1024.
 constexpr int64_t kShort4Steps = 1 << 22;
 
 bpw_status attn4_shape(const bpw_kv4_attn_args *a, Attn4Shape *s) {
@@ -211,9 +224,11 @@ bpw_status attn4_shape(const bpw_kv4_attn_args *a, Attn4Shape *s) {
         return fail(BPW_E_UNSUPPORTED, "%s: more work than one launch deals out", who);
     const int64_t most = items * units;
     s->n_wgs = (int32_t)(most < 2 ? 2 : most < bpw::kAttnWgs ? most : bpw::kAttnWgs);
+    const int64_t waves = s->dp == 256 ? 4 : 8, query_rows = a->n_seqs * max_q * a->q.heads;
     // (a table without columns has no steps, but its items may be more than one grid takes)
-    s->one_launch = s->cap * s->dp <= (items >= kShort4Items ? kShort4WorkFull : kShort4Work) && most * s->dp <= kShort4Steps &&
-                    items <= bpw::kMaxWgs;
+    s->one_launch = s->cap * s->dp <= (items >= kShort4Items ? kShort4WorkFull : kShort4Work) &&
+                    (units + waves - 1) / waves <= kShort4WaveSteps + items / 16 &&
+                    items <= short4_items(s->dp) + query_rows / 16 && most * s->dp <= kShort4Steps && items <= bpw::kMaxWgs;
     const size_t rows = units > 0 ? (size_t)(items + (int64_t)bpw::kAttnWaves * s->n_wgs) * 16 : 0;  // a part per item and per run
     s->po = up256((size_t)(bpw::kSchedHead + 2 * (a->n_seqs + 1)) * 4);
     s->pml = s->po + up256(rows * (size_t)s->dp * 4);

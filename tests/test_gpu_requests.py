@@ -745,6 +745,23 @@ def test_attention4_paths_are_those_they_are_named_for(dev):
         assert two_launches(a.plan()) == name.startswith("split"), name
 
 
+@pytest.mark.parametrize("B,n,Hq,Hk,D,positions,two", [
+    (1, 1, 32, 8, 64, 1280, False), (1, 1, 32, 8, 64, 1536, True), (4, 1, 32, 8, 64, 1536, False), (4, 1, 32, 8, 64, 2560, True),
+    (64, 1, 32, 8, 64, 4096, False), (64, 1, 32, 8, 64, 4160, True), (1, 1, 20, 5, 128, 1280, False), (1, 1, 20, 5, 128, 1344, True),
+    (64, 1, 32, 8, 128, 512, False), (128, 1, 32, 8, 128, 512, True), (8, 64, 32, 8, 128, 512, False), (2, 1000, 32, 8, 128, 1024, True),
+    (256, 1, 16, 4, 256, 256, False), (512, 1, 16, 4, 256, 256, True), (512, 1, 32, 8, 64, 256, False), (1024, 1, 32, 8, 64, 256, True),
+])
+def test_attention4_takes_the_launches_that_its_sizes_call_for(dev, B, n, Hq, Hk, D, positions, two):
+    """On both sides of every bound of the rule, by the table's columns; few positions of them are in use."""
+    a = Attn4(dev, [min(n, 3)] * B, [3 + i % 40 for i in range(B)], 1, 1, D, 64, BF16, seed=67, max_pages=positions // 64)
+    a.cache = [c.expand(-1, Hk, -1, -1).contiguous() for c in a.cache]
+    T = max(n, min(n, 3) * B)
+    a.q = (torch.randn(T, Hq, D, device=dev) * 0.3).to(BF16)
+    a.out, a.lse, a.max_q = torch.full_like(a.q, 77.0), torch.full((T, Hq), 77.0, device=dev), n
+    assert two_launches(a.plan()) == two
+    a.check()
+
+
 def test_attention4_split_over_many_sequences(dev):
     """Sequence counts past one thread's four and past a wave's 256, most idle or short; the most of all."""
     n_q, lens = [i % 3 % 2 for i in range(700)], [(i * 7) % 41 if i % 5 else 0 for i in range(700)]
