@@ -22,8 +22,9 @@ namespace bpw {
 
 constexpr int kAppendThreads = 256;
 // Tokens from which a workgroup takes two of them, not one: its waves then have more to do between loads, but fewer workgroups
-// share few tokens. 48 heads of 128: 9.7 us with one against 12.1 with two at 1024 tokens, 17.0 against 15.8 at 2048, 55.7
-// against 51.8 at 8192 (51.5 with four, 52.2 with eight).
+// share few tokens. Over memory that no cache holds, us with one and with two: 32 + 8 + 8 heads of 128 9.7, 11.8 at 1024 tokens, 14.1,
+// 13.1 at 1536, 16.3, 16.9 at 2048, 31.5, 30.9 at 4096, 56.4, 56.3 at 8192 (four 56.4); 16 + 4 + 4 of 256 9.7, 11.8 at 1024, 16.8,
+// 15.5 at 2048; 8 + 2 + 2 of 64 5.1, 5.7 at 1024, 8.8, 7.1 at 2048, 49.0, 36.7 at 16384 (four 28.8).
 constexpr int32_t kAppendManyTokens = 2048;
 
 template <class R>
