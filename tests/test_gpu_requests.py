@@ -813,6 +813,132 @@ def test_attention4_split_in_a_graph_and_on_another_stream(dev, D, Hq, dt):
         assert same_bits(a.out, got) and same_bits(a.lse, lse)
 
 
+# ------------------------------------------------------------------------------ strides of outputs, counts past one launch, no pages
+
+
+def outputs_of(dev, T, H, D, dt, layout):
+    """An output of 77 inside a larger buffer of 77, and that buffer."""
+    shape, order = {"wide rows": ((T, H + 3, D + 16), (0, 1, 2)), "heads first": ((H + 1, T + 2, D), (1, 0, 2))}[layout]
+    buf = torch.full(shape, 77.0, dtype=dt, device=dev)
+    return buf.permute(order)[:T, 1:H + 1, :D] if layout == "wide rows" else buf.permute(order)[1:T + 1, :H], buf
+
+
+def rest_is_left(view, buf):
+    kept = view.clone()
+    view.fill_(77.0)
+    assert (buf == 77).all()
+    return kept
+
+
+@pytest.mark.parametrize("layout", ["wide rows", "heads first"])
+@pytest.mark.parametrize("counts,Hq,Hk,D,dt", [([40, 3], 6, 2, 80, F16), ([900, 300, 120], 16, 2, 128, BF16), ([150], 4, 4, 256, BF16)])
+def test_prompt_into_outputs_of_any_strides(dev, counts, Hq, Hk, D, dt, layout):
+    p = Prompt(dev, counts, Hq, Hk, D, dt, seed=71)
+    p.run()
+    out, buf = outputs_of(dev, sum(counts), Hq, D, dt, layout)
+    bpw.bpw_prompt_attn(p.q, p.k, p.v, out, p.starts, lse=p.lse)
+    torch.cuda.synchronize()
+    assert same_bits(rest_is_left(out, buf), p.out)
+
+
+@pytest.mark.parametrize("layout", ["wide rows", "heads first"])
+@pytest.mark.parametrize("T,D,dt", [(33, 64, BF16), (33, 96, F16), (2049, 128, BF16)])
+def test_append4_into_outputs_of_any_strides(dev, T, D, dt, layout):
+    Hq, Hk = 5, 2
+    rows = torch.randn(T, Hq + 2 * Hk, D, device=dev)
+    pos, freq = torch.arange(T, dtype=I32, device=dev), 10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64, device=dev) / D)
+    cache = [kv4_cache(dev, T // 16 + 1, Hk, 16, D) for _ in range(2)]
+    want = [torch.empty(T, h, D, dtype=dt, device=dev) for h in (Hq, Hk, Hk)]
+    got = [outputs_of(dev, T, h, D, dt, layout) for h in (Hq, Hk, Hk)]
+    for c, (qo, kv, vv) in zip(cache, (want, [x for x, _ in got])):
+        bpw.bpw_kv4_append(bpw.PagedKv4(*c), rows[:, Hq:Hq + Hk], rows[:, Hq + Hk:], torch.arange(T, device=dev), pos, freq, q=rows[:, :Hq], q_out=qo,
+                           k_values=kv, v_values=vv)
+    torch.cuda.synchronize()
+    for (view, buf), x in zip(got, want):
+        assert same_bits(rest_is_left(view, buf), x)
+    assert all(torch.equal(a, b) for a, b in zip(*cache))
+
+
+@pytest.mark.parametrize("layout", ["wide rows", "heads first"])
+@pytest.mark.parametrize("path", ATTENTION4_PATHS)
+def test_attention4_into_outputs_of_any_strides(dev, path, layout):
+    n_q, lens, Hq, Hk, D, P, pages = ATTENTION4_PATHS[path]
+    a = Attn4(dev, n_q, lens, Hq, Hk, D, P, BF16, seed=73, max_pages=pages)
+    a.run()
+    want = a.out
+    a.out, buf = outputs_of(dev, sum(n_q), Hq, D, BF16, layout)
+    a.plan().run()
+    torch.cuda.synchronize()
+    assert same_bits(rest_is_left(a.out, buf), want)
+
+
+@pytest.mark.parametrize("path", ATTENTION4_PATHS)
+def test_attention4_over_a_cache_without_pages(dev, path):
+    """Every entry of the table is out of range: zeros."""
+    n_q, lens, Hq, Hk, D, P, pages = ATTENTION4_PATHS[path]
+    a = Attn4(dev, n_q, lens, Hq, Hk, D, P, F16, seed=79, max_pages=pages)
+    a.cache = [c[:0].contiguous() for c in a.cache]
+    a.plan().run()
+    torch.cuda.synchronize()
+    assert (a.out == 0).all() and (a.lse == -math.inf).all()
+
+
+def test_append4_to_a_cache_without_pages(dev):
+    """No slot is inside it; the values are handed out all the same."""
+    T, Hk, D = 9, 2, 64
+    k, v = torch.randn(T, Hk, D, device=dev), torch.randn(T, Hk, D, device=dev)
+    out = [torch.empty(T, Hk, D, dtype=BF16, device=dev) for _ in range(2)]
+    kv = bpw.PagedKv4(*(torch.empty(0, Hk, 16, n, dtype=U8, device=dev) for n in (D // 2, D // 2, D // 32, D // 32)))
+    bpw.bpw_kv4_append(kv, k, v, torch.arange(T, device=dev), k_values=out[0], v_values=out[1])
+    torch.cuda.synchronize()
+    for x, got in zip((k, v), out):
+        assert np.array_equal(f64(got), request_ops.from_codes(*request_ops.to_codes(f64(x))[:2]))
+
+
+def test_prompt_of_the_most_sequences(dev):
+    """2^20 sequences of one token: more workgroups than one launch takes, and each output is its own value."""
+    T, H, D = 1 << 20, 8, 8
+    q, k, v = (torch.randn(T, H, D, device=dev).to(BF16) for _ in range(3))
+    out, lse = torch.full_like(q, 77.0), torch.full((T, H), 77.0, device=dev)
+    bpw.bpw_prompt_attn(q, k, v, out, torch.arange(T + 1, dtype=I32, device=dev), scale=0.5, lse=lse)
+    torch.cuda.synchronize()
+    assert torch.equal(out, v)
+    s = (q.double() * k.double()).sum(-1) * 0.5
+    assert ((lse.double() - s).abs() <= (D + 8) * 2 * U * 0.5 * (q.double() * k.double()).abs().sum(-1) + 4 * U * s.abs() + 2.0 ** -22).all()
+
+
+def test_append4_of_more_tokens_than_one_launch(dev):
+    """2^23 workgroups' tokens and some more, rows that repeat; the last ones alone have slots."""
+    T, D, n = (1 << 23) + 5, 32, 64
+    rows = torch.randn(n, 1, D, device=dev).to(BF16)
+    k = rows.repeat(T // n + 1, 1, 1)[:T]
+    slots = torch.full((T,), -1, dtype=torch.int64, device=dev)
+    slots[-16:] = torch.arange(16, device=dev)
+    cache, small = kv4_cache(dev, 1, 1, 16, D), kv4_cache(dev, 1, 1, 16, D)
+    out = torch.full_like(k, 77.0)
+    bpw.bpw_kv4_append(bpw.PagedKv4(*cache), k, k, slots, k_values=out)
+    want = torch.empty_like(rows)
+    bpw.bpw_kv4_append(bpw.PagedKv4(*small), rows, rows, torch.full((n,), -1, dtype=torch.int64, device=dev), k_values=want)
+    bpw.bpw_kv4_append(bpw.PagedKv4(*small), k[-16:].contiguous(), k[-16:].contiguous(), torch.arange(16, device=dev))
+    torch.cuda.synchronize()
+    assert torch.equal(out[:T // n * n].view(-1, n, 1, D), want.expand(T // n, n, 1, D)) and torch.equal(out[T // n * n:], want[:T % n])
+    assert all(torch.equal(a, b) for a, b in zip(cache, small))
+
+
+def test_logprobs_of_more_rows_than_one_launch(dev):
+    T, V = (1 << 22) + 7, 3
+    x = torch.randn(T, V, device=dev)
+    tokens = torch.randint(0, V, (T,), device=dev).int()
+    lp, ent, top, top_lp = torch.empty(T, device=dev), torch.empty(T, device=dev), torch.empty(T, 1, dtype=I32, device=dev), torch.empty(T, 1, device=dev)
+    bpw.bpw_token_logprobs(x, tokens, lp, None, ent, top, top_lp)
+    torch.cuda.synchronize()
+    want = torch.log_softmax(x.double(), -1)
+    assert torch.equal(top[:, 0].long(), want.argmax(-1))
+    # at most three weights: two additions, the exponentials, log and result in half steps of values up to some twenty
+    for got, y in ((lp, want.gather(1, tokens[:, None].long())[:, 0]), (ent, -(want.exp() * want).sum(-1)), (top_lp[:, 0], want.amax(-1))):
+        assert ((got.double() - y).abs() <= 2.0 ** -20 * (1 + y.abs())).all()
+
+
 # ------------------------------------------------------------------------------ log probabilities
 
 
