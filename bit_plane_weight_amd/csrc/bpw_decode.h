@@ -167,8 +167,9 @@ struct PromptArgs {
     float scale_log2;
 };
 
-// Tiles of `rows` query rows: those of a sequence whose first token has `before` rows before it begin at this slot, which leaves room for all of its own, as floor(x + n) >= floor(x) + floor(n) and a sequence adds one. So the slots of a
-// sequence follow from its own start, and no launch or scan has to count tiles.
+// Tiles of `rows` query rows: those of a sequence whose first token has `before` rows before it begin at this slot, which
+// leaves room for all of its own, as floor(x + n) >= floor(x) + floor(n) and a sequence adds one. So the slots of a sequence
+// follow from its own start, and no launch or scan has to count tiles.
 inline __host__ __device__ int32_t prompt_slot(int32_t before, int32_t seq, int32_t rows) { return before / rows + seq; }
 
 int launch_prompt_d64(const PromptArgs &a, int32_t dtype, bool many, void *stream);

@@ -7,10 +7,10 @@
 // key lies on is decided after norm and rotation; these are held in float64, as in float32 one element in some 10^6 would
 // get the neighbouring code, a whole step away.
 //
-// Bound: HBM for prompts (8192 tokens of 32 + 8 + 8 heads of 128 in bfloat16, 210 MB read and written: 58-60 us over memory that no
-// cache holds, 3.6 TB/s; three items are on their way beside the one worked on, with two 63 us, with four or five
+// Bound: HBM for prompts (8192 tokens of 32 + 8 + 8 heads of 128 in bfloat16, 210 MB read and written: 56-60 us over memory that no
+// cache holds, 3.5-3.7 TB/s; three items are on their way beside the one worked on, with two 63 us, with four or five
 // 58-60), while the vector units issue half of the time; the launch for a decode step (64
-// tokens: 6.1 us). The wave's work is one head set's at a time, so that what differs between them is in
+// tokens: 6 us). The wave's work is one head set's at a time, so that what differs between them is in
 // scalar registers (93 us when lanes of a wave chose); sines and cosines are formed once for all heads of a token; a lane
 // holds eight neighbours of a head, a block is four lanes, its largest element two DPP steps away, and its 32 codes four
 // words of 32 bits, from the conversion instruction. Partners of a rotation go through LDS, 16 bytes of each lane beside

@@ -328,154 +328,154 @@ __device__ __forceinline__ void attend4(const Attn4Args &b, const AttnSpan &s, u
     const int end = a.n_pages > 0 ? min(s.len, s.pos1) : s.pos0;
     bool found = false;  // a value that only some rows see is NaN: a weight of zero does not hide it
     const auto pass = [&](auto slow) __attribute__((always_inline)) {
-    int kv0 = s.pos0, next = kv0;
-    Issued x;
-    x.bad = x.none = 0;
-    x.k32 = 32 * b.kc.rs, x.v32 = 32 * b.vc.rs, x.ks32 = 32 * b.kc.s_rs, x.vs32 = 32 * b.vc.s_rs;
-    asm volatile("" : "+s"(x.k32), "+s"(x.v32), "+s"(x.ks32), "+s"(x.vs32));
-    x.pages.fetch(a, s, kv0 >> a.page_log2);
-    // The queries are waited for with the pages, not in the loop, where a wait for them would be one for all loads to LDS.
+        int kv0 = s.pos0, next = kv0;
+        Issued x;
+        x.bad = x.none = 0;
+        x.k32 = 32 * b.kc.rs, x.v32 = 32 * b.vc.rs, x.ks32 = 32 * b.kc.s_rs, x.vs32 = 32 * b.vc.s_rs;
+        asm volatile("" : "+s"(x.k32), "+s"(x.v32), "+s"(x.ks32), "+s"(x.vs32));
+        x.pages.fetch(a, s, kv0 >> a.page_log2);
+        // The queries are waited for with the pages, not in the loop, where a wait for them would be one for all loads to LDS.
 #pragma unroll
-    for (int c = 0; c < KC; ++c)
+        for (int c = 0; c < KC; ++c)
 #pragma unroll
-        for (int i = 0; i < QP; ++i) asm volatile("" : "+v"(q[c][i]));
-    uint32_t at = 0;
+            for (int i = 0; i < QP; ++i) asm volatile("" : "+v"(q[c][i]));
+        uint32_t at = 0;
 #pragma unroll 1
-    for (int i = 0; i < STEPS; ++i, next += kAttnStep, at += Ring::STEP) {
-        if (next < end)
-            issue(x, next, ring + at);
-        else
-            x.bad <<= 2;
-    }
-    at = 0;
-    for (; kv0 < end; kv0 += kAttnStep, next += kAttnStep) {
-        if (next - kAttnStep < end)
-            wait_all_but<Ring::ALL * (STEPS - 1)>();
-        else
-            wait_all_but<0>();
-        Keys k0, k1;
-        Values v0, v1;
-        const Reads r = reads_of(at);
-        read_keys(r, 0, k0);
-        read_keys(r, 1, k1);
-        read_values(r, 0, v0);
-        read_values(r, 1, v1);
-        const int here = kv0;
-        const uint32_t none = x.bad >> (2 * (STEPS - 1)) & 3;
-        if (next < end)
-            issue(x, next, ring + at);
-        else
-            x.bad <<= 2;
-        at = at == (STEPS - 1) * Ring::STEP ? 0 : at + Ring::STEP;
-        f32x4 sc[2] = {scores(k0), scores(k1)};
-        bool odd = false;
-        if (here + kAttnStep > all_see || none) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int pos = here + 16 * t + 4 * g + r;
-                    const bool page = !(none >> t & 1);
-                    if (!page || pos >= vis) sc[t][r] = kNone;
-#pragma unroll
-                    for (int h = 0; h < NH; ++h) {
-                        uint32_t &u = t ? v1.unit[r][h] : v0.unit[r][h];
-                        if (!page || pos >= s.len)
-                            u = 127;  // zero weight times whatever the page holds there is not zero
-                        else if (pos >= all_see)
-                            found |= u > 252;
-                    }
-                }
-            odd = slow;
+        for (int i = 0; i < STEPS; ++i, next += kAttnStep, at += Ring::STEP) {
+            if (next < end)
+                issue(x, next, ring + at);
+            else
+                x.bad <<= 2;
         }
-        // weights against a shift that is raised where a lane's sum of a step passes the limit, as in attend()
-        f32x8 w;
-        float sum = 0.0f;
-        const auto weigh = [&](float shift) {
-            sum = 0.0f;
+        at = 0;
+        for (; kv0 < end; kv0 += kAttnStep, next += kAttnStep) {
+            if (next - kAttnStep < end)
+                wait_all_but<Ring::ALL * (STEPS - 1)>();
+            else
+                wait_all_but<0>();
+            Keys k0, k1;
+            Values v0, v1;
+            const Reads r = reads_of(at);
+            read_keys(r, 0, k0);
+            read_keys(r, 1, k1);
+            read_values(r, 0, v0);
+            read_values(r, 1, v1);
+            const int here = kv0;
+            const uint32_t none = x.bad >> (2 * (STEPS - 1)) & 3;
+            if (next < end)
+                issue(x, next, ring + at);
+            else
+                x.bad <<= 2;
+            at = at == (STEPS - 1) * Ring::STEP ? 0 : at + Ring::STEP;
+            f32x4 sc[2] = {scores(k0), scores(k1)};
+            bool odd = false;
+            if (here + kAttnStep > all_see || none) {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r >> 2][r & 3], a.scale_log2, -shift));
-                sum += w[r];
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int pos = here + 16 * t + 4 * g + r;
+                        const bool page = !(none >> t & 1);
+                        if (!page || pos >= vis) sc[t][r] = kNone;
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) {
+                            uint32_t &u = t ? v1.unit[r][h] : v0.unit[r][h];
+                            if (!page || pos >= s.len)
+                                u = 127;  // zero weight times whatever the page holds there is not zero
+                            else if (pos >= all_see)
+                                found |= u > 252;
+                        }
+                    }
+                odd = slow;
             }
-        };
-        weigh(m);
-        if (__any(!(sum < kShiftLimit<__bf16>))) {
-            float top = kNone;
+            // weights against a shift that is raised where a lane's sum of a step passes the limit, as in attend()
+            f32x8 w;
+            float sum = 0.0f;
+            const auto weigh = [&](float shift) {
+                sum = 0.0f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) top = fmaxf(top, fmaxf(sc[0][r], sc[1][r]));
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
-            const float up = fmaxf(m, top);
-            const float f = up == m ? 1.0f : __builtin_amdgcn_exp2f(m - up);
-            m = up;
-            l *= f;
+                for (int r = 0; r < 8; ++r) {
+                    w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r >> 2][r & 3], a.scale_log2, -shift));
+                    sum += w[r];
+                }
+            };
+            weigh(m);
+            if (__any(!(sum < kShiftLimit<__bf16>))) {
+                float top = kNone;
 #pragma unroll
-            for (int c = 0; c < NH * EL; ++c) o[c] *= f;
-            weigh(up == kNone ? 0.0f : up);
-        }
-        l += sum;
-        // weights as two numbers of bfloat16, the second the rest of the first (2^-17 of a weight are lost)
-        u32v4 w0, w1;
+                for (int r = 0; r < 4; ++r) top = fmaxf(top, fmaxf(sc[0][r], sc[1][r]));
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32)) * a.scale_log2;
+                const float up = fmaxf(m, top);
+                const float f = up == m ? 1.0f : __builtin_amdgcn_exp2f(m - up);
+                m = up;
+                l *= f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-            typedef float f32x2 __attribute__((ext_vector_type(2)));
-            const f32x2 x = {w[2 * i], w[2 * i + 1]};
-            w0[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
-            const f32x2 rest = {x.x - __builtin_bit_cast(float, w0[i] << 16), x.y - __builtin_bit_cast(float, w0[i] & 0xFFFF0000u)};
-            w1[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, bf16x2));
-        }
+                for (int c = 0; c < NH * EL; ++c) o[c] *= f;
+                weigh(up == kNone ? 0.0f : up);
+            }
+            l += sum;
+            // weights as two numbers of bfloat16, the second the rest of the first (2^-17 of a weight are lost)
+            u32v4 w0, w1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+                typedef float f32x2 __attribute__((ext_vector_type(2)));
+                const f32x2 x = {w[2 * i], w[2 * i + 1]};
+                w0[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
+                const f32x2 rest = {x.x - __builtin_bit_cast(float, w0[i] << 16), x.y - __builtin_bit_cast(float, w0[i] & 0xFFFF0000u)};
+                w1[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, bf16x2));
+            }
 
-        uint32_t v[8][NH][VW];
+            uint32_t v[8][NH][VW];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int h = 0; h < NH; ++h)
+                for (int h = 0; h < NH; ++h)
 #pragma unroll
-                for (int i = 0; i < VW; ++i) {
-                    v[r][h][i] = two_of(v0.w[r][h], unit_of_byte(v0.unit[r][h]), i);
-                    v[4 + r][h][i] = two_of(v1.w[r][h], unit_of_byte(v1.unit[r][h]), i);
-                }
-        const auto turned = [&](int h, int c) {
-            u32v4 f;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                f[x] = __builtin_amdgcn_perm(v[2 * x + 1][h][c >> 1], v[2 * x][h][c >> 1], c & 1 ? 0x07060302u : 0x05040100u);
-            return f;
-        };
-        if (!slow || !odd) {
-#pragma unroll
-            for (int h = 0; h < NH; ++h)
-#pragma unroll
-                for (int c = 0; c < EL; ++c) {
-                    const u32v4 f = turned(h, c);
-                    o[h * EL + c] = mma<__bf16>(f, w1, mma<__bf16>(f, w0, o[h * EL + c]));
-                }
-        } else if constexpr (slow) {
-            // one query token at a time, the last first: the values that it does not see are set to zero, and only its
-            // rows take the result
-            const int last = min(s.n_tok, (s.row0 + 15) / a.group + 1);
-            for (int j = last - 1; j >= s.row0 / a.group; --j) {
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    if (here + 16 * (x >> 2) + 4 * g + (x & 3) >= s.len - (s.n_tok - 1 - j)) {
-#pragma unroll
-                        for (int h = 0; h < NH; ++h)
-#pragma unroll
-                            for (int i = 0; i < VW; ++i) v[x][h][i] = 0;
+                    for (int i = 0; i < VW; ++i) {
+                        v[r][h][i] = two_of(v0.w[r][h], unit_of_byte(v0.unit[r][h]), i);
+                        v[4 + r][h][i] = two_of(v1.w[r][h], unit_of_byte(v1.unit[r][h]), i);
                     }
+            const auto turned = [&](int h, int c) {
+                u32v4 f;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    f[x] = __builtin_amdgcn_perm(v[2 * x + 1][h][c >> 1], v[2 * x][h][c >> 1], c & 1 ? 0x07060302u : 0x05040100u);
+                return f;
+            };
+            if (!slow || !odd) {
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
 #pragma unroll
                     for (int c = 0; c < EL; ++c) {
                         const u32v4 f = turned(h, c);
-                        const f32x4 x = mma<__bf16>(f, w1, mma<__bf16>(f, w0, o[h * EL + c]));
-                        if ((s.row0 + n) / a.group == j) o[h * EL + c] = x;
+                        o[h * EL + c] = mma<__bf16>(f, w1, mma<__bf16>(f, w0, o[h * EL + c]));
                     }
+            } else if constexpr (slow) {
+                // one query token at a time, the last first: the values that it does not see are set to zero, and only its
+                // rows take the result
+                const int last = min(s.n_tok, (s.row0 + 15) / a.group + 1);
+                for (int j = last - 1; j >= s.row0 / a.group; --j) {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        if (here + 16 * (x >> 2) + 4 * g + (x & 3) >= s.len - (s.n_tok - 1 - j)) {
+#pragma unroll
+                            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                                for (int i = 0; i < VW; ++i) v[x][h][i] = 0;
+                        }
+#pragma unroll
+                    for (int h = 0; h < NH; ++h)
+#pragma unroll
+                        for (int c = 0; c < EL; ++c) {
+                            const u32v4 f = turned(h, c);
+                            const f32x4 x = mma<__bf16>(f, w1, mma<__bf16>(f, w0, o[h * EL + c]));
+                            if ((s.row0 + n) / a.group == j) o[h * EL + c] = x;
+                        }
+                }
             }
         }
-    }
     };
     pass(std::false_type{});
     if (__any(found)) {  // once more, with what a token does not see set to zero for it

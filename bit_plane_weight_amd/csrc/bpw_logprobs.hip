@@ -8,9 +8,10 @@
 // above zero by more than the shift's rounding and these sums' terms are of one sign, too. (A shift that a logit may pass by 2^16 in
 // weight is raised less often, but t + d l then loses 5e-7 of the entropy where the largest follows one 8 to 11 below it.)
 //
-// Bound: HBM, each logit read once. A wave takes four rounds of 512 entries (eight a lane) while the next four are on their
-// way. 2048 rows of 128256 in bfloat16, the best one: 100 us (5.2 TB/s; 87 without best entries), 168 a round at a time;
-// 64 rows in float32, the best twenty: 21 us, 35 before. The vector units bound it then: 58 instructions for eight entries.
+// Bound: HBM, each logit read once. A workgroup takes four rounds of 2048 entries (eight a lane) while the next four are on their
+// way. 2048 rows of 128256 in bfloat16, the best one: 84-110 us by the box and the values (4.8-6.2 TB/s; 84-90 without best
+// entries), 168 a round at a time; 64 rows in float32, the best twenty: 22 us, 35 before. The vector units bound it then: 59
+// instructions for eight entries.
 // The best n entries are kept by each wave: a list of 64 places in LDS to which lanes add what exceeds a bar. The first is
 // the n-th largest of the 64 lanes' maxima over the first four rounds; a list of 2 n or a full one is ranked (each lane
 // counts the keys above its own) and cut to n, whose last is the next bar: n log(entries / n) are added in expectation.

@@ -14,10 +14,11 @@
 // fill each other's gaps; with 64 rows a wave and one workgroup LDS is read half as often, and long prompts ran as fast,
 // all others slower. Tiles on the diagonal, whose hidden positions cost registers that the pipeline needs, come last, without it.
 // Measured (causal half counted): 16384 tokens of 32 / 8 heads of 128 1.91-2.04 ms, 1.08-1.15 PFLOP/s, against 3.33 ms product by
-// product; 2048 tokens of 20 / 5 heads 40 us; 4096 tokens of 16 / 4 heads of 256 150 us. The matrix cores are busy two
+// product; 2048 tokens of 20 / 5 heads 40-44 us; 4096 tokens of 16 / 4 heads of 256 152-183 us (0.75-0.9 PFLOP/s), where LDS and
+// registers leave one wave a SIMD and nothing fills its gaps. The matrix cores are busy two
 // thirds of the time at the clock that this load sustains (1.6 to 2.0 GHz), which is what bounds long prompts now.
-// Tiles with the most positions start first. The key/value heads are dealt round the XCDs, so that with eight of them each
-// XCD's L2 holds one.
+// Within a sequence tiles with the most positions start first; sequences start in the reverse of their order. The key/value
+// heads are dealt round the XCDs, so that with eight of them each XCD's L2 holds one.
 #pragma once
 
 #include <type_traits>
@@ -116,7 +117,8 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void prompt_kernel(PromptAr
     const int n = lane & 31, g = lane >> 5, part = PARTS == 2 ? wave >> 1 : 0, rows_of = PARTS == 2 ? wave & 1 : wave;
     const int D = a.head_dim;
 
-    // Tiles of many positions first; workgroup id runs on XCD id % 8, so that with eight key/value heads each L2 holds one.
+    // A sequence's tiles of many positions first, the last sequence's before the others'; workgroup id runs on XCD id % 8, so that
+    // with eight key/value heads each L2 holds one.
     const int id = a.first_wg + (int)blockIdx.x, head = id % a.kv_heads, slot = a.slots - 1 - id / a.kv_heads;
     const PromptSeq seq = prompt_seq<M>(a, slot);
     const int t0 = seq.first, len = seq.tokens, n_rows = len * a.group, row0 = (slot - seq.slot) * M;

@@ -38,8 +38,10 @@ bpw::Kv4Rows kv4_values(const bpw_paged_kv4 &c) {
 
 // Query rows of all heads, in tiles of 128, from which a wave of the prompt kernel takes all positions of a tile and a workgroup
 // 128 rows; below it two waves share the positions of 32 rows and a workgroup takes 64, which puts more CUs to work on
-// few rows. Heads of 128, 20 query heads: 13.4 us with two against 14.3 at 80 tiles, 17.7 against 17.9 at 120, 24.2 against 22.0 at
-// 160, 36.2 against 30.1 at 240. Heads of 64, of which more workgroups fit a CU: 22.5 against 23.5 at 384, 97 against 90 at 1024.
+// few rows. One prompt, us, two waves to a row against one: 20 heads of 128 13.1 : 14.4 at 80 tiles, 17.4 : 18.0 at 120, 23.5 : 21.7 at
+// 160, 34.4 : 29.1 at 240; 32 heads 19.0 : 18.5 at 192, 33.0 : 33.9 at 384, 175 : 145 at 1024; 16 heads of 256 36.8 : 39.1 at 128, 47.8 :
+// 45.6 at 160, 80.7 : 69.9 at 256; of 192 31.5 : 32.1 at 128, 38.0 : 37.8 at 160. Heads of 64, of which more workgroups fit a CU: 21.7 :
+// 22.8 at 384, 30.3 : 30.5 at 512, 93.9 : 86.8 at 1024.
 int64_t prompt_many_tiles(int32_t padded_dim) { return padded_dim == 64 ? 512 : 160; }
 
 int32_t padded(int32_t head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }

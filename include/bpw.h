@@ -571,8 +571,8 @@ bpw_status bpw_kv_append(const bpw_kv_append_args *a, void *stream);
  *   out = sum_i softmax_i(scale * <q, K_i>) V_i,   lse = log sum_i exp(scale * <q, K_i>)  (natural log).
  * A token that sees nothing gets out = 0 and lse = -inf; a NaN among the scores that it sees makes both NaN.
  * Scores, maxima, sums and outputs are held in float32; the softmax weights are rounded to the cache's type for
- * the matrix cores (float16: to 2^-30 of the largest at the finest), and out is divided by the sum of the rounded
- * weights.
+ * the matrix cores (float16: to 2^-30 of the largest at the finest, so that an infinite value of less weight makes out
+ * NaN), and out is divided by the sum of the rounded weights.
  * Device values out of range read no memory: a page outside [0, n_pages) has its positions hidden, lengths
  * are cut to [0, max_pages * page_size], query tokens past q's n_tokens or past max_q are left out.
  * Cache contents that a token does not see do not reach its results, whatever they are (NaN in an unused
@@ -648,13 +648,14 @@ bpw_status bpw_verify_draft(const bpw_verify_draft_args *a, void *d_ws, size_t w
  * Scores, maxima, sums and outputs are held in float32; the softmax weights are rounded to the inputs' type for the
  * matrix cores (float16: to 2^-30 of the largest at the finest), and out is divided by the sum of the rounded weights. An
  * infinite value makes the outputs that see it infinite, also where its weight is none in float16 (NaN beside one of the
- * other sign). A NaN among the scores that a token sees makes its out and lse NaN; what it does not see does not reach its results,
- * whatever it is (NaN in a later token's value). Starts are cut to [0, n_tokens]; tokens of no sequence (before the first
- * start, behind the last) are not written, and an empty sequence is none. The sums have a fixed order: the same arguments
- * give the same bits. One launch, no workspace.
+ * other sign). A NaN among the scores that a token sees makes its out and lse NaN; what it does not see does not reach its
+ * results, whatever it is (NaN in a later token's value). Starts are cut to [0, n_tokens]; tokens of no sequence (before
+ * the first start, behind the last) are not written, and an empty sequence is none. The sums have a fixed order: the same
+ * arguments give the same bits. One launch, no workspace.
  * q, k, v and out share a type (BPW_BF16 or BPW_F16) and head_dim, a multiple of 8, 8 .. 256; pointers are 16-byte aligned
- * and strides multiples of 8 elements, a token's of k and v at least head_dim (where there are several) and at most 2^24. q.heads is a multiple of k.heads; k.heads equals
- * v.heads. out may not overlap the inputs. n_tokens * q.heads / k.heads is at most 2^30, n_seqs 1 .. 2^20. */
+ * and strides multiples of 8 elements, a token's of k and v at least head_dim (where there are several) and at most 2^24.
+ * q.heads is a multiple of k.heads; k.heads equals v.heads. out may not overlap the inputs. n_tokens * q.heads / k.heads is
+ * at most 2^30, n_seqs 1 .. 2^20. */
 typedef struct bpw_prompt_attn_args {
     int32_t n_tokens, n_seqs, head_dim;
     float scale;                      /* finite and above 0, usually 1 / sqrt(head_dim) */
@@ -751,7 +752,8 @@ bpw_status bpw_kv4_attn(const bpw_kv4_attn_args *a, void *d_ws, size_t ws_len, v
  * row of nothing but -inf gives logprob -inf and entropy 0. A NaN or +inf in a row makes its logprob, entropy and
  * top_logprobs NaN; NaN is never among the top tokens. A token outside [0, vocab) gets -inf (NaN in such a row).
  * Differences to the largest logit (of at most 3.4e38; beyond it they are infinite) and their sums are held in float32, in
- * a fixed order: the same arguments give the same bits. One launch where there are many rows, two where rows are split over the GPU. */
+ * a fixed order: the same arguments give the same bits. One launch where there are many rows, two where rows are split over
+ * the GPU. */
 typedef struct bpw_token_logprobs_args {
     int32_t n_tokens;                 /* >= 0 */
     int32_t vocab;                    /* 1 .. 2^24 */
