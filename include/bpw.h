@@ -648,10 +648,10 @@ bpw_status bpw_verify_draft(const bpw_verify_draft_args *a, void *d_ws, size_t w
  * Scores, maxima, sums and outputs are held in float32; the softmax weights are rounded to the inputs' type for the
  * matrix cores (float16: to 2^-30 of the largest at the finest), and out is divided by the sum of the rounded weights. An
  * infinite value makes the outputs that see it infinite, also where its weight is none in float16 (NaN beside one of the
- * other sign). A NaN among the scores that a token sees makes its out and lse NaN; what it does not see does not reach its
- * results, whatever it is (NaN in a later token's value). Starts are cut to [0, n_tokens]; tokens of no sequence (before
- * the first start, behind the last) are not written, and an empty sequence is none. The sums have a fixed order: the same
- * arguments give the same bits. One launch, no workspace.
+ * other sign). A NaN among the scores that a token sees makes its out and lse NaN; scores that are all -inf give lse -inf
+ * and out NaN. What a token does not see does not reach its results, whatever it is (NaN in a later token's value). Starts
+ * are cut to [0, n_tokens]; tokens of no sequence (before the first start, behind the last) are not written, and an empty
+ * sequence is none. The sums have a fixed order: the same arguments give the same bits. One launch, no workspace.
  * q, k, v and out share a type (BPW_BF16 or BPW_F16) and head_dim, a multiple of 8, 8 .. 256; pointers are 16-byte aligned
  * and strides multiples of 8 elements, a token's of k and v at least head_dim (where there are several) and at most 2^24.
  * q.heads is a multiple of k.heads; k.heads equals v.heads. out may not overlap the inputs. n_tokens * q.heads / k.heads is

@@ -218,6 +218,26 @@ def test_prompt_infinite_values_of_small_weight(dev, Hq, Hk, D, counts, dt):
     assert torch.isnan(p.out[n // 2 + 1:n, -1, 2]).all() and torch.isinf(p.out[n // 2:n, -1, 3]).all()
 
 
+@pytest.mark.parametrize("counts,Hq,Hk,D,dt", [([120, 90], 4, 2, 64, BF16), ([700, 333], 16, 4, 128, F16), ([400], 12, 4, 256, BF16)])
+def test_prompt_scores_of_minus_infinity(dev, counts, Hq, Hk, D, dt):
+    """Tokens that see nothing but scores of -inf have lse -inf and out NaN (0 / 0); for later ones those positions have no weight."""
+    p = Prompt(dev, counts, Hq, Hk, D, dt, seed=83)
+    n = 70
+    p.q.abs_()
+    kept = p.k[:n].clone()
+    p.k[:n, :, 0] = -math.inf
+    p.run()
+    assert torch.isnan(p.out[:n]).all() and (p.lse[:n] == -math.inf).all()
+    q, k, v = f64(p.q[n:counts[0]]), f64(p.k[n:counts[0]]), f64(p.v[n:counts[0]])
+    out, lse, mag = request_ops.prompt(q, k, v, [0, counts[0] - n], D ** -0.5)
+    tol, tol_lse = attn_tol(out, mag, q, k, v, D, counts[0], D ** -0.5, dt)
+    within(p.out[n:counts[0]], out, tol, "out")
+    within(p.lse[n:counts[0]], lse, tol_lse + 4 * U * np.abs(lse), "lse")
+    p.k[:n] = kept
+    p.run()
+    p.check("finite again")
+
+
 def test_prompt_float16_weights_far_below_the_largest(dev):
     """One position of 32 has all but 2^-25 of the weight and values of zero: the output is what the others add. A step of
     float16's subnormals is 2^-30 of the largest weight, half of one the error."""
